@@ -1,0 +1,311 @@
+// Selective scan with a decay of its own for every channel d and state n:
+//
+//     dt_t = softplus(delta_t + bias)   (or delta_t + bias)
+//     h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t u_t B_t[n]
+//     y_t = sum_n C_t[n] h_t[n] + D u_t;   out_t = y_t z_t sigmoid(z_t)   (or y_t)
+//
+// The decays differ for every (channel, state), so the products do not factor into matrix
+// products as they do with one decay per head: the work is N exponentials, 2 N
+// multiplications and 2 N fused multiply-adds per (token, channel) on the vector units,
+// against 4 activations moved.  At N = 16 that is about 26 cycles per state of a wave, and
+// the vector units, not memory, bound the scan.
+//
+// Chunks.  A tile of 64 channels is one wave, and few channels at batch 1 leave the GPU
+// empty, so the sequence is cut into chunks: (1) every chunk's end state from a zero state,
+// and the sum of its dt; (2) the states passed from chunk to chunk,
+// h <- exp(A sum dt) h + S; (3) every chunk again from the state that enters it.  (1) and (2)
+// are skipped where there are waves enough without.
+#include "ssd_sel.h"
+
+namespace ssd {
+
+constexpr int kSelWaves = 4;     // independent waves per workgroup
+
+// Wave -> (batch row, chunk, tile); tiles are neighbours, so the waves of a workgroup share
+// B and C.  False past the last unit.
+__device__ __forceinline__ bool sel_unit(const SelArgs &a, int nchunks, int64_t *b, int *c, int *tt) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int ntt = a.G * a.tiles;
+    const int64_t u = (int64_t)blockIdx.x * kSelWaves + wave;
+    if (u >= a.batch * nchunks * ntt) return false;
+    *tt = (int)(u % ntt);
+    *c = (int)(u / ntt % nchunks);
+    *b = u / ntt / nchunks;
+    return true;
+}
+
+// (1), and its mirror for the backward (REV): the carry a_t g_t that leaves the chunk's first
+// token when none enters at its end, g_t = C_t r_t + a_{t+1} g_{t+1}.
+template <typename T, int N, bool REV>
+__global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
+    int64_t b;
+    int c, tt;
+    if (!sel_unit(a, a.nc - 1, &b, &c, &tt)) return;
+    if (REV) ++c;
+    const SelTile q = sel_tile(a, tt);
+    const int len = row_length(a.lengths, b, a.L);
+    const int begin = c * a.T, end = min(begin + a.T, len);
+    const bool softplus = (a.flags & SSD_FLAG_SOFTPLUS) != 0;
+    const float bias = a.bias ? a.bias[q.d] : 0.f;
+    float A2[N], h[N], sum = 0.f;
+    sel_rates<N>(a, q.d, 0, A2);
+#pragma unroll
+    for (int n = 0; n < N; ++n) h[n] = 0.f;
+    const View &coef = REV ? a.C : a.B;
+    const View &val = REV ? a.dy : a.u;
+    const bool gate = REV && a.z.p;
+    for (int t0 = begin; t0 < end; t0 += kKeep) {
+        const int m = min(kKeep, end - t0);
+        T dv[kKeep], xv[kKeep], zv[kKeep];
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int k = min(i, m - 1);
+            const int t = REV ? end - 1 - (t0 - begin) - k : t0 + k;
+            dv[i] = row_of<T>(a.delta, b, t)[q.d];
+            xv[i] = row_of<T>(val, b, t)[q.d];
+            if (gate) zv[i] = row_of<T>(a.z, b, t)[q.d];
+        }
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            if (i < m) {
+                const int t = REV ? end - 1 - (t0 - begin) - i : t0 + i;
+                Uniform<T, N> cf;
+                cf.load(row_of<T>(coef, b, t) + q.g * N);
+                float sig;
+                const float dt = sel_dt(to_f32(dv[i]) + bias, softplus, &sig);
+                sum += dt;
+                float x = to_f32(xv[i]);
+                if (!REV) x *= dt;
+                else if (gate) x *= silu_f32(to_f32(zv[i]));
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const float e = exp2_fast(dt * A2[n]);
+                    h[n] = REV ? e * fmaf(x, cf[n], h[n]) : fmaf(e, h[n], x * cf[n]);
+                }
+            }
+        }
+    }
+    float *S = a.S + sel_slot(a, b, c, tt, N);
+#pragma unroll
+    for (int n = 0; n < N; ++n) S[n * 64] = h[n];
+    a.sumdt[sel_slot(a, b, c, tt, 1)] = sum;
+}
+
+// (2): one thread per (batch row, tile, state, channel) walks the chunks; each chunk's slot
+// of S receives the state (REV: the carry) that enters it.
+template <bool REV>
+__global__ __launch_bounds__(256) void sel_pass_kernel(SelArgs a) {
+    const int ntt = a.G * a.tiles;
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (k >= a.batch * ntt * a.N * 64) return;
+    const int lane = (int)(k % 64), n = (int)(k / 64 % a.N), tt = (int)(k / 64 / a.N % ntt);
+    const int64_t b = k / 64 / a.N / ntt;
+    const SelTile q = sel_tile(a, tt);
+    const float A2 = a.A[(int64_t)q.d * a.N + n] * kLog2eF;
+    const float *first = REV ? a.dfinal : a.init;
+    float h = first ? first[(b * a.D + q.d) * (int64_t)a.N + n] : 0.f;
+    const int64_t cs = (int64_t)ntt * a.N * 64, ds = (int64_t)ntt * 64;
+    float *S = a.S + ((b * a.nc * ntt + tt) * (int64_t)a.N + n) * 64 + lane;
+    const float *sd = a.sumdt + (b * a.nc * ntt + tt) * (int64_t)64 + lane;
+    constexpr int U = 8;                      // chunks whose values are in flight together
+    for (int c0 = 0; c0 < a.nc; c0 += U) {
+        float s[U], d[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = min(c0 + i, a.nc - 2);       // the last chunk in order has no slot to read
+            const int at = REV ? a.nc - 1 - c : c;
+            s[i] = S[at * cs];
+            d[i] = sd[at * ds];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = c0 + i;
+            if (c < a.nc) {
+                S[(REV ? a.nc - 1 - c : c) * cs] = h;
+                h = fmaf(exp2_fast(A2 * d[i]), h, s[i]);
+            }
+        }
+    }
+}
+
+// (3)
+template <typename T, int N>
+__global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
+    int64_t b;
+    int c, tt;
+    if (!sel_unit(a, a.nc, &b, &c, &tt)) return;
+    const SelTile q = sel_tile(a, tt);
+    const int len = row_length(a.lengths, b, a.L);
+    const int begin = c * a.T, stop = min(begin + a.T, a.L), end = min(stop, len);
+    const bool softplus = (a.flags & SSD_FLAG_SOFTPLUS) != 0;
+    const float bias = a.bias ? a.bias[q.d] : 0.f, skip = a.Dskip ? a.Dskip[q.d] : 0.f;
+    float A2[N], h[N];
+    sel_rates<N>(a, q.d, 0, A2);
+    const float *S = a.S + sel_slot(a, b, c, tt, N);
+    const float *h0 = a.init ? a.init + (b * a.D + q.d) * (int64_t)N : nullptr;
+#pragma unroll
+    for (int n = 0; n < N; ++n) h[n] = a.nc > 1 ? S[n * 64] : (h0 ? h0[n] : 0.f);
+    T *y = reinterpret_cast<T *>(a.y) + b * a.L * (int64_t)a.D + q.d;
+    T dv[kKeep], uv[kKeep], zv[kKeep];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int t = min(t0 + i, end - 1);
+            dv[i] = row_of<T>(a.delta, b, t)[q.d];
+            uv[i] = row_of<T>(a.u, b, t)[q.d];
+            if (a.z.p) zv[i] = row_of<T>(a.z, b, t)[q.d];
+        }
+    };
+    for (int t0 = begin; t0 < end; t0 += kKeep) {
+        fetch(t0);
+        if (a.keep) {
+            float *kp = a.keep + sel_keep_slot(a, b, t0 / kKeep, tt, 0);
+#pragma unroll
+            for (int n = 0; n < N; ++n) kp[n * 64] = h[n];
+        }
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            if (t0 + i < end) {
+                Uniform<T, N> Bt, Ct;
+                Bt.load(row_of<T>(a.B, b, t0 + i) + q.g * N);
+                Ct.load(row_of<T>(a.C, b, t0 + i) + q.g * N);
+                float sig;
+                const float dt = sel_dt(to_f32(dv[i]) + bias, softplus, &sig);
+                const float u = to_f32(uv[i]), x = dt * u;
+                float acc[2] = {skip * u, 0.f};
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    h[n] = fmaf(exp2_fast(dt * A2[n]), h[n], x * Bt[n]);
+                    acc[n & 1] = fmaf(Ct[n], h[n], acc[n & 1]);
+                }
+                float o = acc[0] + acc[1];
+                if (a.z.p) o *= silu_f32(to_f32(zv[i]));
+                if (q.live) y[(t0 + i) * (int64_t)a.D] = from_f32<T>(o);
+            }
+        }
+    }
+    if (q.live) {
+        for (int t = max(begin, end); t < stop; ++t) y[t * (int64_t)a.D] = from_f32<T>(0.f);
+        if (a.final_state && c == a.nc - 1) {
+            float *f = a.final_state + (b * a.D + q.d) * (int64_t)N;
+#pragma unroll
+            for (int n = 0; n < N; ++n) f[n] = h[n];
+        }
+    }
+}
+
+// One token.  The state, 8 bytes read and written per element, is the traffic: N/4 threads
+// share a channel, each with 4 states (one 16-byte access each way), and add their parts of
+// the sum over n with wave shuffles.
+template <typename T, int N>
+__global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
+    constexpr int Q = N / 4;
+    const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) / Q;
+    const int n0 = threadIdx.x % Q * 4;
+    if (k >= a.batch * a.D) return;                     // whole channels leave together
+    const int64_t b = k / a.D;
+    const int d = (int)(k % a.D), g = d / (a.D / a.G);
+    const bool softplus = (a.flags & SSD_FLAG_SOFTPLUS) != 0;
+    const T *Bp = reinterpret_cast<const T *>(a.B) + b * a.B_bs + g * N + n0;
+    const T *Cp = reinterpret_cast<const T *>(a.C) + b * a.C_bs + g * N + n0;
+    const float *A = a.A + (int64_t)d * N + n0;
+    const f32x4 s = *reinterpret_cast<const f32x4 *>(a.state_in + k * N + n0);
+    const float u = to_f32(reinterpret_cast<const T *>(a.u)[b * a.u_bs + d]);
+    float sig;
+    const float dt = sel_dt(to_f32(reinterpret_cast<const T *>(a.delta)[b * a.delta_bs + d]) +
+                            (a.bias ? a.bias[d] : 0.f), softplus, &sig);
+    const float x = dt * u;
+    f32x4 h;
+    float part = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = fmaf(exp2_fast(dt * (A[i] * kLog2eF)), s[i], x * to_f32(Bp[i]));
+        part = fmaf(to_f32(Cp[i]), h[i], part);
+    }
+    *reinterpret_cast<f32x4 *>(a.state_out + k * N + n0) = h;
+#pragma unroll
+    for (int o = Q / 2; o >= 1; o >>= 1) part += __shfl_xor(part, o, 64);
+    if (n0 == 0) {
+        float o = fmaf(a.Dskip ? a.Dskip[d] : 0.f, u, part);
+        if (a.z) o *= silu_f32(to_f32(reinterpret_cast<const T *>(a.z)[b * a.z_bs + d]));
+        reinterpret_cast<T *>(a.y)[k] = from_f32<T>(o);
+    }
+}
+
+bool sel_supported(int64_t N) { return N == 16 || N == 32 || N == 64; }
+
+// Chunks so that about `target` waves run, of at least 16 tokens; one chunk where the waves of
+// a single pass already come to one for each of the 1024 SIMDs.
+void sel_chunks(int64_t waves, int64_t target, int64_t L, int *nc, int *T) {
+    const int64_t n = waves >= 1024 ? 1 : (target + waves - 1) / waves;
+    int64_t t = (L + n - 1) / n;
+    t = (t + kKeep - 1) / kKeep * kKeep;
+    if (t < 16) t = 16;
+    *nc = (int)((L + t - 1) / t);
+    *T = (int)t;
+}
+
+static hipError_t sel_grid(int64_t units, uint32_t *blocks) {
+    const int64_t n = (units + kSelWaves - 1) / kSelWaves;
+    if (n < 1 || n > INT32_MAX) return hipErrorInvalidValue;
+    *blocks = (uint32_t)n;
+    return hipSuccess;
+}
+
+hipError_t launch_sel_pass(const SelArgs &a, bool reverse, hipStream_t s) {
+    const int64_t n = (a.batch * a.G * a.tiles * a.N * 64 + 255) / 256;
+    if (n > INT32_MAX) return hipErrorInvalidValue;
+    if (reverse) sel_pass_kernel<true><<<(uint32_t)n, 256, 0, s>>>(a);
+    else sel_pass_kernel<false><<<(uint32_t)n, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+static hipError_t sel_fwd_t(const SelArgs &a, hipStream_t s) {
+    const int64_t per = a.batch * a.G * a.tiles;
+    uint32_t blocks;
+    hipError_t e;
+    if (a.nc > 1) {
+        if ((e = sel_grid(per * (a.nc - 1), &blocks)) != hipSuccess) return e;
+        sel_local_kernel<T, N, false><<<blocks, 256, 0, s>>>(a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if ((e = launch_sel_pass(a, false, s)) != hipSuccess) return e;
+    }
+    if ((e = sel_grid(per * a.nc, &blocks)) != hipSuccess) return e;
+    sel_scan_kernel<T, N><<<blocks, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+static hipError_t sel_step_t(const SelStepArgs &a, hipStream_t s) {
+    const int64_t n = (a.batch * a.D * (N / 4) + 255) / 256;
+    if (n > INT32_MAX) return hipErrorInvalidValue;
+    sel_step_kernel<T, N><<<(uint32_t)n, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+static hipError_t sel_rev_t(const SelArgs &a, hipStream_t s) {
+    uint32_t blocks;
+    hipError_t e = sel_grid(a.batch * a.G * a.tiles * (a.nc - 1), &blocks);
+    if (e != hipSuccess) return e;
+    sel_local_kernel<T, N, true><<<blocks, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+#define SEL_PICK(FN, T)                          \
+    switch (a.N) {                               \
+        case 16: return FN<T, 16>(a, s);         \
+        case 32: return FN<T, 32>(a, s);         \
+        case 64: return FN<T, 64>(a, s);         \
+        default: return hipErrorInvalidValue;    \
+    }
+#define SEL_DISPATCH(FN)                         \
+    if (a.dtype == 1) { SEL_PICK(FN, bf16) }     \
+    SEL_PICK(FN, float)
+
+hipError_t launch_sel_fwd(const SelArgs &a, hipStream_t s) { SEL_DISPATCH(sel_fwd_t) }
+hipError_t launch_sel_step(const SelStepArgs &a, hipStream_t s) { SEL_DISPATCH(sel_step_t) }
+hipError_t launch_sel_local_reverse(const SelArgs &a, hipStream_t s) { SEL_DISPATCH(sel_rev_t) }
+
+}  // namespace ssd

@@ -8,51 +8,23 @@
 // with a per-layer state store).
 #include "libssdscan.h"
 
-#include <stdarg.h>
-#include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
 
 #include <mutex>
-#include <string>
 
+#include "ssd_check.h"
 #include "ssd_common.h"
+
+using namespace ssd_check;
 
 namespace {
 
-thread_local std::string g_err;
-
-ssd_status_t fail(ssd_status_t st, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_err = buf;
-    return st;
-}
-
-ssd_status_t ok() {
-    g_err.clear();
-    return SSD_OK;
-}
-
-constexpr size_t kAlign = 256;
 constexpr int kStages = 4;   // chunk_cumsum, chunk_state, state_pass, chunk_scan
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
     size_t dA, bintra, bin, ctot, dblk, wend, total;
 };
-
-int64_t act_bytes(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t lim, int64_t *out) {
-    if (a < 0 || b < 0) return false;
-    if (a != 0 && b > lim / a) return false;
-    *out = a * b;
-    return true;
-}
 
 // Workspace of one layer call over `L` tokens.
 bool layout_for(const ssd_dims_t &d, int64_t L, int32_t Q, Layout *lo) {
@@ -114,8 +86,6 @@ ssd_status_t check_dims(const ssd_dims_t *d, int32_t Q) {
     return SSD_OK;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
 // Tensors read or written with 16-byte vector accesses must be 16-byte aligned; A and D
 // (scalar float loads) need 4 bytes, dt its element size.
 ssd_status_t check_alignment(const void *x, const void *dt, const void *A, const void *B, const void *C,
@@ -128,11 +98,6 @@ ssd_status_t check_alignment(const void *x, const void *dt, const void *A, const
     if (((uintptr_t)dt & (dtal - 1)) || ((uintptr_t)A & 3u) || (D && ((uintptr_t)D & 3u)))
         return fail(SSD_ERR_MISALIGNED, "dt, A or D is not aligned to its element size");
     return SSD_OK;
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
 }
 
 // Work partition: heads per workgroup so that there are at least `target` workgroups
@@ -594,7 +559,7 @@ const char *ssd_status_string(ssd_status_t status) {
     return "SSD_ERR_UNKNOWN";
 }
 
-const char *ssd_last_error_message(void) { return g_err.c_str(); }
+const char *ssd_last_error_message(void) { return g_err; }
 
 int32_t ssd_version(void) { return 100; }
 

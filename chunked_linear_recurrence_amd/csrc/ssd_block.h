@@ -1,0 +1,190 @@
+// Arguments and launch functions of the operators around a scan: the short causal
+// convolution, the selective scan with a decay per channel and state, and layer norm.
+#pragma once
+
+#include "libssdscan.h"
+#include "ssd_common.h"
+
+namespace ssd {
+
+// A tensor [batch, seqlen, channels] whose channels are contiguous: token t of batch row b
+// starts at p + b * bs + t * ts (elements).
+struct View {
+    const void *p;
+    int64_t bs, ts;
+};
+
+template <typename T>
+__device__ __forceinline__ const T *row_of(const View &v, int64_t b, int64_t t) {
+    return reinterpret_cast<const T *>(v.p) + b * v.bs + t * v.ts;
+}
+
+struct ConvArgs {
+    int64_t batch;
+    int L, C, W, dtype;
+    uint32_t flags;
+    View x;
+    const float *w, *bias;        // [C, W]; [C] or null
+    const void *init;             // [batch, W-1, C] or null
+    const int32_t *lengths;       // [batch] or null
+    void *y, *final_state;        // forward: [batch, L, C]; [batch, W-1, C] or null
+    // backward
+    View dy;
+    const void *dfinal;           // [batch, W-1, C] or null
+    void *dx, *dinit;             // [batch, L, C]; [batch, W-1, C] or null
+    float *dw, *dbias;            // [C, W]; [C] or null
+    float *part;                  // workspace: [conv_bwd_rows, W+1, C] partial sums
+};
+
+hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t s);
+hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
+hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t s);
+int64_t conv_bwd_rows(int64_t batch, int64_t L);
+bool conv_supported(int W);
+
+struct NormArgs {
+    int64_t rows;
+    int D, dtype;
+    const void *x;
+    int64_t x_stride;             // elements between rows of x
+    const float *w, *bias;        // [D] or null
+    float eps;
+    void *y;                      // [rows, D]
+    float *mean, *rstd;           // [rows]; forward: written when not null
+    // backward
+    const void *dy;
+    int64_t dy_stride;
+    void *dx;                     // [rows, D]
+    float *dw, *db;               // [D] or null
+    float *part;                  // workspace: [norm_bwd_blocks, 2, D]
+};
+
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
+int64_t norm_bwd_blocks(int64_t rows, int64_t D);
+
+// Tokens between two kept states of the selective scan.
+constexpr int kKeep = 8;
+
+struct SelArgs {
+    int64_t batch;
+    int L, D, N, G, dtype;
+    uint32_t flags;
+    View u, delta, z, B, C;       // z.p may be null; B and C rows hold [G, N]
+    const float *A;               // [D, N]
+    const float *Dskip, *bias;    // [D] or null
+    const float *init;            // [batch, D, N] or null
+    const int32_t *lengths;       // [batch] or null
+    void *y;                      // [batch, L, D]
+    float *final_state;           // [batch, D, N] or null
+    float *keep;                  // kept states or null (see sel_keep_floats)
+    int tiles;                    // tiles of 64 channels per group
+    int nc, T;                    // chunks and tokens per chunk (T a multiple of kKeep)
+    float *S;                     // workspace [batch, nc, G*tiles, N, 64]
+    float *sumdt;                 // workspace [batch, nc, G*tiles, 64]
+    // backward
+    View dy;
+    const float *dfinal;
+    void *du, *ddelta, *dz, *dB, *dC;
+    float *dA, *dD, *dbias, *dinit;
+    float *part_bc;               // [sel_bwd_parts, batch, L, G, 2, N]: dB, dC partial sums
+    float *part_par;              // [batch, nc, G*tiles, N + 2, 64]: dA, dD, dbias partial sums
+};
+
+inline int sel_tiles(int64_t D, int64_t G) { return (int)((D / G + 63) / 64); }
+
+bool sel_supported(int64_t N);
+// Tiles of 64 channels that one workgroup of the backward takes (its 4 waves are tiles times
+// blocks of 16 states), and workgroups per group of channels.
+inline int sel_bwd_tiles(int64_t N) { return (int)(64 / N); }
+inline int sel_bwd_parts(int64_t D, int64_t G, int64_t N) {
+    return (sel_tiles(D, G) + sel_bwd_tiles(N) - 1) / sel_bwd_tiles(N);
+}
+// Chunks of the sequence: *nc chunks of *T tokens, for `waves` waves per chunk and about
+// `target` waves in all.
+void sel_chunks(int64_t waves, int64_t target, int64_t L, int *nc, int *T);
+hipError_t launch_sel_fwd(const SelArgs &a, hipStream_t s);
+hipError_t launch_sel_bwd(const SelArgs &a, hipStream_t s);
+hipError_t launch_sel_pass(const SelArgs &a, bool reverse, hipStream_t s);
+hipError_t launch_sel_local_reverse(const SelArgs &a, hipStream_t s);
+
+struct SelStepArgs {
+    int64_t batch;
+    int D, N, G, dtype;
+    uint32_t flags;
+    const void *u, *delta, *z, *B, *C;
+    int64_t u_bs, delta_bs, z_bs, B_bs, C_bs;
+    const float *A, *Dskip, *bias, *state_in;
+    float *state_out;
+    void *y;
+};
+hipError_t launch_sel_step(const SelStepArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------------
+constexpr float kLog2eF = 1.44269504088896340736f;
+constexpr float kLn2F = 0.69314718055994530942f;
+
+// V consecutive elements as one access (V * sizeof(T) bytes, naturally aligned).
+template <typename T, int V>
+struct Pack {
+    typedef __attribute__((ext_vector_type(V))) T type;
+};
+template <typename T>
+struct Pack<T, 1> {
+    typedef T type;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void load_f32(const T *p, float (&v)[V]) {
+    const auto q = *reinterpret_cast<const typename Pack<T, V>::type *>(p);
+    if constexpr (V == 1) v[0] = to_f32(q);
+    else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = (float)q[i];
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_f32(T *p, const float (&v)[V]) {
+    typename Pack<T, V>::type q;
+    if constexpr (V == 1) q = from_f32<T>(v[0]);
+    else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = from_f32<T>(v[i]);
+    }
+    *reinterpret_cast<typename Pack<T, V>::type *>(p) = q;
+}
+
+__device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }   // ~1 ulp
+
+// 1 / (1 + e^-v): e^-v overflows to infinity for v below -88 and the quotient is then 0.
+__device__ __forceinline__ float sigmoid_f32(float v) { return rcp_fast(1.f + exp2_fast(-v * kLog2eF)); }
+
+__device__ __forceinline__ float silu_f32(float v) { return v * sigmoid_f32(v); }
+
+// d/dv (v sigmoid(v))
+__device__ __forceinline__ float dsilu_f32(float v) {
+    const float s = sigmoid_f32(v);
+    return s * fmaf(v, 1.f - s, 1.f);
+}
+
+// log(1 + e^v) and, in *sig, its derivative.  With w = fl(1 + e^v) the logarithm of w misses
+// what the addition rounded off; (e^v - (w - 1)) / w puts it back, so small results keep
+// their relative accuracy.  Above 20 the result is v to float32.
+__device__ __forceinline__ float softplus_f32(float v, float *sig) {
+    const float e = exp2_fast(fminf(v, 30.f) * kLog2eF);
+    const float w = 1.f + e;
+    const float r = rcp_fast(w);
+    *sig = e * r;
+    const float l = fmaf(__builtin_amdgcn_logf(w), kLn2F, (e - (w - 1.f)) * r);
+    return v > 20.f ? v : l;
+}
+
+__device__ __forceinline__ int row_length(const int32_t *lengths, int64_t b, int L) {
+    if (!lengths) return L;
+    return max(0, min(lengths[b], L));
+}
+
+}  // namespace ssd

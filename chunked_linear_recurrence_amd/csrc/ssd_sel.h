@@ -1,0 +1,78 @@
+// Device code shared by the selective scan's forward and backward kernels.
+//
+// A tile is 64 channels of one group, one lane each; a lane keeps its channel's N states in
+// registers.  B_t and C_t are the same for all lanes, so they are read through the scalar
+// cache into scalar registers, which the vector units take as operands directly.
+#pragma once
+
+#include "ssd_block.h"
+
+namespace ssd {
+
+// N consecutive activations at a wave-uniform address (4-byte aligned), in scalar registers.
+template <typename T, int N>
+struct Uniform;
+typedef const __attribute__((address_space(4))) uint32_t *scalar_ptr;
+
+template <int N>
+struct Uniform<float, N> {
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const float *p) {
+        scalar_ptr s = (scalar_ptr)(uintptr_t)p;
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = s[i];
+    }
+    __device__ __forceinline__ float operator[](int i) const { return __builtin_bit_cast(float, w[i]); }
+};
+template <int N>
+struct Uniform<bf16, N> {
+    uint32_t w[N / 2];
+    __device__ __forceinline__ void load(const bf16 *p) {
+        scalar_ptr s = (scalar_ptr)(uintptr_t)p;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = s[i];
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        return __builtin_bit_cast(float, (i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    }
+};
+
+// A wave's tile: group, the lane's channel and its place in the [D] tensors.
+struct SelTile {
+    int tt, g, d;
+    bool live;
+};
+__device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int tt) {
+    SelTile q;
+    const int per = a.D / a.G;
+    q.tt = tt;
+    q.g = tt / a.tiles;
+    const int c = (tt % a.tiles) * 64 + (int)(threadIdx.x % 64);
+    q.live = c < per;
+    q.d = q.g * per + min(c, per - 1);       // idle lanes read a channel that exists
+    return q;
+}
+
+template <int N>
+__device__ __forceinline__ void sel_rates(const SelArgs &a, int d, int n0, float (&A2)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) A2[n] = a.A[(int64_t)d * a.N + n0 + n] * kLog2eF;
+}
+
+// The step size of one token and its derivative by delta.
+__device__ __forceinline__ float sel_dt(float raw, bool softplus, float *sig) {
+    if (softplus) return softplus_f32(raw, sig);
+    *sig = 1.f;
+    return raw;
+}
+
+// Offset of chunk c of batch row b in S (floats), lane included; state n is at n * 64.
+__device__ __forceinline__ int64_t sel_slot(const SelArgs &a, int64_t b, int c, int tt, int width) {
+    return (((b * a.nc + c) * (a.G * a.tiles) + tt) * (int64_t)width) * 64 + threadIdx.x % 64;
+}
+__device__ __forceinline__ int64_t sel_keep_slot(const SelArgs &a, int64_t b, int sub, int tt, int n0) {
+    const int64_t nsub = (a.L + kKeep - 1) / kKeep;
+    return (((b * nsub + sub) * (a.G * a.tiles) + tt) * (int64_t)a.N + n0) * 64 + threadIdx.x % 64;
+}
+
+}  // namespace ssd

@@ -6,6 +6,7 @@ built library is missing the first call raises; there is no fallback path.
 """
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -16,6 +17,8 @@ SSD_F32, SSD_BF16 = 0, 1
 SSD_FLAG_RESIDUAL = 1
 SSD_FLAG_WAVEFRONT = 2
 SSD_FLAG_SCAN_FORM = 4
+SSD_FLAG_SILU = 8
+SSD_FLAG_SOFTPLUS = 16
 
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL_ARG", 2: "SSD_ERR_BAD_SHAPE", 3: "SSD_ERR_BAD_DTYPE",
           4: "SSD_ERR_UNSUPPORTED", 5: "SSD_ERR_MISALIGNED", 6: "SSD_ERR_WORKSPACE",
@@ -25,7 +28,11 @@ STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL_ARG", 2: "SSD_ERR_BAD_SHAPE", 3: "SSD_ER
 EXPORTS = ["ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_fwd", "ssd_segmented_workspace_bytes",
            "ssd_chunk_scan_segmented", "ssd_chunk_scan_stages", "ssd_workspace_layout",
            "ssd_shape_supported", "ssd_status_string", "ssd_last_error_message", "ssd_version", "ssd_step",
-           "ssd_scan_form_supported", "ssd_chunk_scan_fwd_noalloc"]
+           "ssd_scan_form_supported", "ssd_chunk_scan_fwd_noalloc",
+           "ssd_conv_fwd", "ssd_conv_step", "ssd_conv_bwd", "ssd_conv_bwd_workspace_bytes",
+           "ssd_selective_fwd", "ssd_selective_step", "ssd_selective_bwd", "ssd_selective_kept_bytes",
+           "ssd_selective_fwd_workspace_bytes", "ssd_selective_bwd_workspace_bytes",
+           "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_bytes"]
 
 # Workspace limit of ssd_chunk_scan_fwd_noalloc (SSD_NOALLOC_SCRATCH_BYTES in the header).
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -35,6 +42,25 @@ class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ConvDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("x_batch_stride", ctypes.c_int64), ("x_token_stride", ctypes.c_int64),
+                ("dy_batch_stride", ctypes.c_int64), ("dy_token_stride", ctypes.c_int64)]
+
+
+class SelectiveDims(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("batch", "seqlen", "channels", "dstate", "ngroups")] +
+                [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)] +
+                [(n + s, ctypes.c_int64) for n in ("u", "delta", "z", "B", "C", "dy")
+                 for s in ("_batch_stride", "_token_stride")])
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_row_stride", ctypes.c_int64), ("dy_row_stride", ctypes.c_int64)]
 
 
 class SSDError(RuntimeError):
@@ -76,6 +102,23 @@ def lib():
         L.ssd_scan_form_supported.restype = i32
         L.ssd_shape_supported.argtypes = [i32, i32, i64, i64]
         L.ssd_shape_supported.restype = i32
+        cp, sp, np_ = ctypes.POINTER(ConvDims), ctypes.POINTER(SelectiveDims), ctypes.POINTER(NormDims)
+        f32 = ctypes.c_float
+        for name, args in (("ssd_conv_fwd", [cp] + [vp] * 7 + [u32, vp]),
+                           ("ssd_conv_step", [cp] + [vp] * 6 + [u32, vp]),
+                           ("ssd_conv_bwd", [cp] + [vp] * 11 + [u32, vp, sz, vp]),
+                           ("ssd_selective_fwd", [sp] + [vp] * 13 + [u32, vp, sz, vp]),
+                           ("ssd_selective_step", [sp] + [vp] * 11 + [u32, vp]),
+                           ("ssd_selective_bwd", [sp] + [vp] * 21 + [u32, vp, sz, vp]),
+                           ("ssd_norm_fwd", [np_, vp, vp, vp, f32, vp, vp, vp, vp]),
+                           ("ssd_norm_bwd", [np_] + [vp] * 9 + [sz, vp])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
+        for name, arg in (("ssd_conv_bwd_workspace_bytes", cp), ("ssd_selective_kept_bytes", sp),
+                          ("ssd_selective_fwd_workspace_bytes", sp), ("ssd_selective_bwd_workspace_bytes", sp),
+                          ("ssd_norm_bwd_workspace_bytes", np_)):
+            getattr(L, name).argtypes = [arg]
+            getattr(L, name).restype = sz
         L.ssd_status_string.argtypes = [ctypes.c_int]
         L.ssd_status_string.restype = ctypes.c_char_p
         L.ssd_last_error_message.argtypes = []
@@ -354,3 +397,347 @@ def tile_order_to_pn(t, P, N):
     nd = len(lead)
     perm = list(range(nd)) + [nd + 1, nd + 3, nd + 0, nd + 2, nd + 4]   # pt, col, nt, g, r
     return v.permute(*perm).reshape(*lead, P, N)
+
+
+# ---------------------------------------------------------------- operators around a scan
+# These take views (rows of contiguous channels at any batch and token stride) for their
+# activation inputs, and run on the tensors' own device.  With `stream`, outputs and
+# workspaces are allocated for that stream, so that the allocator reuses their memory in its
+# order.
+
+_DTYPE_CODE = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+
+
+def _param(name, t, shape, device, dtype=torch.float32):
+    """A contiguous tensor of this shape and dtype on `device`, or None; its pointer."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), shape))
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s; expected %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, like):
+    """An activation view: `like`'s dtype and device, contiguous channels.  Its pointer, batch
+    stride and token stride (0 where the shape has no tokens)."""
+    if t.shape != shape:
+        raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), shape))
+    if t.dtype != like.dtype:
+        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, like.dtype))
+    if t.device != like.device:
+        raise ValueError("%s is on %s; expected %s" % (name, t.device, like.device))
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError("%s must have contiguous channels" % name)
+    return t.data_ptr(), st[0], (st[1] if len(shape) == 3 else 0)
+
+
+def _coef_rows(name, t, lead, like):
+    """B or C [*lead, G, N]: as _rows, with [G, N] contiguous together."""
+    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
+        raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), tuple(lead) + ("*", "*")))
+    if t.dtype != like.dtype:
+        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, like.dtype))
+    if t.device != like.device:
+        raise ValueError("%s is on %s; expected %s" % (name, t.device, like.device))
+    st = t.stride()
+    if st[-1] != 1 or (st[-2] != t.shape[-1] and t.shape[-2] != 1):
+        raise ValueError("%s must have contiguous groups of states" % name)
+    return t.data_ptr(), st[0], (st[1] if len(lead) == 2 else 0)
+
+
+def _activation(name, t, dim):
+    """The tensor whose dtype, device and shape the others follow."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a torch.Tensor (got %s)" % (name, type(t).__name__))
+    if t.dim() != dim:
+        raise ValueError("%s has shape %s; expected %d dimensions" % (name, tuple(t.shape), dim))
+    if t.dtype not in _DTYPE_CODE:
+        raise ValueError("%s has dtype %s; expected torch.float32 or torch.bfloat16" % (name, t.dtype))
+    return _DTYPE_CODE[t.dtype]
+
+
+class _On:
+    """The device and stream of one call: makes them current for its allocations and launches."""
+
+    def __init__(self, t, stream):
+        if t.device.type != "cuda":
+            raise ValueError("tensors are on %s; every tensor must be on a CUDA device" % t.device)
+        self.ctx = None
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError("the stream is on %s and the tensors are on %s" % (stream.device, t.device))
+            self.ctx = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(t.device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return (self.stream if self.stream is not None else torch.cuda.current_stream()).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _workspace(t, nbytes, device):
+    """A caller's workspace or a fresh one; the tensor and its size in bytes."""
+    if t is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device:
+        raise ValueError("workspace must be a contiguous torch.uint8 tensor on %s" % device)
+    return t
+
+
+def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, y=None, final_state=None,
+             want_final=True, stream=None):
+    """Short causal convolution with an optional SiLU (ssd_conv_fwd): x [b, L, C], weight
+    [C, W] and bias [C] float32, init_state [b, W-1, C] (the inputs before the first token),
+    lengths [b] int32 (each row's own tokens).  Returns (y [b, L, C], final_state [b, W-1, C]);
+    final_state may be init_state, which is then updated in place."""
+    L_ = lib()
+    code = _activation("x", x, 3)
+    b, L, C = x.shape
+    W = weight.shape[1] if weight.dim() == 2 else 0
+    dev = x.device
+    xp, xb, xt = _rows("x", x, (b, L, C), x)
+    wp = _param("weight", weight, (C, W), dev)
+    bp = _param("bias", bias, (C,), dev)
+    ip = _param("init_state", init_state, (b, W - 1, C), dev, x.dtype)
+    lp = _param("lengths", lengths, (b,), dev, torch.int32)
+    with _On(x, stream) as s:
+        if y is None:
+            y = torch.empty((b, L, C), dtype=x.dtype, device=dev)
+        if final_state is None and want_final and W > 1:
+            final_state = torch.empty((b, W - 1, C), dtype=x.dtype, device=dev)
+        dims = ConvDims(b, L, C, W, code, xb, xt, 0, 0)
+        _check(L_.ssd_conv_fwd(dims, xp, wp, bp, ip, lp, _param("y", y, (b, L, C), dev, x.dtype),
+                               _param("final_state", final_state, (b, W - 1, C), dev, x.dtype),
+                               SSD_FLAG_SILU if silu else 0, s))
+    return y, final_state
+
+
+def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stream=None):
+    """One token of the convolution (ssd_conv_step): x [b, C], state [b, W-1, C], updated in
+    place unless state_out is given.  Returns y [b, C]."""
+    L_ = lib()
+    code = _activation("x", x, 2)
+    b, C = x.shape
+    W = weight.shape[1] if weight.dim() == 2 else 0
+    dev, shape = x.device, (b, W - 1, C)
+    xp, xb, _ = _rows("x", x, (b, C), x)
+    wp = _param("weight", weight, (C, W), dev)
+    bp = _param("bias", bias, (C,), dev)
+    ip = _param("state", state, shape, dev, x.dtype)
+    op = ip if state_out is None else _param("state_out", state_out, shape, dev, x.dtype)
+    with _On(x, stream) as s:
+        if y is None:
+            y = torch.empty((b, C), dtype=x.dtype, device=dev)
+        dims = ConvDims(b, 1, C, W, code, xb, 0, 0, 0)
+        _check(L_.ssd_conv_step(dims, xp, wp, bp, ip, op, _param("y", y, (b, C), dev, x.dtype),
+                                SSD_FLAG_SILU if silu else 0, s))
+    return y
+
+
+class ConvGrads(NamedTuple):
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: Optional[torch.Tensor]
+    dinit: Optional[torch.Tensor]
+
+
+def conv_bwd(dy, x, weight, bias=None, init_state=None, *, dfinal=None, lengths=None, silu=True, workspace=None,
+             stream=None):
+    """Gradients of conv_fwd (ssd_conv_bwd) from dy [b, L, C] and dfinal [b, W-1, C], the
+    gradient of final_state.  dbias and dinit are None where the forward had no bias or
+    init_state."""
+    L_ = lib()
+    code = _activation("x", x, 3)
+    b, L, C = x.shape
+    W = weight.shape[1] if weight.dim() == 2 else 0
+    dev, st = x.device, (b, W - 1, C)
+    xp, xb, xt = _rows("x", x, (b, L, C), x)
+    gp, gb, gt = _rows("dy", dy, (b, L, C), x)
+    wp = _param("weight", weight, (C, W), dev)
+    bp = _param("bias", bias, (C,), dev)
+    ip = _param("init_state", init_state, st, dev, x.dtype)
+    fp = _param("dfinal", dfinal, st, dev, x.dtype)
+    lp = _param("lengths", lengths, (b,), dev, torch.int32)
+    dims = ConvDims(b, L, C, W, code, xb, xt, gb, gt)
+    with _On(x, stream) as s:
+        ws = _workspace(workspace, L_.ssd_conv_bwd_workspace_bytes(dims), dev)
+        g = ConvGrads(torch.empty((b, L, C), dtype=x.dtype, device=dev),
+                      torch.empty((C, W), dtype=torch.float32, device=dev),
+                      None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev),
+                      None if init_state is None else torch.empty(st, dtype=x.dtype, device=dev))
+        _check(L_.ssd_conv_bwd(dims, gp, xp, wp, bp, ip, fp, lp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias),
+                               _ptr(g.dinit), SSD_FLAG_SILU if silu else 0, ws.data_ptr(), ws.numel(), s))
+    return g
+
+
+def _selective_inputs(u, delta, A, B, C, D, z, delta_bias, step, dy=None):
+    """Checks of the selective scan's inputs; (dims, pointers in the C ABI's order up to
+    delta_bias, pointer of dy)."""
+    code = _activation("u", u, 2 if step else 3)
+    shape, dev = tuple(u.shape), u.device
+    lead, d = shape[:-1], shape[-1]
+    up, ub, ut = _rows("u", u, shape, u)
+    ep, eb, et = _rows("delta", delta, shape, u)
+    Bp, Bb, Bt = _coef_rows("B", B, lead, u)
+    Cp, Cb, Ct = _coef_rows("C", C, lead, u)
+    G, N = B.shape[-2:]
+    if C.shape[-2:] != (G, N):
+        raise ValueError("C has shape %s; expected %s" % (tuple(C.shape), tuple(B.shape)))
+    zp, zb, zt = _rows("z", z, shape, u) if z is not None else (None, 0, 0)
+    gp, gb, gt = _rows("dy", dy, shape, u) if dy is not None else (None, 0, 0)
+    ptrs = (up, ep, _param("A", A, (d, N), dev), Bp, Cp, _param("D", D, (d,), dev), zp,
+            _param("delta_bias", delta_bias, (d,), dev))
+    dims = SelectiveDims(lead[0], 1 if step else lead[1], d, N, G, code, 0, ub, ut, eb, et, zb, zt, Bb, Bt, Cb, Ct,
+                         gb, gt)
+    return dims, ptrs, gp
+
+
+def selective_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state=None, *, lengths=None,
+                  softplus=True, y=None, final_state=None, keep=False, workspace=None, stream=None):
+    """Selective scan with a decay for every channel and state (ssd_selective_fwd):
+        dt = softplus(delta + delta_bias);  h = exp(dt A) h + dt u B;  y = (C.h + D u) silu(z)
+    u, delta, z [b, L, D], A [D, N], B and C [b, L, G, N], D and delta_bias [D], init_state
+    [b, D, N] float32, lengths [b] int32.  Returns (y, final_state), or with keep=True
+    (y, final_state, kept), where kept is what selective_bwd needs.  final_state may be
+    init_state, which is then updated in place.  Unlike fwd, the input term carries dt."""
+    L_ = lib()
+    dims, ptrs, _ = _selective_inputs(u, delta, A, B, C, D, z, delta_bias, False)
+    b, L, d = u.shape
+    dev, st = u.device, (b, d, B.shape[3])
+    ip = _param("init_state", init_state, st, dev)
+    lp = _param("lengths", lengths, (b,), dev, torch.int32)
+    with _On(u, stream) as s:
+        ws = _workspace(workspace, L_.ssd_selective_fwd_workspace_bytes(dims), dev)
+        if y is None:
+            y = torch.empty((b, L, d), dtype=u.dtype, device=dev)
+        if final_state is None:
+            final_state = torch.empty(st, dtype=torch.float32, device=dev)
+        kept = torch.empty(L_.ssd_selective_kept_bytes(dims), dtype=torch.uint8, device=dev) if keep else None
+        _check(L_.ssd_selective_fwd(dims, *ptrs, ip, lp, _param("y", y, (b, L, d), dev, u.dtype),
+                                    _param("final_state", final_state, st, dev), _ptr(kept),
+                                    SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), s))
+    return (y, final_state, kept) if keep else (y, final_state)
+
+
+def selective_step(u, delta, A, B, C, D, z, delta_bias, state, *, softplus=True, y=None, state_out=None, stream=None):
+    """One token of the selective scan (ssd_selective_step): u, delta, z [b, D], B and C
+    [b, G, N], state [b, D, N] float32, updated in place unless state_out is given.
+    Returns y [b, D]."""
+    L_ = lib()
+    dims, ptrs, _ = _selective_inputs(u, delta, A, B, C, D, z, delta_bias, True)
+    b, d = u.shape
+    dev, st = u.device, (b, d, B.shape[2])
+    ip = _param("state", state, st, dev)
+    op = ip if state_out is None else _param("state_out", state_out, st, dev)
+    with _On(u, stream) as s:
+        if y is None:
+            y = torch.empty((b, d), dtype=u.dtype, device=dev)
+        _check(L_.ssd_selective_step(dims, *ptrs, ip, op, _param("y", y, (b, d), dev, u.dtype),
+                                     SSD_FLAG_SOFTPLUS if softplus else 0, s))
+    return y
+
+
+class SelectiveGrads(NamedTuple):
+    du: torch.Tensor
+    ddelta: torch.Tensor
+    dA: torch.Tensor
+    dB: torch.Tensor
+    dC: torch.Tensor
+    dD: Optional[torch.Tensor]
+    dz: Optional[torch.Tensor]
+    ddelta_bias: Optional[torch.Tensor]
+    dinit: torch.Tensor
+
+
+def selective_bwd(dy, u, delta, A, B, C, D, z, delta_bias, kept, *, dfinal=None, lengths=None, softplus=True,
+                  workspace=None, stream=None):
+    """Gradients of selective_fwd (ssd_selective_bwd) from dy [b, L, D] and dfinal [b, D, N]
+    (the gradient of final_state), with the kept states of a selective_fwd(keep=True) on the
+    same arguments.  dD, dz and ddelta_bias are None where the forward had no such input."""
+    L_ = lib()
+    dims, ptrs, gp = _selective_inputs(u, delta, A, B, C, D, z, delta_bias, False, dy)
+    b, L, d = u.shape
+    G, N = B.shape[2:]
+    dev = u.device
+    fp = _param("dfinal", dfinal, (b, d, N), dev)
+    lp = _param("lengths", lengths, (b,), dev, torch.int32)
+    kp = _param("kept", kept, (L_.ssd_selective_kept_bytes(dims),), dev, torch.uint8)
+    with _On(u, stream) as s:
+        ws = _workspace(workspace, L_.ssd_selective_bwd_workspace_bytes(dims), dev)
+
+        def act(*shape):
+            return torch.empty(shape, dtype=u.dtype, device=dev)
+
+        def f32(*shape):
+            return torch.empty(shape, dtype=torch.float32, device=dev)
+        g = SelectiveGrads(act(b, L, d), act(b, L, d), f32(d, N), act(b, L, G, N), act(b, L, G, N),
+                           None if D is None else f32(d), None if z is None else act(b, L, d),
+                           None if delta_bias is None else f32(d), f32(b, d, N))
+        _check(L_.ssd_selective_bwd(dims, gp, *ptrs, kp, fp, lp, _ptr(g.du), _ptr(g.ddelta), _ptr(g.dA), _ptr(g.dB),
+                                    _ptr(g.dC), _ptr(g.dD), _ptr(g.dz), _ptr(g.ddelta_bias), _ptr(g.dinit),
+                                    SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), s))
+    return g
+
+
+def norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, want_stats=False, stream=None):
+    """Layer norm of the rows of x [rows, D] (ssd_norm_fwd), weight and bias [D] float32.
+    Returns y, or (y, mean, rstd) with want_stats=True, which norm_bwd needs."""
+    L_ = lib()
+    code = _activation("x", x, 2)
+    rows, d = x.shape
+    dev = x.device
+    xp, xs, _ = _rows("x", x, (rows, d), x)
+    wp = _param("weight", weight, (d,), dev)
+    bp = _param("bias", bias, (d,), dev)
+    mean = rstd = None
+    with _On(x, stream) as s:
+        if y is None:
+            y = torch.empty((rows, d), dtype=x.dtype, device=dev)
+        if want_stats:
+            mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+            rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        dims = NormDims(rows, d, code, 0, xs, 0)
+        _check(L_.ssd_norm_fwd(dims, xp, wp, bp, eps, _param("y", y, (rows, d), dev, x.dtype), _ptr(mean), _ptr(rstd),
+                               s))
+    return (y, mean, rstd) if want_stats else y
+
+
+class NormGrads(NamedTuple):
+    dx: torch.Tensor
+    dweight: torch.Tensor
+    dbias: torch.Tensor
+
+
+def norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
+    """Gradients of norm_fwd (ssd_norm_bwd) from dy [rows, D] and the forward's mean and rstd."""
+    L_ = lib()
+    code = _activation("x", x, 2)
+    rows, d = x.shape
+    dev = x.device
+    xp, xs, _ = _rows("x", x, (rows, d), x)
+    gp, gs, _ = _rows("dy", dy, (rows, d), x)
+    wp = _param("weight", weight, (d,), dev)
+    mp = _param("mean", mean, (rows,), dev)
+    rp = _param("rstd", rstd, (rows,), dev)
+    dims = NormDims(rows, d, code, 0, xs, gs)
+    with _On(x, stream) as s:
+        ws = _workspace(workspace, L_.ssd_norm_bwd_workspace_bytes(dims), dev)
+        g = NormGrads(torch.empty((rows, d), dtype=x.dtype, device=dev),
+                      torch.empty((d,), dtype=torch.float32, device=dev),
+                      torch.empty((d,), dtype=torch.float32, device=dev))
+        _check(L_.ssd_norm_bwd(dims, gp, xp, wp, mp, rp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias), ws.data_ptr(),
+                               ws.numel(), s))
+    return g

@@ -226,6 +226,153 @@ ssd_status_t ssd_step(const ssd_dims_t *dims, const void *x, const void *dt, con
                       const void *B, const void *C, const float *D, float *state, void *y,
                       uint32_t flags, void *stream);
 
+/* ---- the operators around a scan ------------------------------------------------- *
+ *
+ * A selective block runs norm -> projection -> short causal convolution -> selective scan
+ * (gated) -> projection; the convolution stands in front of ssd_chunk_scan_fwd as well.
+ * Each operator has a forward for prompts, the convolution and the scan one for a single
+ * token, and each a backward.  They share the conventions above (caller-owned device
+ * memory, caller's workspace, errors before anything is enqueued, no allocation, no
+ * synchronisation) with these differences:
+ *
+ * Strides.  An activation input may be a view: rows of contiguous channels at any
+ *   batch and token stride (elements, >= 0), for example one half of a projection's output.
+ *   The strides are fields of the dims.  Outputs, states and parameters are contiguous.
+ * Alignment.  Pointers are aligned to their element size; B and C rows, in bfloat16, to 4
+ *   bytes (even strides).  Where addresses and sizes allow 16-byte accesses, the
+ *   convolution and the norm use them; results are the same either way.  Single-token
+ *   states of the scan must be 16-byte aligned.
+ * Lengths.  `lengths` (device, int32 [batch], or NULL for seqlen everywhere) gives each
+ *   row's own tokens, clamped to 0..seqlen.  Tokens past a row's length are not read into
+ *   any result (whatever they hold), their outputs and gradients are 0, and the final state
+ *   is the one after the row's last token (the initial state of an empty row).
+ * Arithmetic.  Everything is computed in float32 and rounded once when stored in the
+ *   activation dtype; parameters, their gradients and the scan's states are float32.
+ *   Sums over tokens, rows and channels are added in a fixed order: results do not change
+ *   from call to call.
+ */
+#define SSD_FLAG_SILU 8u       /* ssd_conv_*: y = pre * sigmoid(pre) instead of y = pre      */
+#define SSD_FLAG_SOFTPLUS 16u  /* ssd_selective_*: dt = log(1 + exp(delta + delta_bias))
+                                  instead of dt = delta + delta_bias                          */
+
+typedef struct ssd_conv_dims {
+    int64_t batch, seqlen, channels;
+    int32_t width;     /* W: taps, 2..4                                                  */
+    int32_t dtype;     /* ssd_dtype_t                                                    */
+    int64_t x_batch_stride, x_token_stride;
+    int64_t dy_batch_stride, dy_token_stride;   /* backward only                         */
+} ssd_conv_dims_t;
+
+/* Short causal convolution of every channel:
+ *     pre[b,t,c] = bias[c] + sum_j weight[c,j] x[b, t - (W-1) + j, c];  y = pre, or its SiLU
+ *   x            view [batch, seqlen, channels] (act)
+ *   weight       [channels, W] float32; bias [channels] float32 or NULL
+ *   init_state   [batch, W-1, channels] (act) or NULL (zeros): the inputs before the first
+ *                token, oldest first
+ *   y            [batch, seqlen, channels] (act)
+ *   final_state  [batch, W-1, channels] (act) or NULL: the last W-1 inputs of each row; may
+ *                be init_state (updated in place)
+ *   flags        0 or SSD_FLAG_SILU */
+ssd_status_t ssd_conv_fwd(const ssd_conv_dims_t *dims, const void *x, const float *weight, const float *bias,
+                          const void *init_state, const int32_t *lengths, void *y, void *final_state,
+                          uint32_t flags, void *stream);
+
+/* One token: dims.seqlen must be 1; x [batch, channels] at x_batch_stride, state_in and
+ * state_out [batch, W-1, channels] (act; the same pointer updates in place), y [batch, channels]. */
+ssd_status_t ssd_conv_step(const ssd_conv_dims_t *dims, const void *x, const float *weight, const float *bias,
+                           const void *state_in, void *state_out, void *y, uint32_t flags, void *stream);
+
+/* Gradients of ssd_conv_fwd, from dy (view, act) and dfinal ([batch, W-1, channels] (act),
+ * the gradient of final_state, or NULL): dx [batch, seqlen, channels] (act), dweight
+ * [channels, W] and dbias [channels] (or NULL) float32, dinit [batch, W-1, channels] (act,
+ * or NULL).  The other arguments are the forward's. */
+size_t ssd_conv_bwd_workspace_bytes(const ssd_conv_dims_t *dims);
+ssd_status_t ssd_conv_bwd(const ssd_conv_dims_t *dims, const void *dy, const void *x, const float *weight,
+                          const float *bias, const void *init_state, const void *dfinal, const int32_t *lengths,
+                          void *dx, float *dweight, float *dbias, void *dinit, uint32_t flags, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+typedef struct ssd_selective_dims {
+    int64_t batch, seqlen, channels;
+    int64_t dstate;    /* N: 16, 32 or 64                                                */
+    int64_t ngroups;   /* G: channel d reads B and C of group d / (channels / G)          */
+    int32_t dtype;     /* ssd_dtype_t                                                    */
+    int32_t reserved;  /* must be 0                                                      */
+    int64_t u_batch_stride, u_token_stride;
+    int64_t delta_batch_stride, delta_token_stride;
+    int64_t z_batch_stride, z_token_stride;
+    int64_t B_batch_stride, B_token_stride;
+    int64_t C_batch_stride, C_token_stride;
+    int64_t dy_batch_stride, dy_token_stride;   /* backward only                         */
+} ssd_selective_dims_t;
+
+/* Selective scan with a decay for every channel and state (unlike ssd_chunk_scan_fwd, the
+ * input term carries dt, and dt may be derived here):
+ *     dt_t = delta[b,t,d] + delta_bias[d], through SSD_FLAG_SOFTPLUS if given
+ *     h_t[n] = exp(dt_t A[d,n]) h_{t-1}[n] + dt_t u[b,t,d] B[b,t,g,n]
+ *     y[b,t,d] = sum_n C[b,t,g,n] h_t[n] + D[d] u[b,t,d], times z sigmoid(z) if z is given
+ *   u, delta, z     views [batch, seqlen, channels] (act); z may be NULL
+ *   A               [channels, dstate]; D and delta_bias [channels] or NULL (float32)
+ *   B, C            views [batch, seqlen, ngroups * dstate] (act)
+ *   init_state      [batch, channels, dstate] float32 or NULL (zeros)
+ *   y               [batch, seqlen, channels] (act)
+ *   final_state     [batch, channels, dstate] float32 or NULL; may be init_state
+ *   kept            NULL, or ssd_selective_kept_bytes of device memory: the states before
+ *                   every 8th token, which ssd_selective_bwd needs
+ * Any finite A and dt whose exp(dt A) does not overflow; dt A <= 0 makes decays. */
+size_t ssd_selective_kept_bytes(const ssd_selective_dims_t *dims);
+size_t ssd_selective_fwd_workspace_bytes(const ssd_selective_dims_t *dims);
+ssd_status_t ssd_selective_fwd(const ssd_selective_dims_t *dims, const void *u, const void *delta, const float *A,
+                               const void *B, const void *C, const float *D, const void *z,
+                               const float *delta_bias, const float *init_state, const int32_t *lengths, void *y,
+                               float *final_state, void *kept, uint32_t flags, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* One token: dims.seqlen must be 1; u, delta, z and y [batch, channels], B and C [batch,
+ * ngroups * dstate], at the batch strides; state_in and state_out [batch, channels, dstate]
+ * float32 (the same pointer updates in place). */
+ssd_status_t ssd_selective_step(const ssd_selective_dims_t *dims, const void *u, const void *delta, const float *A,
+                                const void *B, const void *C, const float *D, const void *z,
+                                const float *delta_bias, const float *state_in, float *state_out, void *y,
+                                uint32_t flags, void *stream);
+
+/* Gradients of ssd_selective_fwd from dy (view, act) and dfinal ([batch, channels, dstate]
+ * float32, the gradient of final_state, or NULL), with the `kept` states of a forward call
+ * on the same arguments.  Outputs: du, ddelta and dz [batch, seqlen, channels] (act; dz
+ * exactly if z is given), dB and dC [batch, seqlen, ngroups, dstate] (act), dA [channels,
+ * dstate], dD and ddelta_bias [channels] (or NULL) and dinit [batch, channels, dstate] (or
+ * NULL), float32. */
+size_t ssd_selective_bwd_workspace_bytes(const ssd_selective_dims_t *dims);
+ssd_status_t ssd_selective_bwd(const ssd_selective_dims_t *dims, const void *dy, const void *u, const void *delta,
+                               const float *A, const void *B, const void *C, const float *D, const void *z,
+                               const float *delta_bias, const void *kept, const float *dfinal,
+                               const int32_t *lengths, void *du, void *ddelta, float *dA, void *dB, void *dC,
+                               float *dD, void *dz, float *ddelta_bias, float *dinit, uint32_t flags,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct ssd_norm_dims {
+    int64_t rows, channels;
+    int32_t dtype;     /* ssd_dtype_t                                                    */
+    int32_t reserved;  /* must be 0                                                      */
+    int64_t x_row_stride;
+    int64_t dy_row_stride;   /* backward only                                            */
+} ssd_norm_dims_t;
+
+/* Layer norm of rows of channels:
+ *     y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   x [rows, channels] (act) at x_row_stride; weight and bias [channels] float32 or NULL;
+ *   eps >= 0; y [rows, channels] (act); mean and rstd [rows] float32 or NULL. */
+ssd_status_t ssd_norm_fwd(const ssd_norm_dims_t *dims, const void *x, const float *weight, const float *bias,
+                          float eps, void *y, float *mean, float *rstd, void *stream);
+
+/* Gradients of ssd_norm_fwd from dy [rows, channels] (act) at dy_row_stride and the
+ * forward's mean and rstd: dx [rows, channels] (act), dweight and dbias [channels] float32
+ * (or NULL). */
+size_t ssd_norm_bwd_workspace_bytes(const ssd_norm_dims_t *dims);
+ssd_status_t ssd_norm_bwd(const ssd_norm_dims_t *dims, const void *dy, const void *x, const float *weight,
+                          const float *mean, const float *rstd, void *dx, float *dweight, float *dbias,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- inspection (tests and tools) ------------------------------------------------ */
 
 /* Runs steps first_stage..last_stage of ssd_chunk_scan_fwd (1 = log-decay prefix sums,
