@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     const float *h0 = a.init ? a.init + (b * a.D + q.d) * (int64_t)N : nullptr;
 #pragma unroll
     for (int n = 0; n < N; ++n) h[n] = a.nc > 1 ? S[n * 64] : (h0 ? h0[n] : 0.f);
-    T *y = reinterpret_cast<T *>(a.y) + b * a.L * (int64_t)a.D + q.d;
+    T *y = reinterpret_cast<T *>(a.y) + b * a.L * (int64_t)a.D;
     T dv[kKeep], uv[kKeep], zv[kKeep];
     auto fetch = [&](int t0) {
 #pragma unroll
@@ -180,12 +180,12 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
                 }
                 float o = acc[0] + acc[1];
                 if (a.z.p) o *= silu_f32(to_f32(zv[i]));
-                if (q.live) y[(t0 + i) * (int64_t)a.D] = from_f32<T>(o);
+                if (q.live) (y + (t0 + i) * (int64_t)a.D)[q.d] = from_f32<T>(o);
             }
         }
     }
     if (q.live) {
-        for (int t = max(begin, end); t < stop; ++t) y[t * (int64_t)a.D] = from_f32<T>(0.f);
+        for (int t = max(begin, end); t < stop; ++t) (y + t * (int64_t)a.D)[q.d] = from_f32<T>(0.f);
         if (a.final_state && c == a.nc - 1) {
             float *f = a.final_state + (b * a.D + q.d) * (int64_t)N;
 #pragma unroll

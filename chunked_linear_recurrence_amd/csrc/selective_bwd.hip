@@ -26,16 +26,20 @@
 
 namespace ssd {
 
-constexpr int kSB = 16;               // states per wave
-constexpr int kRow = 36;              // floats per lane in the reduction buffer: 32 and padding, 16-byte rows
-constexpr int kHalf = 32 * kRow + 32; // second half of the lanes: 32 banks away from the first
+constexpr int kSB = 16;                  // states per wave
+// The reduction buffer of a wave: a row of 16 products (and 4 of padding) per lane, 16 rows
+// per quarter of the lanes, quarters 16 banks apart, so that both the 16-byte writes along a
+// row and the reads down a column are free of bank conflicts.
+constexpr int kRow = 20, kQuarter = 16 * kRow + 16;
 
-template <typename T, int N>
+template <typename T, int N, bool GATE>
 __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     constexpr int NB = N / kSB, TPB = 4 / NB, K = kKeep;
-    __shared__ float red[4][2 * kHalf];
-    __shared__ float comb[4][K][64];
-    __shared__ float cross[NB > 1 ? 4 : 1][NB > 1 ? K : 1][3][64];
+    __shared__ __align__(16) float red[4][4 * kQuarter];
+    __shared__ float comb[4][K][2][64];
+    // dt, u, d(softplus), r lane by lane and, where a tile has several blocks of states, a
+    // block's part of y, q and sum A w
+    __shared__ float tok[4][K][NB > 1 ? 7 : 4][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int parts = (a.tiles + TPB - 1) / TPB;
     const int pg = blockIdx.x % (parts * a.G), g = pg / parts, part = pg % parts;
@@ -59,139 +63,186 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
         carry[n] = a.nc > 1 ? S[n * 64] : (f0 ? f0[n] : 0.f);
         dA[n] = 0.f;
     }
-    T *du = reinterpret_cast<T *>(a.du) + b * a.L * (int64_t)a.D + q.d;
-    T *dd = reinterpret_cast<T *>(a.ddelta) + b * a.L * (int64_t)a.D + q.d;
-    T *dz = reinterpret_cast<T *>(a.dz) + b * a.L * (int64_t)a.D + q.d;
+    // row t of an output [batch, L, D]
+    auto out_row = [&](void *p, int t) { return reinterpret_cast<T *>(p) + (b * a.L + t) * a.D; };
+    // Reads of tok go by a lane index of their own, so that the values come back from LDS and
+    // are not kept in registers from the way forward to the way back.
+    const int back = hidden_lane(lane);
+    float *mine = red[wave] + (lane / 16) * kQuarter + (lane % 16) * kRow;
+    const float *column = red[wave] + (lane / 16) * kQuarter + lane % 16;
+    const float live = q.live ? 1.f : 0.f;
+
+    // dz and dD of a token, given its y without the skip term
+    auto finish_z = [&](int t, float u, float r, float gz, float y) {
+        dD = fmaf(r, u, dD);
+        if (GATE && q.live && t < end) out_row(a.dz, t)[q.d] = from_f32<T>(gz * fmaf(skip, u, y));
+    };
+    // du and ddelta of a token, given q and sum A w (base-2 rates)
+    auto finish_u = [&](int t, float dt, float u, float sig, float r, float qq, float dw) {
+        const float dl = fmaf(dw, kLn2F, u * qq) * sig;
+        if (q.live && t < end) {
+            dbias += dl;
+            out_row(a.du, t)[q.d] = from_f32<T>(fmaf(dt, qq, skip * r));
+            out_row(a.ddelta, t)[q.d] = from_f32<T>(dl);
+        }
+    };
+    // r = dout silu(z) and dout d(silu)(z)
+    auto upstream = [&](T dyv, T zv, float in, float *r, float *gz) {
+        *r = to_f32(dyv) * in;
+        *gz = 0.f;
+        if (GATE) {
+            const float z = to_f32(zv), s = sigmoid_f32(z);
+            *gz = *r * s * fmaf(z, 1.f - s, 1.f);
+            *r *= z * s;
+        }
+    };
+    // The lane's quarter of column lane % 16 of the products in the buffer.  Reads are started
+    // before the next token's products are written (a wave's LDS operations run in order) and
+    // added up after its arithmetic.
+    float col[16];
+    auto column_read = [&]() {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) col[k] = column[k * kRow];
+    };
+    auto column_sum = [&]() {
+        float s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[k] = (col[k] + col[4 + k]) + (col[8 + k] + col[12 + k]);
+        return (s[0] + s[1]) + (s[2] + s[3]);
+    };
+    auto kept_state = [&](int t0, float (&h)[kSB]) {
+        const float *kp = a.keep + sel_keep_slot(a, b, t0 / K, q.tt, n0);
+#pragma unroll
+        for (int n = 0; n < kSB; ++n) h[n] = kp[n * 64];
+    };
 
     for (int t0 = begin + (max(end - begin, 1) - 1) / K * K; t0 >= begin && t0 < end; t0 -= K) {
         const int m = min(K, end - t0);
-        float dt[K], u[K], sig[K], r[K], gz[K], yp[K], qs[K], ds[K], rs[K];
         float h0[kSB], hs[K][kSB];
-        const float *kp = a.keep + sel_keep_slot(a, b, t0 / K, q.tt, n0);
-#pragma unroll
-        for (int n = 0; n < kSB; ++n) h0[n] = kp[n * 64];
+        kept_state(t0, h0);
+        Uniform<T, kSB> Bt, Ct, Bn, Cn;
+        T dv[3], uv[3], dyv[3], zv[3];                      // tokens i, i + 1 and i + 2, by i mod 3
+        // The token after the group's last is a copy of an earlier one: `in` is 0 for it.
+        auto fetch = [&](int i) {
+            const int t = hidden(min(t0 + i, end - 1));
+            dv[i % 3] = row_of<T>(a.delta, b, t)[q.d];
+            uv[i % 3] = row_of<T>(a.u, b, t)[q.d];
+            dyv[i % 3] = row_of<T>(a.dy, b, t)[q.d];
+            if (GATE) zv[i % 3] = row_of<T>(a.z, b, t)[q.d];
+        };
+        auto coefficients = [&](int i, Uniform<T, kSB> &B, Uniform<T, kSB> &C) {
+            const int t = hidden(min(t0 + i, end - 1));
+            B.load(row_of<T>(a.B, b, t) + g * N + n0);
+            C.load(row_of<T>(a.C, b, t) + g * N + n0);
+        };
+        // Forward through the group: states, y, and dC's products.
+        fetch(0);
+        fetch(1);
+        coefficients(0, Bt, Ct);
 #pragma unroll
         for (int i = 0; i < K; ++i) {
-            const int t = min(t0 + i, end - 1);
-            const bool in = q.live && i < m;                // others add nothing to any sum
-            const float dy = to_f32(row_of<T>(a.dy, b, t)[q.d]);
-            const float raw = to_f32(row_of<T>(a.delta, b, t)[q.d]) + bias;
-            u[i] = in ? to_f32(row_of<T>(a.u, b, t)[q.d]) : 0.f;
-            dt[i] = sel_dt(raw, softplus, &sig[i]);
-            dt[i] = in ? dt[i] : 0.f;
-            r[i] = in ? dy : 0.f;
-            gz[i] = 0.f;
-            if (a.z.p) {
-                const float z = to_f32(row_of<T>(a.z, b, t)[q.d]);
-                gz[i] = r[i] * dsilu_f32(z);
-                r[i] = in ? r[i] * silu_f32(z) : 0.f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int t = min(t0 + i, end - 1);
-            Uniform<T, kSB> Bt, Ct;
-            Bt.load(row_of<T>(a.B, b, t) + g * N + n0);
-            Ct.load(row_of<T>(a.C, b, t) + g * N + n0);
-            const float x = dt[i] * u[i];
-            float y = 0.f;
+            if (i + 2 < K) fetch(i + 2);
+            if (i + 1 < K) coefficients(i + 1, Bn, Cn);
+            if (i > 0) column_read();
+            const float in = i < m ? live : 0.f;
+            float sig, r, gz, y = 0.f;
+            const float dt = in * sel_dt(to_f32(dv[i % 3]) + bias, softplus, &sig);
+            const float u = in * to_f32(uv[i % 3]), x = dt * u;
+            upstream(dyv[i % 3], GATE ? zv[i % 3] : dyv[i % 3], in, &r, &gz);
+            tok[wave][i][0][lane] = dt;
+            tok[wave][i][1][lane] = u;
+            tok[wave][i][2][lane] = sig;
+            tok[wave][i][3][lane] = r;
+            f32x4 p;
 #pragma unroll
             for (int n = 0; n < kSB; ++n) {
-                hs[i][n] = fmaf(exp2_fast(dt[i] * A2[n]), i ? hs[i ? i - 1 : 0][n] : h0[n], x * Bt[n]);
-                y = fmaf(Ct[n], hs[i][n], y);
+                hs[i][n] = fmaf(exp2_fast(dt * A2[n]), i ? hs[i ? i - 1 : 0][n] : h0[n], x * Bt[n]);
+                if (GATE) y = fmaf(Ct[n], hs[i][n], y);
+                p[n & 3] = r * hs[i][n];
+                if ((n & 3) == 3) *reinterpret_cast<f32x4 *>(mine + (n - 3)) = p;
             }
-            yp[i] = y;
+            if (i > 0) comb[wave][i - 1][1][lane] = column_sum();
+            if constexpr (NB == 1) finish_z(t0 + i, u, r, gz, y);
+            else {
+                tok[wave][i][4][lane] = y;
+            }
+            Bt = Bn;
+            Ct = Cn;
+            __builtin_amdgcn_sched_barrier(0);
         }
-        float *mine = red[wave] + (lane / 32) * kHalf + (lane % 32) * kRow;
-        const float *column = red[wave] + (lane / 32) * kHalf + lane % 32;
+        // And back: g, what follows from it, and dB's products.
+        coefficients(K - 1, Bt, Ct);
 #pragma unroll
         for (int i = K - 1; i >= 0; --i) {
-            const int t = min(t0 + i, end - 1);
-            Uniform<T, kSB> Bt, Ct;
-            Bt.load(row_of<T>(a.B, b, t) + g * N + n0);
-            Ct.load(row_of<T>(a.C, b, t) + g * N + n0);
-            const float x = dt[i] * u[i];
+            if (i > 0) coefficients(i - 1, Bn, Cn);
+            if (i == 2) kept_state(hidden(t0), h0);         // again, now that later tokens' states are done with
+            column_read();
+            const float dt = tok[wave][i][0][back], u = tok[wave][i][1][back], sig = tok[wave][i][2][back];
+            const float r = tok[wave][i][3][back], x = dt * u;
             float qq = 0.f, dw = 0.f;
-            f32x4 pb, pc;
+            f32x4 p;
 #pragma unroll
             for (int n = 0; n < kSB; ++n) {
-                const float gg = fmaf(r[i], Ct[n], carry[n]);
+                const float gg = fmaf(r, Ct[n], carry[n]);
                 qq = fmaf(gg, Bt[n], qq);
-                pb[n & 3] = gg * x;
-                pc[n & 3] = r[i] * hs[i][n];
-                carry[n] = exp2_fast(dt[i] * A2[n]) * gg;
+                p[n & 3] = gg * x;
+                carry[n] = exp2_fast(dt * A2[n]) * gg;
                 const float w = carry[n] * (i ? hs[i ? i - 1 : 0][n] : h0[n]);
                 dw = fmaf(w, A2[n], dw);
-                dA[n] = fmaf(w, dt[i], dA[n]);
-                if ((n & 3) == 3) {
-                    *reinterpret_cast<f32x4 *>(mine + (n - 3)) = pb;
-                    *reinterpret_cast<f32x4 *>(mine + 16 + (n - 3)) = pc;
-                }
+                dA[n] = fmaf(w, dt, dA[n]);
+                if ((n & 3) == 3) *reinterpret_cast<f32x4 *>(mine + (n - 3)) = p;
             }
-            qs[i] = qq;
-            ds[i] = dw;
-            __builtin_amdgcn_wave_barrier();
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-                s0 += column[k * kRow];
-                s1 += column[(k + 1) * kRow];
+            const float s = column_sum();
+            if (i == K - 1) comb[wave][K - 1][1][lane] = s;
+            else comb[wave][i + 1][0][lane] = s;
+            if constexpr (NB == 1) finish_u(t0 + i, dt, u, sig, r, qq, dw);
+            else {
+                tok[wave][i][5][lane] = qq;
+                tok[wave][i][6][lane] = dw;
             }
-            rs[i] = s0 + s1;
-            __builtin_amdgcn_wave_barrier();
+            Bt = Bn;
+            Ct = Cn;
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int i = 0; i < K; ++i) comb[wave][i][lane] = rs[i];
-        if constexpr (NB > 1) {
-#pragma unroll
-            for (int i = 0; i < K; ++i) {
-                cross[wave][i][0][lane] = yp[i];
-                cross[wave][i][1][lane] = qs[i];
-                cross[wave][i][2][lane] = ds[i];
-            }
-        }
+        column_read();
+        comb[wave][0][0][lane] = column_sum();
         __syncthreads();
-        // dB, dC of the 8 tokens: the sums of the workgroup's tiles and lane halves
+        // dB, dC of the 8 tokens: the sums of the workgroup's tiles and lane quarters
 #pragma unroll
         for (int e = threadIdx.x; e < K * 32 * NB; e += 256) {
-            const int v = e % 32, i = e / 32 % K, k = e / 32 / K;
+            const int v = e % 16, which = e / 16 % 2, i = e / 32 % K, k = e / 32 / K;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < TPB; ++w) s += comb[w * NB + k][i][v] + comb[w * NB + k][i][32 + v];
+            for (int w = 0; w < TPB; ++w) {
+                const float *p = comb[w * NB + k][i][which] + v;
+                s += (p[0] + p[16]) + (p[32] + p[48]);
+            }
             if (i < m)
-                a.part_bc[(((((int64_t)part * a.batch + b) * a.L + t0 + i) * a.G + g) * 2 + v / 16) * N + k * kSB + v % 16] = s;
+                a.part_bc[(((((int64_t)part * a.batch + b) * a.L + t0 + i) * a.G + g) * 2 + which) * N + k * kSB + v] = s;
         }
+        if constexpr (NB > 1) {
+            // the tile's NB waves share out its tokens, each adding the blocks' parts
+            for (int i = nb; i < K; i += NB) {
+                float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < K; ++i) {
-            if (i % NB == nb) {
-                if constexpr (NB > 1) {
-                    yp[i] = qs[i] = ds[i] = 0.f;
-                    const int w0 = wave - nb;
+                for (int w = 0; w < NB; ++w)
 #pragma unroll
-                    for (int w = 0; w < NB; ++w) {
-                        yp[i] += cross[w0 + w][i][0][lane];
-                        qs[i] += cross[w0 + w][i][1][lane];
-                        ds[i] += cross[w0 + w][i][2][lane];
-                    }
-                }
-                const float dl = fmaf(ds[i], kLn2F, u[i] * qs[i]) * sig[i];
-                dD = fmaf(r[i], u[i], dD);
-                if (q.live && i < m) {
-                    const int64_t at = (t0 + i) * (int64_t)a.D;
-                    dbias += dl;
-                    du[at] = from_f32<T>(fmaf(dt[i], qs[i], skip * r[i]));
-                    dd[at] = from_f32<T>(dl);
-                    if (a.z.p) dz[at] = from_f32<T>(gz[i] * fmaf(skip, u[i], yp[i]));
-                }
+                    for (int k = 0; k < 3; ++k) s[k] += tok[wave - nb + w][i][4 + k][lane];
+                const int t = min(t0 + i, end - 1);
+                float r, gz;
+                T dy1 = row_of<T>(a.dy, b, t)[q.d], z1 = dy1;
+                if (GATE) z1 = row_of<T>(a.z, b, t)[q.d];
+                upstream(dy1, z1, i < m ? live : 0.f, &r, &gz);
+                finish_z(t0 + i, tok[wave][i][1][lane], r, gz, s[0]);
+                finish_u(t0 + i, tok[wave][i][0][lane], tok[wave][i][1][lane], tok[wave][i][2][lane], r, s[1], s[2]);
             }
         }
         __syncthreads();
     }
     if (q.live) {
         for (int t = max(begin, end) + nb; t < stop; t += NB) {
-            const int64_t at = t * (int64_t)a.D;
-            du[at] = dd[at] = from_f32<T>(0.f);
-            if (a.z.p) dz[at] = from_f32<T>(0.f);
+            out_row(a.du, t)[q.d] = out_row(a.ddelta, t)[q.d] = from_f32<T>(0.f);
+            if (GATE) out_row(a.dz, t)[q.d] = from_f32<T>(0.f);
         }
         if (c == 0 && a.dinit) {
             float *o = a.dinit + (b * a.D + q.d) * (int64_t)N + n0;
@@ -201,14 +252,14 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     }
     // sums over this chunk's tokens; dD and dbias are spread over the blocks of states
     if constexpr (NB > 1) {
-        cross[wave][0][0][lane] = dD;
-        cross[wave][0][1][lane] = dbias;
+        comb[wave][0][0][lane] = dD;
+        comb[wave][0][1][lane] = dbias;
         __syncthreads();
         dD = dbias = 0.f;
 #pragma unroll
         for (int w = 0; w < NB; ++w) {
-            dD += cross[wave - nb + w][0][0][lane];
-            dbias += cross[wave - nb + w][0][1][lane];
+            dD += comb[wave - nb + w][0][0][lane];
+            dbias += comb[wave - nb + w][0][1][lane];
         }
     }
     if (real) {
@@ -269,7 +320,8 @@ static hipError_t sel_bwd_t(const SelArgs &a, hipStream_t s) {
     const int64_t sums = (a.batch * a.L * a.G * a.N * 2 + 255) / 256;
     const int64_t pars = (int64_t)a.G * a.tiles * (N + 2);
     if (blocks > INT32_MAX || sums > INT32_MAX || pars > INT32_MAX) return hipErrorInvalidValue;
-    sel_bwd_kernel<T, N><<<(uint32_t)blocks, 256, 0, s>>>(a);
+    if (a.z.p) sel_bwd_kernel<T, N, true><<<(uint32_t)blocks, 256, 0, s>>>(a);
+    else sel_bwd_kernel<T, N, false><<<(uint32_t)blocks, 256, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     sel_bwd_bc_kernel<T><<<(uint32_t)sums, 256, 0, s>>>(a, parts);
     if ((e = hipGetLastError()) != hipSuccess) return e;

@@ -37,9 +37,21 @@ struct Uniform<bf16, N> {
     }
 };
 
+// The same value, unknown to the compiler: addresses of unrolled tokens are then formed where
+// they are used instead of all at once, which the scalar registers cannot hold.
+__device__ __forceinline__ int hidden(int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+__device__ __forceinline__ int hidden_lane(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // A wave's tile: group, the lane's channel and its place in the [D] tensors.
 struct SelTile {
-    int tt, g, d;
+    int tt, g;
+    uint32_t d;          // unsigned: an address is a scalar row plus this, one vector register for all tensors
     bool live;
 };
 __device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int tt) {
@@ -49,21 +61,23 @@ __device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int tt) {
     q.g = tt / a.tiles;
     const int c = (tt % a.tiles) * 64 + (int)(threadIdx.x % 64);
     q.live = c < per;
-    q.d = q.g * per + min(c, per - 1);       // idle lanes read a channel that exists
+    q.d = (uint32_t)(q.g * per + min(c, per - 1));       // idle lanes read a channel that exists
     return q;
 }
 
 template <int N>
-__device__ __forceinline__ void sel_rates(const SelArgs &a, int d, int n0, float (&A2)[N]) {
+__device__ __forceinline__ void sel_rates(const SelArgs &a, uint32_t d, int n0, float (&A2)[N]) {
 #pragma unroll
     for (int n = 0; n < N; ++n) A2[n] = a.A[(int64_t)d * a.N + n0 + n] * kLog2eF;
 }
 
-// The step size of one token and its derivative by delta.
+// The step size of one token and its derivative by delta.  Chosen without a branch, which
+// would cut the unrolled tokens into blocks that cannot be scheduled together.
 __device__ __forceinline__ float sel_dt(float raw, bool softplus, float *sig) {
-    if (softplus) return softplus_f32(raw, sig);
-    *sig = 1.f;
-    return raw;
+    float s;
+    const float dt = softplus_f32(raw, &s);
+    *sig = softplus ? s : 1.f;
+    return softplus ? dt : raw;
 }
 
 // Offset of chunk c of batch row b in S (floats), lane included; state n is at n * 64.
