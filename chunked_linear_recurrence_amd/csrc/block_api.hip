@@ -147,7 +147,7 @@ ssd_status_t check_sel(const ssd_selective_dims_t *d, bool step) {
 }
 
 // Chunks of the forward (4 waves on each of 1024 SIMDs) and of the backward (2).
-constexpr int64_t kSelFwdWaves = 4096, kSelBwdWaves = 2048;
+constexpr int64_t kSelFwdWaves = 4096, kSelBwdWaves = 4096;
 
 ssd::SelArgs sel_args(const ssd_selective_dims_t &d, bool backward) {
     ssd::SelArgs a;

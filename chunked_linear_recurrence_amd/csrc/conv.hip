@@ -248,25 +248,16 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int TS) {
     }
 }
 
-// dw[c][j] and dbias[c] from the rows of partial sums [rows, W+1, C], in row order within
-// each of the workgroup's 4 quarters of the rows, quarters in order.
-__global__ __launch_bounds__(256) void conv_bwd_sum_kernel(const float *part, int64_t rows, int C, int W, float *dw,
-                                                           float *dbias) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x % 64, k = threadIdx.x / 64;
-    const int64_t cols = (int64_t)(W + 1) * C;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
-    float s = 0.f;
-    if (col < cols)
-        for (int64_t r = rows * k / 4; r < rows * (k + 1) / 4; ++r) s += part[r * cols + col];
-    red[k][lane] = s;
-    __syncthreads();
-    if (k == 0 && col < cols) {
-        s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
-        const int j = (int)(col / C), c = (int)(col % C);
-        if (j < W) dw[(int64_t)c * W + j] = s;
-        else if (dbias) dbias[c] = s;
-    }
+// dw[c][j] and dbias[c] from the rows of partial sums [rows, W+1, C].
+__global__ __launch_bounds__(1024) void conv_bwd_sum_kernel(const float *part, int64_t rows, int C, int W, float *dw,
+                                                            float *dbias) {
+    __shared__ float red[16][64];
+    const int64_t cols = (int64_t)(W + 1) * C, col = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+    const float s = rows_sum<16>(part + min(col, cols - 1), rows, cols, red);
+    if (threadIdx.x >= 64 || col >= cols) return;
+    const int j = (int)(col / C), c = (int)(col % C);
+    if (j < W) dw[(int64_t)c * W + j] = s;
+    else if (dbias) dbias[c] = s;
 }
 
 bool conv_supported(int W) { return W >= 2 && W <= 4; }
@@ -308,7 +299,7 @@ static hipError_t conv_bwd_t(const ConvArgs &a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t cols = (int64_t)(W + 1) * a.C;
-    conv_bwd_sum_kernel<<<(uint32_t)((cols + 63) / 64), 256, 0, s>>>(a.part, rows, a.C, W, a.dw, a.dbias);
+    conv_bwd_sum_kernel<<<(uint32_t)((cols + 63) / 64), 1024, 0, s>>>(a.part, rows, a.C, W, a.dw, a.dbias);
     return hipGetLastError();
 }
 

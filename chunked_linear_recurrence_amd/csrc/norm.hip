@@ -269,21 +269,14 @@ __global__ __launch_bounds__(256) void norm_bwd_cols_kernel(NormArgs a) {
     part[a.D + c] = db;
 }
 
-__global__ __launch_bounds__(256) void norm_bwd_sum_kernel(const float *part, int rows, int D, float *dw, float *db) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x % 64, k = threadIdx.x / 64;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
-    float s = 0.f;
-    if (col < 2 * (int64_t)D)
-        for (int r = rows * k / 4; r < rows * (k + 1) / 4; ++r) s += part[(int64_t)r * 2 * D + col];
-    red[k][lane] = s;
-    __syncthreads();
-    if (k == 0 && col < 2 * (int64_t)D) {
-        s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
-        if (col < D) {
-            if (dw) dw[col] = s;
-        } else if (db) db[col - D] = s;
-    }
+__global__ __launch_bounds__(1024) void norm_bwd_sum_kernel(const float *part, int rows, int D, float *dw, float *db) {
+    __shared__ float red[16][64];
+    const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x % 64, cols = 2 * (int64_t)D;
+    const float s = rows_sum<16>(part + min(col, cols - 1), rows, cols, red);
+    if (threadIdx.x >= 64 || col >= cols) return;
+    if (col < D) {
+        if (dw) dw[col] = s;
+    } else if (db) db[col - D] = s;
 }
 
 int64_t norm_bwd_blocks(int64_t rows, int64_t D) { return rows < kNormBwdBlocks ? rows : kNormBwdBlocks; }
@@ -299,7 +292,7 @@ static hipError_t norm_fwd_t(const NormArgs &a, hipStream_t s) {
 
 static hipError_t norm_bwd_sum(const NormArgs &a, int64_t blocks, hipStream_t s) {
     if (!a.dw && !a.db) return hipSuccess;
-    norm_bwd_sum_kernel<<<(uint32_t)((2 * (int64_t)a.D + 63) / 64), 256, 0, s>>>(a.part, (int)blocks, a.D, a.dw, a.db);
+    norm_bwd_sum_kernel<<<(uint32_t)((2 * (int64_t)a.D + 63) / 64), 1024, 0, s>>>(a.part, (int)blocks, a.D, a.dw, a.db);
     return hipGetLastError();
 }
 

@@ -20,6 +20,7 @@
 namespace ssd {
 
 constexpr int kSelWaves = 4;     // independent waves per workgroup
+constexpr int kAhead = 3, kRing = 4;   // steps that activations are fetched ahead, and their places
 
 // Wave -> (batch row, chunk, tile); tiles are neighbours, so the waves of a workgroup share
 // B and C.  False past the last unit.
@@ -54,35 +55,47 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     const View &coef = REV ? a.C : a.B;
     const View &val = REV ? a.dy : a.u;
     const bool gate = REV && a.z.p;
-    for (int t0 = begin; t0 < end; t0 += kKeep) {
-        const int m = min(kKeep, end - t0);
-        T dv[kKeep], xv[kKeep], zv[kKeep];
+    // Step k is token begin + k, or end - 1 - k backwards.  Activations are fetched kAhead steps
+    // early into a ring, coefficients one block of 16 states early.
+    T dv[kRing], xv[kRing], zv[kRing];
+    auto token = [&](int k) { return hidden(REV ? end - 1 - min(k, end - begin - 1) : begin + min(k, end - begin - 1)); };
+    auto fetch = [&](int k, int slot) {
+        const int t = token(k);
+        dv[slot] = row_of<T>(a.delta, b, t)[q.d];
+        xv[slot] = row_of<T>(val, b, t)[q.d];
+        if (gate) zv[slot] = row_of<T>(a.z, b, t)[q.d];
+    };
+    Uniform<T, 16> cf, cn;
+    auto coefficients = [&](int k, int n0) { cn.load(row_of<T>(coef, b, token(k)) + q.g * N + n0); };
+    if (begin < end) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) fetch(k, k);
+        coefficients(0, 0);
+    }
+    for (int k0 = 0; k0 < end - begin; k0 += kKeep) {
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
-            const int k = min(i, m - 1);
-            const int t = REV ? end - 1 - (t0 - begin) - k : t0 + k;
-            dv[i] = row_of<T>(a.delta, b, t)[q.d];
-            xv[i] = row_of<T>(val, b, t)[q.d];
-            if (gate) zv[i] = row_of<T>(a.z, b, t)[q.d];
-        }
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            if (i < m) {
-                const int t = REV ? end - 1 - (t0 - begin) - i : t0 + i;
-                Uniform<T, N> cf;
-                cf.load(row_of<T>(coef, b, t) + q.g * N);
+            if (k0 + i < end - begin) {
+                fetch(k0 + i + kAhead, (i + kAhead) % kRing);
                 float sig;
-                const float dt = sel_dt(to_f32(dv[i]) + bias, softplus, &sig);
+                const float dt = sel_dt(to_f32(dv[i % kRing]) + bias, softplus, &sig);
                 sum += dt;
-                float x = to_f32(xv[i]);
+                float x = to_f32(xv[i % kRing]);
                 if (!REV) x *= dt;
-                else if (gate) x *= silu_f32(to_f32(zv[i]));
+                else if (gate) x *= silu_f32(to_f32(zv[i % kRing]));
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const float e = exp2_fast(dt * A2[n]);
-                    h[n] = REV ? e * fmaf(x, cf[n], h[n]) : fmaf(e, h[n], x * cf[n]);
+                for (int n0 = 0; n0 < N; n0 += 16) {
+                    cf = cn;
+                    if (n0 + 16 < N) coefficients(k0 + i, n0 + 16);
+                    else coefficients(k0 + i + 1, 0);
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) {
+                        const float e = exp2_fast(dt * A2[n0 + n]);
+                        h[n0 + n] = REV ? e * fmaf(x, cf[n], h[n0 + n]) : fmaf(e, h[n0 + n], x * cf[n]);
+                    }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     float *S = a.S + sel_slot(a, b, c, tt, N);
@@ -107,7 +120,7 @@ __global__ __launch_bounds__(256) void sel_pass_kernel(SelArgs a) {
     const int64_t cs = (int64_t)ntt * a.N * 64, ds = (int64_t)ntt * 64;
     float *S = a.S + ((b * a.nc * ntt + tt) * (int64_t)a.N + n) * 64 + lane;
     const float *sd = a.sumdt + (b * a.nc * ntt + tt) * (int64_t)64 + lane;
-    constexpr int U = 8;                      // chunks whose values are in flight together
+    constexpr int U = 32;                     // chunks whose values are in flight together
     for (int c0 = 0; c0 < a.nc; c0 += U) {
         float s[U], d[U];
 #pragma unroll
@@ -146,18 +159,26 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
 #pragma unroll
     for (int n = 0; n < N; ++n) h[n] = a.nc > 1 ? S[n * 64] : (h0 ? h0[n] : 0.f);
     T *y = reinterpret_cast<T *>(a.y) + b * a.L * (int64_t)a.D;
-    T dv[kKeep], uv[kKeep], zv[kKeep];
-    auto fetch = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int t = min(t0 + i, end - 1);
-            dv[i] = row_of<T>(a.delta, b, t)[q.d];
-            uv[i] = row_of<T>(a.u, b, t)[q.d];
-            if (a.z.p) zv[i] = row_of<T>(a.z, b, t)[q.d];
-        }
+    T dv[kRing], uv[kRing], zv[kRing];
+    auto token = [&](int t) { return hidden(min(t, end - 1)); };
+    auto fetch = [&](int k, int slot) {
+        const int t = token(k);
+        dv[slot] = row_of<T>(a.delta, b, t)[q.d];
+        uv[slot] = row_of<T>(a.u, b, t)[q.d];
+        if (a.z.p) zv[slot] = row_of<T>(a.z, b, t)[q.d];
     };
+    Uniform<T, 16> Bt, Ct, Bn, Cn;
+    auto coefficients = [&](int k, int n0) {
+        const int t = token(k);
+        Bn.load(row_of<T>(a.B, b, t) + q.g * N + n0);
+        Cn.load(row_of<T>(a.C, b, t) + q.g * N + n0);
+    };
+    if (begin < end) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) fetch(begin + k, k);
+        coefficients(begin, 0);
+    }
     for (int t0 = begin; t0 < end; t0 += kKeep) {
-        fetch(t0);
         if (a.keep) {
             float *kp = a.keep + sel_keep_slot(a, b, t0 / kKeep, tt, 0);
 #pragma unroll
@@ -166,22 +187,28 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
             if (t0 + i < end) {
-                Uniform<T, N> Bt, Ct;
-                Bt.load(row_of<T>(a.B, b, t0 + i) + q.g * N);
-                Ct.load(row_of<T>(a.C, b, t0 + i) + q.g * N);
+                fetch(t0 + i + kAhead, (i + kAhead) % kRing);
                 float sig;
-                const float dt = sel_dt(to_f32(dv[i]) + bias, softplus, &sig);
-                const float u = to_f32(uv[i]), x = dt * u;
+                const float dt = sel_dt(to_f32(dv[i % kRing]) + bias, softplus, &sig);
+                const float u = to_f32(uv[i % kRing]), x = dt * u;
                 float acc[2] = {skip * u, 0.f};
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    h[n] = fmaf(exp2_fast(dt * A2[n]), h[n], x * Bt[n]);
-                    acc[n & 1] = fmaf(Ct[n], h[n], acc[n & 1]);
+                for (int n0 = 0; n0 < N; n0 += 16) {
+                    Bt = Bn;
+                    Ct = Cn;
+                    if (n0 + 16 < N) coefficients(t0 + i, n0 + 16);
+                    else coefficients(t0 + i + 1, 0);
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) {
+                        h[n0 + n] = fmaf(exp2_fast(dt * A2[n0 + n]), h[n0 + n], x * Bt[n]);
+                        acc[n & 1] = fmaf(Ct[n], h[n0 + n], acc[n & 1]);
+                    }
                 }
                 float o = acc[0] + acc[1];
-                if (a.z.p) o *= silu_f32(to_f32(zv[i]));
+                if (a.z.p) o *= silu_f32(to_f32(zv[i % kRing]));
                 if (q.live) (y + (t0 + i) * (int64_t)a.D)[q.d] = from_f32<T>(o);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (q.live) {

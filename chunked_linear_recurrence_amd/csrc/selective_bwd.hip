@@ -288,24 +288,17 @@ __global__ __launch_bounds__(256) void sel_bwd_bc_kernel(SelArgs a, int parts) {
     reinterpret_cast<T *>(which ? a.dC : a.dB)[bt * gn + g * a.N + n] = from_f32<T>(s);
 }
 
-// dA, dD and dbias: partial sums of all (batch row, chunk), 4 quarters of them in order.
-__global__ __launch_bounds__(256) void sel_bwd_par_kernel(SelArgs a) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x % 64, k = threadIdx.x / 64;
+// dA, dD and dbias: partial sums of all (batch row, chunk).
+__global__ __launch_bounds__(1024) void sel_bwd_par_kernel(SelArgs a) {
+    __shared__ float red[16][64];
     const int n = blockIdx.x % (a.N + 2), tt = blockIdx.x / (a.N + 2);
     const SelTile q = sel_tile(a, tt);
-    const int64_t rows = a.batch * a.nc, rs = (int64_t)a.G * a.tiles * (a.N + 2) * 64;
-    const float *p = a.part_par + ((int64_t)tt * (a.N + 2) + n) * 64 + lane;
-    float s = 0.f;
-    for (int64_t r = rows * k / 4; r < rows * (k + 1) / 4; ++r) s += p[r * rs];
-    red[k][lane] = s;
-    __syncthreads();
-    if (k == 0 && q.live) {
-        s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
-        if (n < a.N) a.dA[(int64_t)q.d * a.N + n] = s;
-        else if (n == a.N) { if (a.dD) a.dD[q.d] = s; }
-        else if (a.dbias) a.dbias[q.d] = s;
-    }
+    const float s = rows_sum<16>(a.part_par + ((int64_t)tt * (a.N + 2) + n) * 64 + threadIdx.x % 64, a.batch * a.nc,
+                                 (int64_t)a.G * a.tiles * (a.N + 2) * 64, red);
+    if (threadIdx.x >= 64 || !q.live) return;
+    if (n < a.N) a.dA[(int64_t)q.d * a.N + n] = s;
+    else if (n == a.N) { if (a.dD) a.dD[q.d] = s; }
+    else if (a.dbias) a.dbias[q.d] = s;
 }
 
 template <typename T, int N>
@@ -325,7 +318,7 @@ static hipError_t sel_bwd_t(const SelArgs &a, hipStream_t s) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
     sel_bwd_bc_kernel<T><<<(uint32_t)sums, 256, 0, s>>>(a, parts);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    sel_bwd_par_kernel<<<(uint32_t)pars, 256, 0, s>>>(a);
+    sel_bwd_par_kernel<<<(uint32_t)pars, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -182,6 +182,30 @@ __device__ __forceinline__ float softplus_f32(float v, float *sig) {
     return v > 20.f ? v : l;
 }
 
+// Sum over `rows` values a stride apart, for the 64 columns of a workgroup of W waves (p: this
+// lane's column).  Each wave adds a contiguous share in order, 8 loads in flight at a time, and
+// the first wave adds the shares in order; its lanes receive the result.
+template <int W>
+__device__ __forceinline__ float rows_sum(const float *p, int64_t rows, int64_t stride, float (&red)[W][64]) {
+    const int lane = threadIdx.x % 64, k = threadIdx.x / 64;
+    const int64_t end = rows * (k + 1) / W;
+    float s = 0.f;
+    for (int64_t r = rows * k / W; r < end; r += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = p[min(r + i, end - 1) * stride];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += r + i < end ? v[i] : 0.f;
+    }
+    red[k][lane] = s;
+    __syncthreads();
+    s = 0.f;
+    if (k == 0)
+#pragma unroll
+        for (int w = 0; w < W; ++w) s += red[w][lane];
+    return s;
+}
+
 __device__ __forceinline__ int row_length(const int32_t *lengths, int64_t b, int L) {
     if (!lengths) return L;
     return max(0, min(lengths[b], L));
