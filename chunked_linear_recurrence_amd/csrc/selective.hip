@@ -61,9 +61,9 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     auto token = [&](int k) { return hidden(REV ? end - 1 - min(k, end - begin - 1) : begin + min(k, end - begin - 1)); };
     auto fetch = [&](int k, int slot) {
         const int t = token(k);
-        dv[slot] = row_of<T>(a.delta, b, t)[q.d];
-        xv[slot] = row_of<T>(val, b, t)[q.d];
-        if (gate) zv[slot] = row_of<T>(a.z, b, t)[q.d];
+        dv[slot] = lane_load(row_of<T>(a.delta, b, t), q.d);
+        xv[slot] = lane_load(row_of<T>(val, b, t), q.d);
+        if (gate) zv[slot] = lane_load(row_of<T>(a.z, b, t), q.d);
     };
     Uniform<T, 16> cf, cn;
     auto coefficients = [&](int k, int n0) { cn.load(row_of<T>(coef, b, token(k)) + q.g * N + n0); };
@@ -72,77 +72,100 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
         for (int k = 0; k < kAhead; ++k) fetch(k, k);
         coefficients(0, 0);
     }
-    for (int k0 = 0; k0 < end - begin; k0 += kKeep) {
+    auto step = [&](int k, int slot) {
+        float sig;
+        const float dt = sel_dt(to_f32(dv[slot]) + bias, softplus, &sig);
+        sum += dt;
+        float x = to_f32(xv[slot]);
+        if (!REV) x *= dt;
+        else if (gate) x *= silu_f32(to_f32(zv[slot]));
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            if (k0 + i < end - begin) {
-                fetch(k0 + i + kAhead, (i + kAhead) % kRing);
-                float sig;
-                const float dt = sel_dt(to_f32(dv[i % kRing]) + bias, softplus, &sig);
-                sum += dt;
-                float x = to_f32(xv[i % kRing]);
-                if (!REV) x *= dt;
-                else if (gate) x *= silu_f32(to_f32(zv[i % kRing]));
+        for (int n0 = 0; n0 < N; n0 += 16) {
+            cf = cn;
+            if (n0 + 16 < N) coefficients(k, n0 + 16);
+            else coefficients(k + 1, 0);
 #pragma unroll
-                for (int n0 = 0; n0 < N; n0 += 16) {
-                    cf = cn;
-                    if (n0 + 16 < N) coefficients(k0 + i, n0 + 16);
-                    else coefficients(k0 + i + 1, 0);
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        const float e = exp2_fast(dt * A2[n0 + n]);
-                        h[n0 + n] = REV ? e * fmaf(x, cf[n], h[n0 + n]) : fmaf(e, h[n0 + n], x * cf[n]);
-                    }
-                }
+            for (int n = 0; n < 16; ++n) {
+                const float e = exp2_fast(dt * A2[n0 + n]);
+                h[n0 + n] = REV ? e * fmaf(x, cf[n], h[n0 + n]) : fmaf(e, h[n0 + n], x * cf[n]);
             }
-            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int steps = max(end - begin, 0);
+    int k0 = 0;
+    for (; k0 + kRing <= steps; k0 += kRing) {
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) {
+            fetch(k0 + i + kAhead, (i + kAhead) % kRing);
+            step(k0 + i, i);
         }
     }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (k0 + i < steps) step(k0 + i, i);
     float *S = a.S + sel_slot(a, b, c, tt, N);
 #pragma unroll
     for (int n = 0; n < N; ++n) S[n * 64] = h[n];
     a.sumdt[sel_slot(a, b, c, tt, 1)] = sum;
 }
 
-// (2): one thread per (batch row, tile, state, channel) walks the chunks; each chunk's slot
-// of S receives the state (REV: the carry) that enters it.
-template <bool REV>
-__global__ __launch_bounds__(256) void sel_pass_kernel(SelArgs a) {
-    const int ntt = a.G * a.tiles;
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= a.batch * ntt * a.N * 64) return;
-    const int lane = (int)(k % 64), n = (int)(k / 64 % a.N), tt = (int)(k / 64 / a.N % ntt);
-    const int64_t b = k / 64 / a.N / ntt;
+// (2).  A workgroup takes one state of one tile: its W waves share out the chunks, each first
+// joins its own (decay and end state), the joined parts meet in LDS, and each then walks its
+// chunks from the state that enters them.  Each chunk's slot of S receives the state (REV: the
+// carry) that enters it.  W is such that a wave has at most 16 chunks, whose values it then
+// holds in registers; it waits for memory once.
+constexpr int kPassChunks = 16;
+template <bool REV, int W>
+__global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
+    constexpr int U = kPassChunks;
+    __shared__ float part[W][2][64];
+    const int ntt = a.G * a.tiles, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int n = blockIdx.x % a.N, tt = blockIdx.x / a.N % ntt;
+    const int64_t b = blockIdx.x / a.N / ntt;
     const SelTile q = sel_tile(a, tt);
     const float A2 = a.A[(int64_t)q.d * a.N + n] * kLog2eF;
     const float *first = REV ? a.dfinal : a.init;
-    float h = first ? first[(b * a.D + q.d) * (int64_t)a.N + n] : 0.f;
     const int64_t cs = (int64_t)ntt * a.N * 64, ds = (int64_t)ntt * 64;
     float *S = a.S + ((b * a.nc * ntt + tt) * (int64_t)a.N + n) * 64 + lane;
     const float *sd = a.sumdt + (b * a.nc * ntt + tt) * (int64_t)64 + lane;
-    constexpr int U = 32;                     // chunks whose values are in flight together
-    for (int c0 = 0; c0 < a.nc; c0 += U) {
-        float s[U], d[U];
+    // in walking order, the last chunk has no values of its own (none follows it)
+    const int c0 = (int)((int64_t)a.nc * wave / W), c1 = (int)((int64_t)a.nc * (wave + 1) / W);
+    auto slot = [&](int c) { return (int64_t)(REV ? a.nc - 1 - c : c); };
+    float h = 0.f, total = 0.f, s[U], d[U];
+    auto walk = [&](bool write) {
+        for (int c = c0; c < c1; c += U) {
+            if (!write || c1 - c0 > U || W == 1) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int c = min(c0 + i, a.nc - 2);       // the last chunk in order has no slot to read
-            const int at = REV ? a.nc - 1 - c : c;
-            s[i] = S[at * cs];
-            d[i] = sd[at * ds];
-        }
+                for (int i = 0; i < U; ++i) {
+                    const int64_t at = slot(min(min(c + i, c1 - 1), a.nc - 2));
+                    s[i] = S[at * cs];
+                    d[i] = sd[at * ds];
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int c = c0 + i;
-            if (c < a.nc) {
-                S[(REV ? a.nc - 1 - c : c) * cs] = h;
-                h = fmaf(exp2_fast(A2 * d[i]), h, s[i]);
+            for (int i = 0; i < U; ++i) {
+                if (c + i < c1) {
+                    if (write) S[slot(c + i) * cs] = h;
+                    h = fmaf(exp2_fast(A2 * d[i]), h, s[i]);
+                    total += d[i];
+                }
             }
         }
+    };
+    if (W > 1) {
+        walk(false);
+        part[wave][0][lane] = h;
+        part[wave][1][lane] = total;
+        __syncthreads();
     }
+    h = first ? first[(b * a.D + q.d) * (int64_t)a.N + n] : 0.f;
+    for (int w = 0; w < wave; ++w) h = fmaf(exp2_fast(A2 * part[w][1][lane]), h, part[w][0][lane]);
+    walk(true);
 }
 
-// (3)
-template <typename T, int N>
+// (3); GATE: z is given
+template <typename T, int N, bool GATE>
 __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     int64_t b;
     int c, tt;
@@ -163,9 +186,9 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     auto token = [&](int t) { return hidden(min(t, end - 1)); };
     auto fetch = [&](int k, int slot) {
         const int t = token(k);
-        dv[slot] = row_of<T>(a.delta, b, t)[q.d];
-        uv[slot] = row_of<T>(a.u, b, t)[q.d];
-        if (a.z.p) zv[slot] = row_of<T>(a.z, b, t)[q.d];
+        dv[slot] = lane_load(row_of<T>(a.delta, b, t), q.d);
+        uv[slot] = lane_load(row_of<T>(a.u, b, t), q.d);
+        if (GATE) zv[slot] = lane_load(row_of<T>(a.z, b, t), q.d);
     };
     Uniform<T, 16> Bt, Ct, Bn, Cn;
     auto coefficients = [&](int k, int n0) {
@@ -178,41 +201,51 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
         for (int k = 0; k < kAhead; ++k) fetch(begin + k, k);
         coefficients(begin, 0);
     }
-    for (int t0 = begin; t0 < end; t0 += kKeep) {
-        if (a.keep) {
-            float *kp = a.keep + sel_keep_slot(a, b, t0 / kKeep, tt, 0);
+    auto step = [&](int t, int slot) {
+        float sig;
+        const float dt = sel_dt(to_f32(dv[slot]) + bias, softplus, &sig);
+        const float u = to_f32(uv[slot]), x = dt * u;
+        float acc[2] = {skip * u, 0.f};
+#pragma unroll
+        for (int n0 = 0; n0 < N; n0 += 16) {
+            Bt = Bn;
+            Ct = Cn;
+            if (n0 + 16 < N) coefficients(t, n0 + 16);
+            else coefficients(t + 1, 0);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                h[n0 + n] = fmaf(exp2_fast(dt * A2[n0 + n]), h[n0 + n], x * Bt[n]);
+                acc[n & 1] = fmaf(Ct[n], h[n0 + n], acc[n & 1]);
+            }
+        }
+        float o = acc[0] + acc[1];
+        if (GATE) o *= silu_f32(to_f32(zv[slot]));
+        if (q.live) lane_store(y + t * (int64_t)a.D, q.d, from_f32<T>(o));
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto keep_state = [&](int t) {
+        if (a.keep && t % kKeep == 0) {
+            float *kp = a.keep + sel_keep_slot(a, b, t / kKeep, tt, 0);
 #pragma unroll
             for (int n = 0; n < N; ++n) kp[n * 64] = h[n];
         }
+    };
+    static_assert(kKeep % kRing == 0, "states are kept between groups of kRing tokens");
+    int t0 = begin;
+    for (; t0 + kRing <= end; t0 += kRing) {
+        keep_state(t0);
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            if (t0 + i < end) {
-                fetch(t0 + i + kAhead, (i + kAhead) % kRing);
-                float sig;
-                const float dt = sel_dt(to_f32(dv[i % kRing]) + bias, softplus, &sig);
-                const float u = to_f32(uv[i % kRing]), x = dt * u;
-                float acc[2] = {skip * u, 0.f};
-#pragma unroll
-                for (int n0 = 0; n0 < N; n0 += 16) {
-                    Bt = Bn;
-                    Ct = Cn;
-                    if (n0 + 16 < N) coefficients(t0 + i, n0 + 16);
-                    else coefficients(t0 + i + 1, 0);
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        h[n0 + n] = fmaf(exp2_fast(dt * A2[n0 + n]), h[n0 + n], x * Bt[n]);
-                        acc[n & 1] = fmaf(Ct[n], h[n0 + n], acc[n & 1]);
-                    }
-                }
-                float o = acc[0] + acc[1];
-                if (a.z.p) o *= silu_f32(to_f32(zv[i % kRing]));
-                if (q.live) (y + (t0 + i) * (int64_t)a.D)[q.d] = from_f32<T>(o);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < kRing; ++i) {
+            fetch(t0 + i + kAhead, (i + kAhead) % kRing);
+            step(t0 + i, i);
         }
     }
+    if (t0 < end) keep_state(t0);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (t0 + i < end) step(t0 + i, i);
     if (q.live) {
-        for (int t = max(begin, end); t < stop; ++t) (y + t * (int64_t)a.D)[q.d] = from_f32<T>(0.f);
+        for (int t = max(begin, end); t < stop; ++t) lane_store(y + t * (int64_t)a.D, q.d, from_f32<T>(0.f));
         if (a.final_state && c == a.nc - 1) {
             float *f = a.final_state + (b * a.D + q.d) * (int64_t)N;
 #pragma unroll
@@ -261,10 +294,11 @@ __global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
 
 bool sel_supported(int64_t N) { return N == 16 || N == 32 || N == 64; }
 
-// Chunks so that about `target` waves run, of at least 16 tokens; one chunk where the waves of
-// a single pass already come to one for each of the 1024 SIMDs.
+// Chunks so that about `target` waves run, of at least 16 tokens.  One chunk, and so a single
+// pass, where its waves already come to two for each of the 1024 SIMDs: a pass with 2 waves a
+// SIMD takes 1.5 times one with 8, but the two passes over chunks take 1.8 times one.
 void sel_chunks(int64_t waves, int64_t target, int64_t L, int *nc, int *T) {
-    const int64_t n = waves >= 1024 ? 1 : (target + waves - 1) / waves;
+    const int64_t n = waves >= 2048 ? 1 : (target + waves - 1) / waves;
     int64_t t = (L + n - 1) / n;
     t = (t + kKeep - 1) / kKeep * kKeep;
     if (t < 16) t = 16;
@@ -280,10 +314,18 @@ static hipError_t sel_grid(int64_t units, uint32_t *blocks) {
 }
 
 hipError_t launch_sel_pass(const SelArgs &a, bool reverse, hipStream_t s) {
-    const int64_t n = (a.batch * a.G * a.tiles * a.N * 64 + 255) / 256;
+    const int64_t n = a.batch * a.G * a.tiles * a.N;
     if (n > INT32_MAX) return hipErrorInvalidValue;
-    if (reverse) sel_pass_kernel<true><<<(uint32_t)n, 256, 0, s>>>(a);
-    else sel_pass_kernel<false><<<(uint32_t)n, 256, 0, s>>>(a);
+#define SEL_PASS(W)                                                                        \
+    do {                                                                                   \
+        if (reverse) sel_pass_kernel<true, W><<<(uint32_t)n, 64 * W, 0, s>>>(a);           \
+        else sel_pass_kernel<false, W><<<(uint32_t)n, 64 * W, 0, s>>>(a);                  \
+    } while (0)
+    if (a.nc <= kPassChunks) SEL_PASS(1);
+    else if (a.nc <= 4 * kPassChunks) SEL_PASS(4);
+    else if (a.nc <= 8 * kPassChunks) SEL_PASS(8);
+    else SEL_PASS(16);
+#undef SEL_PASS
     return hipGetLastError();
 }
 
@@ -299,7 +341,8 @@ static hipError_t sel_fwd_t(const SelArgs &a, hipStream_t s) {
         if ((e = launch_sel_pass(a, false, s)) != hipSuccess) return e;
     }
     if ((e = sel_grid(per * a.nc, &blocks)) != hipSuccess) return e;
-    sel_scan_kernel<T, N><<<blocks, 256, 0, s>>>(a);
+    if (a.z.p) sel_scan_kernel<T, N, true><<<blocks, 256, 0, s>>>(a);
+    else sel_scan_kernel<T, N, false><<<blocks, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

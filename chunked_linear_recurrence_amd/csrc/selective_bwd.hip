@@ -75,15 +75,15 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     // dz and dD of a token, given its y without the skip term
     auto finish_z = [&](int t, float u, float r, float gz, float y) {
         dD = fmaf(r, u, dD);
-        if (GATE && q.live && t < end) out_row(a.dz, t)[q.d] = from_f32<T>(gz * fmaf(skip, u, y));
+        if (GATE && q.live && t < end) lane_store(out_row(a.dz, t), q.d, from_f32<T>(gz * fmaf(skip, u, y)));
     };
     // du and ddelta of a token, given q and sum A w (base-2 rates)
     auto finish_u = [&](int t, float dt, float u, float sig, float r, float qq, float dw) {
         const float dl = fmaf(dw, kLn2F, u * qq) * sig;
         if (q.live && t < end) {
             dbias += dl;
-            out_row(a.du, t)[q.d] = from_f32<T>(fmaf(dt, qq, skip * r));
-            out_row(a.ddelta, t)[q.d] = from_f32<T>(dl);
+            lane_store(out_row(a.du, t), q.d, from_f32<T>(fmaf(dt, qq, skip * r)));
+            lane_store(out_row(a.ddelta, t), q.d, from_f32<T>(dl));
         }
     };
     // r = dout silu(z) and dout d(silu)(z)
@@ -125,10 +125,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
         // The token after the group's last is a copy of an earlier one: `in` is 0 for it.
         auto fetch = [&](int i) {
             const int t = hidden(min(t0 + i, end - 1));
-            dv[i % 3] = row_of<T>(a.delta, b, t)[q.d];
-            uv[i % 3] = row_of<T>(a.u, b, t)[q.d];
-            dyv[i % 3] = row_of<T>(a.dy, b, t)[q.d];
-            if (GATE) zv[i % 3] = row_of<T>(a.z, b, t)[q.d];
+            dv[i % 3] = lane_load(row_of<T>(a.delta, b, t), q.d);
+            uv[i % 3] = lane_load(row_of<T>(a.u, b, t), q.d);
+            dyv[i % 3] = lane_load(row_of<T>(a.dy, b, t), q.d);
+            if (GATE) zv[i % 3] = lane_load(row_of<T>(a.z, b, t), q.d);
         };
         auto coefficients = [&](int i, Uniform<T, kSB> &B, Uniform<T, kSB> &C) {
             const int t = hidden(min(t0 + i, end - 1));
@@ -230,8 +230,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
                     for (int k = 0; k < 3; ++k) s[k] += tok[wave - nb + w][i][4 + k][lane];
                 const int t = min(t0 + i, end - 1);
                 float r, gz;
-                T dy1 = row_of<T>(a.dy, b, t)[q.d], z1 = dy1;
-                if (GATE) z1 = row_of<T>(a.z, b, t)[q.d];
+                T dy1 = lane_load(row_of<T>(a.dy, b, t), q.d), z1 = dy1;
+                if (GATE) z1 = lane_load(row_of<T>(a.z, b, t), q.d);
                 upstream(dy1, z1, i < m ? live : 0.f, &r, &gz);
                 finish_z(t0 + i, tok[wave][i][1][lane], r, gz, s[0]);
                 finish_u(t0 + i, tok[wave][i][0][lane], tok[wave][i][1][lane], tok[wave][i][2][lane], r, s[1], s[2]);
@@ -241,8 +241,9 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     }
     if (q.live) {
         for (int t = max(begin, end) + nb; t < stop; t += NB) {
-            out_row(a.du, t)[q.d] = out_row(a.ddelta, t)[q.d] = from_f32<T>(0.f);
-            if (GATE) out_row(a.dz, t)[q.d] = from_f32<T>(0.f);
+            lane_store(out_row(a.du, t), q.d, from_f32<T>(0.f));
+            lane_store(out_row(a.ddelta, t), q.d, from_f32<T>(0.f));
+            if (GATE) lane_store(out_row(a.dz, t), q.d, from_f32<T>(0.f));
         }
         if (c == 0 && a.dinit) {
             float *o = a.dinit + (b * a.D + q.d) * (int64_t)N + n0;

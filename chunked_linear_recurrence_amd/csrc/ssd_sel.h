@@ -51,9 +51,27 @@ __device__ __forceinline__ int hidden_lane(int v) {
 // A wave's tile: group, the lane's channel and its place in the [D] tensors.
 struct SelTile {
     int tt, g;
-    uint32_t d;          // unsigned: an address is a scalar row plus this, one vector register for all tensors
+    uint32_t d;
     bool live;
 };
+
+// Element d of a row.  The row's address is the same for all lanes and kept apart from the
+// lane's offset, so that the load or store takes a scalar base and one 32-bit vector offset
+// that serves all tensors, with no 64-bit vector arithmetic.
+template <typename T>
+__device__ __forceinline__ T *scalar_row(T *p) {
+    uint64_t a = (uint64_t)p;
+    asm volatile("" : "+s"(a));
+    return reinterpret_cast<T *>(a);
+}
+template <typename T>
+__device__ __forceinline__ T lane_load(const T *row, uint32_t d) {
+    return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(scalar_row(row)) + d * (uint32_t)sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ void lane_store(T *row, uint32_t d, T v) {
+    *reinterpret_cast<T *>(reinterpret_cast<char *>(scalar_row(row)) + d * (uint32_t)sizeof(T)) = v;
+}
 __device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int tt) {
     SelTile q;
     const int per = a.D / a.G;
