@@ -204,6 +204,8 @@ ssd_status_t sel_spans(const ssd_selective_dims_t &d, size_t out[6]) {
     for (int i = 0; i < 6; ++i) {
         if (!span(d.batch, bs[i], d.seqlen, ts[i], i == 3 || i == 4 ? gn : d.channels, e, &out[i]))
             return fail(SSD_ERR_BAD_SHAPE, "strides must be >= 0 and spans below 2^58 elements");
+        if (ts[i] > INT32_MAX / e)
+            return fail(SSD_ERR_UNSUPPORTED, "a token stride spans more than 2^31 bytes");
         if ((i == 3 || i == 4) && e == 2 && ((bs[i] | ts[i]) & 1))
             return fail(SSD_ERR_MISALIGNED, "bfloat16 B and C need even strides (4-byte rows)");
     }

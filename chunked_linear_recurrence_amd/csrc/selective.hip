@@ -52,8 +52,7 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     sel_rates<N>(a, q.d, 0, A2);
 #pragma unroll
     for (int n = 0; n < N; ++n) h[n] = 0.f;
-    const View &coef = REV ? a.C : a.B;
-    const View &val = REV ? a.dy : a.u;
+    const Rows<T> coef(REV ? a.C : a.B, b), val(REV ? a.dy : a.u, b), delta(a.delta, b), zr(a.z, b);
     const bool gate = REV && a.z.p;
     // Step k is token begin + k, or end - 1 - k backwards.  Activations are fetched kAhead steps
     // early into a ring, coefficients one block of 16 states early.
@@ -61,12 +60,12 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     auto token = [&](int k) { return hidden(REV ? end - 1 - min(k, end - begin - 1) : begin + min(k, end - begin - 1)); };
     auto fetch = [&](int k, int slot) {
         const int t = token(k);
-        dv[slot] = lane_load(row_of<T>(a.delta, b, t), q.d);
-        xv[slot] = lane_load(row_of<T>(val, b, t), q.d);
-        if (gate) zv[slot] = lane_load(row_of<T>(a.z, b, t), q.d);
+        dv[slot] = lane_load(delta.at(t), q.d);
+        xv[slot] = lane_load(val.at(t), q.d);
+        if (gate) zv[slot] = lane_load(zr.at(t), q.d);
     };
     Uniform<T, 16> cf, cn;
-    auto coefficients = [&](int k, int n0) { cn.load(row_of<T>(coef, b, token(k)) + q.g * N + n0); };
+    auto coefficients = [&](int k, int n0) { cn.load(coef.at(token(k)) + q.g * N + n0); };
     if (begin < end) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) fetch(k, k);
@@ -182,19 +181,20 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
 #pragma unroll
     for (int n = 0; n < N; ++n) h[n] = a.nc > 1 ? S[n * 64] : (h0 ? h0[n] : 0.f);
     T *y = reinterpret_cast<T *>(a.y) + b * a.L * (int64_t)a.D;
+    const Rows<T> delta(a.delta, b), u(a.u, b), z(a.z, b), B(a.B, b), C(a.C, b);
     T dv[kRing], uv[kRing], zv[kRing];
     auto token = [&](int t) { return hidden(min(t, end - 1)); };
     auto fetch = [&](int k, int slot) {
         const int t = token(k);
-        dv[slot] = lane_load(row_of<T>(a.delta, b, t), q.d);
-        uv[slot] = lane_load(row_of<T>(a.u, b, t), q.d);
-        if (GATE) zv[slot] = lane_load(row_of<T>(a.z, b, t), q.d);
+        dv[slot] = lane_load(delta.at(t), q.d);
+        uv[slot] = lane_load(u.at(t), q.d);
+        if (GATE) zv[slot] = lane_load(z.at(t), q.d);
     };
     Uniform<T, 16> Bt, Ct, Bn, Cn;
     auto coefficients = [&](int k, int n0) {
         const int t = token(k);
-        Bn.load(row_of<T>(a.B, b, t) + q.g * N + n0);
-        Cn.load(row_of<T>(a.C, b, t) + q.g * N + n0);
+        Bn.load(B.at(t) + q.g * N + n0);
+        Cn.load(C.at(t) + q.g * N + n0);
     };
     if (begin < end) {
 #pragma unroll
@@ -204,8 +204,8 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     auto step = [&](int t, int slot) {
         float sig;
         const float dt = sel_dt(to_f32(dv[slot]) + bias, softplus, &sig);
-        const float u = to_f32(uv[slot]), x = dt * u;
-        float acc[2] = {skip * u, 0.f};
+        const float ut = to_f32(uv[slot]), x = dt * ut;
+        float acc[2] = {skip * ut, 0.f};
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 16) {
             Bt = Bn;

@@ -63,8 +63,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
         carry[n] = a.nc > 1 ? S[n * 64] : (f0 ? f0[n] : 0.f);
         dA[n] = 0.f;
     }
+    const Rows<T> r_u(a.u, b), r_delta(a.delta, b), r_dy(a.dy, b), r_z(a.z, b), r_B(a.B, b), r_C(a.C, b);
     // row t of an output [batch, L, D]
-    auto out_row = [&](void *p, int t) { return reinterpret_cast<T *>(p) + (b * a.L + t) * a.D; };
+    const int64_t out_first = b * a.L * (int64_t)a.D;
+    auto out_row = [&](void *p, int t) { return reinterpret_cast<T *>(p) + out_first + (uint64_t)(uint32_t)t * (uint32_t)a.D; };
     // Reads of tok go by a lane index of their own, so that the values come back from LDS and
     // are not kept in registers from the way forward to the way back.
     const int back = hidden_lane(lane);
@@ -116,33 +118,39 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
         for (int n = 0; n < kSB; ++n) h[n] = kp[n * 64];
     };
 
-    for (int t0 = begin + (max(end - begin, 1) - 1) / K * K; t0 >= begin && t0 < end; t0 -= K) {
+    float h0[kSB], hn[kSB];
+    Uniform<T, kSB> Bt, Ct, Bn, Cn;
+    T dv[3], uv[3], dyv[3], zv[3];                          // tokens i, i + 1 and i + 2 of a group, by i mod 3
+    // A token past the row's last is a copy of an earlier one: `in` is 0 for it.
+    auto fetch = [&](int t0, int i) {
+        const int t = hidden(min(t0 + i, end - 1));
+        dv[i % 3] = lane_load(r_delta.at(t), q.d);
+        uv[i % 3] = lane_load(r_u.at(t), q.d);
+        dyv[i % 3] = lane_load(r_dy.at(t), q.d);
+        if (GATE) zv[i % 3] = lane_load(r_z.at(t), q.d);
+    };
+    auto coefficients = [&](int t0, int i, Uniform<T, kSB> &B, Uniform<T, kSB> &C) {
+        const int t = hidden(min(t0 + i, end - 1));
+        B.load(r_B.at(t) + g * N + n0);
+        C.load(r_C.at(t) + g * N + n0);
+    };
+    const int last = begin + (max(end - begin, 1) - 1) / K * K;
+    if (begin < end) {
+        kept_state(last, hn);
+        fetch(last, 0);
+        fetch(last, 1);
+    }
+    for (int t0 = last; t0 >= begin && t0 < end; t0 -= K) {
         const int m = min(K, end - t0);
-        float h0[kSB], hs[K][kSB];
-        kept_state(t0, h0);
-        Uniform<T, kSB> Bt, Ct, Bn, Cn;
-        T dv[3], uv[3], dyv[3], zv[3];                      // tokens i, i + 1 and i + 2, by i mod 3
-        // The token after the group's last is a copy of an earlier one: `in` is 0 for it.
-        auto fetch = [&](int i) {
-            const int t = hidden(min(t0 + i, end - 1));
-            dv[i % 3] = lane_load(row_of<T>(a.delta, b, t), q.d);
-            uv[i % 3] = lane_load(row_of<T>(a.u, b, t), q.d);
-            dyv[i % 3] = lane_load(row_of<T>(a.dy, b, t), q.d);
-            if (GATE) zv[i % 3] = lane_load(row_of<T>(a.z, b, t), q.d);
-        };
-        auto coefficients = [&](int i, Uniform<T, kSB> &B, Uniform<T, kSB> &C) {
-            const int t = hidden(min(t0 + i, end - 1));
-            B.load(row_of<T>(a.B, b, t) + g * N + n0);
-            C.load(row_of<T>(a.C, b, t) + g * N + n0);
-        };
+        float hs[K][kSB];
+#pragma unroll
+        for (int n = 0; n < kSB; ++n) h0[n] = hn[n];
         // Forward through the group: states, y, and dC's products.
-        fetch(0);
-        fetch(1);
-        coefficients(0, Bt, Ct);
+        coefficients(t0, 0, Bt, Ct);
 #pragma unroll
         for (int i = 0; i < K; ++i) {
-            if (i + 2 < K) fetch(i + 2);
-            if (i + 1 < K) coefficients(i + 1, Bn, Cn);
+            if (i + 2 < K) fetch(t0, i + 2);
+            if (i + 1 < K) coefficients(t0, i + 1, Bn, Cn);
             if (i > 0) column_read();
             const float in = i < m ? live : 0.f;
             float sig, r, gz, y = 0.f;
@@ -171,11 +179,17 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             __builtin_amdgcn_sched_barrier(0);
         }
         // And back: g, what follows from it, and dB's products.
-        coefficients(K - 1, Bt, Ct);
+        coefficients(t0, K - 1, Bt, Ct);
 #pragma unroll
         for (int i = K - 1; i >= 0; --i) {
-            if (i > 0) coefficients(i - 1, Bn, Cn);
+            if (i > 0) coefficients(t0, i - 1, Bn, Cn);
             if (i == 2) kept_state(hidden(t0), h0);         // again, now that later tokens' states are done with
+            if (i == 1) {                                   // what the next group starts with
+                const int tp = hidden(max(t0 - K, begin));
+                kept_state(tp, hn);
+                fetch(tp, 0);
+                fetch(tp, 1);
+            }
             column_read();
             const float dt = tok[wave][i][0][back], u = tok[wave][i][1][back], sig = tok[wave][i][2][back];
             const float r = tok[wave][i][3][back], x = dt * u;
@@ -190,6 +204,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
                 const float w = carry[n] * (i ? hs[i ? i - 1 : 0][n] : h0[n]);
                 dw = fmaf(w, A2[n], dw);
                 dA[n] = fmaf(w, dt, dA[n]);
+                pinned(dA[n]);
                 if ((n & 3) == 3) *reinterpret_cast<f32x4 *>(mine + (n - 3)) = p;
             }
             const float s = column_sum();
@@ -230,8 +245,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
                     for (int k = 0; k < 3; ++k) s[k] += tok[wave - nb + w][i][4 + k][lane];
                 const int t = min(t0 + i, end - 1);
                 float r, gz;
-                T dy1 = lane_load(row_of<T>(a.dy, b, t), q.d), z1 = dy1;
-                if (GATE) z1 = lane_load(row_of<T>(a.z, b, t), q.d);
+                T dy1 = lane_load(r_dy.at(t), q.d), z1 = dy1;
+                if (GATE) z1 = lane_load(r_z.at(t), q.d);
                 upstream(dy1, z1, i < m ? live : 0.f, &r, &gz);
                 finish_z(t0 + i, tok[wave][i][1][lane], r, gz, s[0]);
                 finish_u(t0 + i, tok[wave][i][0][lane], tok[wave][i][1][lane], tok[wave][i][2][lane], r, s[1], s[2]);

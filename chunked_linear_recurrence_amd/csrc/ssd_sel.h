@@ -48,6 +48,10 @@ __device__ __forceinline__ int hidden_lane(int v) {
     return v;
 }
 
+// Keeps a running sum where it is written: the compiler otherwise moves a chain of additions
+// whose result is used late past the branches in between, and holds all the terms until then.
+__device__ __forceinline__ void pinned(float &v) { asm volatile("" : "+v"(v)); }
+
 // A wave's tile: group, the lane's channel and its place in the [D] tensors.
 struct SelTile {
     int tt, g;
@@ -64,6 +68,18 @@ __device__ __forceinline__ T *scalar_row(T *p) {
     asm volatile("" : "+s"(a));
     return reinterpret_cast<T *>(a);
 }
+// The rows of one batch row of a view: token t at p + t * ts bytes (the host has checked that
+// ts fits), two scalar multiplications and two additions.
+template <typename T>
+struct Rows {
+    const char *p;
+    uint32_t ts;
+    __device__ __forceinline__ Rows(const View &v, int64_t b)
+        : p(reinterpret_cast<const char *>(v.p) + b * v.bs * (int64_t)sizeof(T)), ts((uint32_t)(v.ts * (int64_t)sizeof(T))) {}
+    __device__ __forceinline__ const T *at(int t) const {
+        return reinterpret_cast<const T *>(p + (uint64_t)(uint32_t)t * ts);
+    }
+};
 template <typename T>
 __device__ __forceinline__ T lane_load(const T *row, uint32_t d) {
     return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(scalar_row(row)) + d * (uint32_t)sizeof(T));
