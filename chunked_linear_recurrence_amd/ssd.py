@@ -463,29 +463,31 @@ def _activation(name, t, dim):
     return _DTYPE_CODE[t.dtype]
 
 
-class _On:
-    """The device and stream of one call: makes them current for its allocations and launches."""
+def _elsewhere(t, stream):
+    """The context in which a call on tensor t has to run, or None when it is the current one:
+    the given stream's, or t's device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors are on %s; every tensor must be on a CUDA device" % t.device)
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("the stream is on %s and the tensors are on %s" % (stream.device, t.device))
+        return torch.cuda.stream(stream)
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
-    def __init__(self, t, stream):
-        if t.device.type != "cuda":
-            raise ValueError("tensors are on %s; every tensor must be on a CUDA device" % t.device)
-        self.ctx = None
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError("the stream is on %s and the tensors are on %s" % (stream.device, t.device))
-            self.ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.device)
-        self.stream = stream
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return (self.stream if self.stream is not None else torch.cuda.current_stream()).cuda_stream
+def _current(t):
+    """The current stream of t's device as an integer.  (torch.cuda.current_stream builds a
+    Stream object: 2.7 us, where a single-token kernel takes 3.)"""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _out(name, t, shape, dtype, device):
+    """A caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _param(name, t, shape, device, dtype)
+    return t
 
 
 def _workspace(t, nbytes, device):
@@ -513,15 +515,17 @@ def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, 
     bp = _param("bias", bias, (C,), dev)
     ip = _param("init_state", init_state, (b, W - 1, C), dev, x.dtype)
     lp = _param("lengths", lengths, (b,), dev, torch.int32)
-    with _On(x, stream) as s:
-        if y is None:
-            y = torch.empty((b, L, C), dtype=x.dtype, device=dev)
-        if final_state is None and want_final and W > 1:
-            final_state = torch.empty((b, W - 1, C), dtype=x.dtype, device=dev)
-        dims = ConvDims(b, L, C, W, code, xb, xt, 0, 0)
-        _check(L_.ssd_conv_fwd(dims, xp, wp, bp, ip, lp, _param("y", y, (b, L, C), dev, x.dtype),
-                               _param("final_state", final_state, (b, W - 1, C), dev, x.dtype),
-                               SSD_FLAG_SILU if silu else 0, s))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return conv_fwd(x, weight, bias, init_state, lengths=lengths, silu=silu, y=y, final_state=final_state,
+                            want_final=want_final)
+    y = _out("y", y, (b, L, C), x.dtype, dev)
+    if final_state is not None or (want_final and W > 1):
+        final_state = _out("final_state", final_state, (b, W - 1, C), x.dtype, dev)
+    dims = ConvDims(b, L, C, W, code, xb, xt, 0, 0)
+    _check(L_.ssd_conv_fwd(dims, xp, wp, bp, ip, lp, y.data_ptr(), _ptr(final_state), SSD_FLAG_SILU if silu else 0,
+                           _current(x)))
     return y, final_state
 
 
@@ -538,12 +542,13 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stre
     bp = _param("bias", bias, (C,), dev)
     ip = _param("state", state, shape, dev, x.dtype)
     op = ip if state_out is None else _param("state_out", state_out, shape, dev, x.dtype)
-    with _On(x, stream) as s:
-        if y is None:
-            y = torch.empty((b, C), dtype=x.dtype, device=dev)
-        dims = ConvDims(b, 1, C, W, code, xb, 0, 0, 0)
-        _check(L_.ssd_conv_step(dims, xp, wp, bp, ip, op, _param("y", y, (b, C), dev, x.dtype),
-                                SSD_FLAG_SILU if silu else 0, s))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return conv_step(x, weight, bias, state, silu=silu, y=y, state_out=state_out)
+    y = _out("y", y, (b, C), x.dtype, dev)
+    dims = ConvDims(b, 1, C, W, code, xb, 0, 0, 0)
+    _check(L_.ssd_conv_step(dims, xp, wp, bp, ip, op, y.data_ptr(), SSD_FLAG_SILU if silu else 0, _current(x)))
     return y
 
 
@@ -572,14 +577,18 @@ def conv_bwd(dy, x, weight, bias=None, init_state=None, *, dfinal=None, lengths=
     fp = _param("dfinal", dfinal, st, dev, x.dtype)
     lp = _param("lengths", lengths, (b,), dev, torch.int32)
     dims = ConvDims(b, L, C, W, code, xb, xt, gb, gt)
-    with _On(x, stream) as s:
-        ws = _workspace(workspace, L_.ssd_conv_bwd_workspace_bytes(dims), dev)
-        g = ConvGrads(torch.empty((b, L, C), dtype=x.dtype, device=dev),
-                      torch.empty((C, W), dtype=torch.float32, device=dev),
-                      None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev),
-                      None if init_state is None else torch.empty(st, dtype=x.dtype, device=dev))
-        _check(L_.ssd_conv_bwd(dims, gp, xp, wp, bp, ip, fp, lp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias),
-                               _ptr(g.dinit), SSD_FLAG_SILU if silu else 0, ws.data_ptr(), ws.numel(), s))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return conv_bwd(dy, x, weight, bias, init_state, dfinal=dfinal, lengths=lengths, silu=silu,
+                            workspace=workspace)
+    ws = _workspace(workspace, L_.ssd_conv_bwd_workspace_bytes(dims), dev)
+    g = ConvGrads(torch.empty((b, L, C), dtype=x.dtype, device=dev),
+                  torch.empty((C, W), dtype=torch.float32, device=dev),
+                  None if bias is None else torch.empty((C,), dtype=torch.float32, device=dev),
+                  None if init_state is None else torch.empty(st, dtype=x.dtype, device=dev))
+    _check(L_.ssd_conv_bwd(dims, gp, xp, wp, bp, ip, fp, lp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias),
+                           _ptr(g.dinit), SSD_FLAG_SILU if silu else 0, ws.data_ptr(), ws.numel(), _current(x)))
     return g
 
 
@@ -619,16 +628,17 @@ def selective_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state
     dev, st = u.device, (b, d, B.shape[3])
     ip = _param("init_state", init_state, st, dev)
     lp = _param("lengths", lengths, (b,), dev, torch.int32)
-    with _On(u, stream) as s:
-        ws = _workspace(workspace, L_.ssd_selective_fwd_workspace_bytes(dims), dev)
-        if y is None:
-            y = torch.empty((b, L, d), dtype=u.dtype, device=dev)
-        if final_state is None:
-            final_state = torch.empty(st, dtype=torch.float32, device=dev)
-        kept = torch.empty(L_.ssd_selective_kept_bytes(dims), dtype=torch.uint8, device=dev) if keep else None
-        _check(L_.ssd_selective_fwd(dims, *ptrs, ip, lp, _param("y", y, (b, L, d), dev, u.dtype),
-                                    _param("final_state", final_state, st, dev), _ptr(kept),
-                                    SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), s))
+    ctx = _elsewhere(u, stream)
+    if ctx is not None:
+        with ctx:
+            return selective_fwd(u, delta, A, B, C, D, z, delta_bias, init_state, lengths=lengths, softplus=softplus,
+                                 y=y, final_state=final_state, keep=keep, workspace=workspace)
+    ws = _workspace(workspace, L_.ssd_selective_fwd_workspace_bytes(dims), dev)
+    y = _out("y", y, (b, L, d), u.dtype, dev)
+    final_state = _out("final_state", final_state, st, torch.float32, dev)
+    kept = torch.empty(L_.ssd_selective_kept_bytes(dims), dtype=torch.uint8, device=dev) if keep else None
+    _check(L_.ssd_selective_fwd(dims, *ptrs, ip, lp, y.data_ptr(), final_state.data_ptr(), _ptr(kept),
+                                SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), _current(u)))
     return (y, final_state, kept) if keep else (y, final_state)
 
 
@@ -642,11 +652,14 @@ def selective_step(u, delta, A, B, C, D, z, delta_bias, state, *, softplus=True,
     dev, st = u.device, (b, d, B.shape[2])
     ip = _param("state", state, st, dev)
     op = ip if state_out is None else _param("state_out", state_out, st, dev)
-    with _On(u, stream) as s:
-        if y is None:
-            y = torch.empty((b, d), dtype=u.dtype, device=dev)
-        _check(L_.ssd_selective_step(dims, *ptrs, ip, op, _param("y", y, (b, d), dev, u.dtype),
-                                     SSD_FLAG_SOFTPLUS if softplus else 0, s))
+    ctx = _elsewhere(u, stream)
+    if ctx is not None:
+        with ctx:
+            return selective_step(u, delta, A, B, C, D, z, delta_bias, state, softplus=softplus, y=y,
+                                  state_out=state_out)
+    y = _out("y", y, (b, d), u.dtype, dev)
+    _check(L_.ssd_selective_step(dims, *ptrs, ip, op, y.data_ptr(), SSD_FLAG_SOFTPLUS if softplus else 0,
+                                 _current(u)))
     return y
 
 
@@ -675,20 +688,24 @@ def selective_bwd(dy, u, delta, A, B, C, D, z, delta_bias, kept, *, dfinal=None,
     fp = _param("dfinal", dfinal, (b, d, N), dev)
     lp = _param("lengths", lengths, (b,), dev, torch.int32)
     kp = _param("kept", kept, (L_.ssd_selective_kept_bytes(dims),), dev, torch.uint8)
-    with _On(u, stream) as s:
-        ws = _workspace(workspace, L_.ssd_selective_bwd_workspace_bytes(dims), dev)
+    ctx = _elsewhere(u, stream)
+    if ctx is not None:
+        with ctx:
+            return selective_bwd(dy, u, delta, A, B, C, D, z, delta_bias, kept, dfinal=dfinal, lengths=lengths,
+                                 softplus=softplus, workspace=workspace)
+    ws = _workspace(workspace, L_.ssd_selective_bwd_workspace_bytes(dims), dev)
 
-        def act(*shape):
-            return torch.empty(shape, dtype=u.dtype, device=dev)
+    def act(*shape):
+        return torch.empty(shape, dtype=u.dtype, device=dev)
 
-        def f32(*shape):
-            return torch.empty(shape, dtype=torch.float32, device=dev)
-        g = SelectiveGrads(act(b, L, d), act(b, L, d), f32(d, N), act(b, L, G, N), act(b, L, G, N),
-                           None if D is None else f32(d), None if z is None else act(b, L, d),
-                           None if delta_bias is None else f32(d), f32(b, d, N))
-        _check(L_.ssd_selective_bwd(dims, gp, *ptrs, kp, fp, lp, _ptr(g.du), _ptr(g.ddelta), _ptr(g.dA), _ptr(g.dB),
-                                    _ptr(g.dC), _ptr(g.dD), _ptr(g.dz), _ptr(g.ddelta_bias), _ptr(g.dinit),
-                                    SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), s))
+    def f32(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=dev)
+    g = SelectiveGrads(act(b, L, d), act(b, L, d), f32(d, N), act(b, L, G, N), act(b, L, G, N),
+                       None if D is None else f32(d), None if z is None else act(b, L, d),
+                       None if delta_bias is None else f32(d), f32(b, d, N))
+    _check(L_.ssd_selective_bwd(dims, gp, *ptrs, kp, fp, lp, _ptr(g.du), _ptr(g.ddelta), _ptr(g.dA), _ptr(g.dB),
+                                _ptr(g.dC), _ptr(g.dD), _ptr(g.dz), _ptr(g.ddelta_bias), _ptr(g.dinit),
+                                SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), _current(u)))
     return g
 
 
@@ -702,16 +719,17 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, want_stats=False, s
     xp, xs, _ = _rows("x", x, (rows, d), x)
     wp = _param("weight", weight, (d,), dev)
     bp = _param("bias", bias, (d,), dev)
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return norm_fwd(x, weight, bias, eps, y=y, want_stats=want_stats)
+    y = _out("y", y, (rows, d), x.dtype, dev)
     mean = rstd = None
-    with _On(x, stream) as s:
-        if y is None:
-            y = torch.empty((rows, d), dtype=x.dtype, device=dev)
-        if want_stats:
-            mean = torch.empty((rows,), dtype=torch.float32, device=dev)
-            rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
-        dims = NormDims(rows, d, code, 0, xs, 0)
-        _check(L_.ssd_norm_fwd(dims, xp, wp, bp, eps, _param("y", y, (rows, d), dev, x.dtype), _ptr(mean), _ptr(rstd),
-                               s))
+    if want_stats:
+        mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    dims = NormDims(rows, d, code, 0, xs, 0)
+    _check(L_.ssd_norm_fwd(dims, xp, wp, bp, eps, y.data_ptr(), _ptr(mean), _ptr(rstd), _current(x)))
     return (y, mean, rstd) if want_stats else y
 
 
@@ -733,11 +751,14 @@ def norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
     mp = _param("mean", mean, (rows,), dev)
     rp = _param("rstd", rstd, (rows,), dev)
     dims = NormDims(rows, d, code, 0, xs, gs)
-    with _On(x, stream) as s:
-        ws = _workspace(workspace, L_.ssd_norm_bwd_workspace_bytes(dims), dev)
-        g = NormGrads(torch.empty((rows, d), dtype=x.dtype, device=dev),
-                      torch.empty((d,), dtype=torch.float32, device=dev),
-                      torch.empty((d,), dtype=torch.float32, device=dev))
-        _check(L_.ssd_norm_bwd(dims, gp, xp, wp, mp, rp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias), ws.data_ptr(),
-                               ws.numel(), s))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return norm_bwd(dy, x, weight, mean, rstd, workspace=workspace)
+    ws = _workspace(workspace, L_.ssd_norm_bwd_workspace_bytes(dims), dev)
+    g = NormGrads(torch.empty((rows, d), dtype=x.dtype, device=dev),
+                  torch.empty((d,), dtype=torch.float32, device=dev),
+                  torch.empty((d,), dtype=torch.float32, device=dev))
+    _check(L_.ssd_norm_bwd(dims, gp, xp, wp, mp, rp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias), ws.data_ptr(),
+                           ws.numel(), _current(x)))
     return g
