@@ -117,7 +117,7 @@ ssd::ConvArgs conv_args(const ssd_conv_dims_t &d, const void *x, const float *w,
 
 size_t conv_ws(const ssd_conv_dims_t &d) {
     int64_t n;
-    if (!product({ssd::conv_bwd_rows(d.batch, d.seqlen), d.width + 1, d.channels, 4}, &n)) return 0;
+    if (!product({ssd::conv_bwd_rows(d.batch, d.seqlen, d.channels, d.dtype), d.width + 1, d.channels, 4}, &n)) return 0;
     return align_up((size_t)n);
 }
 

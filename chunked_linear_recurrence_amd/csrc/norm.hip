@@ -17,12 +17,25 @@
 
 namespace ssd {
 
-constexpr int kNormBwdBlocks = 512;   // workgroups (rows of partial sums) of the backward at most
+constexpr int kNormBwdBlocks = 512;    // workgroups (rows of partial sums) of the backward at most
+constexpr int kNormFwdBlocks = 1024;   // workgroups of 4 waves of the forward at most
 
+// Sum over the 64 lanes, the same in every lane: 4 steps within rows of 16 lanes on the vector
+// units' own lane permutations, then the 4 rows' sums by way of scalar registers.  (Shuffles
+// through LDS wait for it at each of 6 steps.)
+template <int CTRL>
+__device__ __forceinline__ float permuted(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    v += permuted<0xb1>(v);       // lanes 1 apart
+    v += permuted<0x4e>(v);       // 2 apart
+    v += permuted<0x141>(v);      // the other 4 of 8, mirrored
+    v += permuted<0x140>(v);      // the other 8 of 16, mirrored
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
 // Sums over the WPR waves that share a row (WPR > 1: every wave of the workgroup).
@@ -42,6 +55,7 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 }
 
 template <int WPR> constexpr int norm_threads() { return WPR == 16 ? 1024 : 256; }
+template <int WPR> constexpr bool norm_ahead() { return WPR < 16; }           // 1024 threads leave 128 registers each
 template <int WPR> constexpr int norm_rows() { return WPR == 1 ? 4 : 1; }     // rows a workgroup holds at a time
 
 template <typename T, int V>
@@ -56,53 +70,74 @@ __device__ __forceinline__ void load_param(const float *p, int c, float none, fl
     for (int i = 0; i < V; ++i) v[i] = p ? p[c + i] : none;
 }
 
+// A row's K accesses of this thread; those past the row are left alone.
+template <typename T, int V, int K, int WPR>
+__device__ __forceinline__ void load_row(const T *x, int D, int tid, typename Pack<T, V>::type (&v)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (k * 64 * WPR + tid) * V;
+        if (c < D) v[k] = *reinterpret_cast<const typename Pack<T, V>::type *>(x + c);
+    }
+}
+
+// A workgroup walks many rows with weight and bias in registers (read per row they are four
+// times a bfloat16 row's own traffic) and, where registers allow, the next row on its way while
+// one is reduced: 32768 rows of 2048 channels take 50 us (5.4 TB/s), against 71 with a row a
+// wave.
 template <typename T, int V, int K, int WPR>
 __global__ __launch_bounds__(norm_threads<WPR>()) void norm_fwd_kernel(NormArgs a) {
     __shared__ float red[16];
     typedef typename Pack<T, V>::type P;
-    const int64_t row = (int64_t)blockIdx.x * norm_rows<WPR>() + (WPR == 1 ? threadIdx.x / 64 : 0);
-    if (WPR == 1 && row >= a.rows) return;
+    constexpr int R = norm_rows<WPR>();
     const int tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
-    const T *x = reinterpret_cast<const T *>(a.x) + row * a.x_stride;
-    P v[K];
-    float s = 0.f;
+    const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? threadIdx.x / 64 : 0), by = (int64_t)gridDim.x * R;
+    const T *x = reinterpret_cast<const T *>(a.x);
+    P v[K] = {}, next[K] = {};
+    if (first < a.rows) load_row<T, V, K, WPR>(x + first * a.x_stride, a.D, tid, next);
+    float w[K][V], b[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * 64 * WPR + tid) * V;
-        if (c < a.D) {
-            v[k] = *reinterpret_cast<const P *>(x + c);
-#pragma unroll
-            for (int i = 0; i < V; ++i) s += pick<T, V>(v[k], i);
-        }
+        load_param<V>(c < a.D ? a.w : nullptr, c, 1.f, w[k]);
+        load_param<V>(c < a.D ? a.bias : nullptr, c, 0.f, b[k]);
     }
-    const float mean = row_sum<WPR>(s, red) / a.D;
-    s = 0.f;
+    for (int64_t row = first; row < a.rows; row += by) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        if ((k * 64 * WPR + tid) * V < a.D)
+        for (int k = 0; k < K; ++k) v[k] = next[k];
+        if (norm_ahead<WPR>() && row + by < a.rows) load_row<T, V, K, WPR>(x + (row + by) * a.x_stride, a.D, tid, next);
+        float s = 0.f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = pick<T, V>(v[k], i) - mean;
-                s = fmaf(d, d, s);
+        for (int k = 0; k < K; ++k)
+            if ((k * 64 * WPR + tid) * V < a.D)
+#pragma unroll
+                for (int i = 0; i < V; ++i) s += pick<T, V>(v[k], i);
+        const float mean = row_sum<WPR>(s, red) / a.D;
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if ((k * 64 * WPR + tid) * V < a.D)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float d = pick<T, V>(v[k], i) - mean;
+                    s = fmaf(d, d, s);
+                }
+        const float rstd = 1.f / sqrtf(row_sum<WPR>(s, red) / a.D + a.eps);
+        T *y = reinterpret_cast<T *>(a.y) + row * a.D;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * 64 * WPR + tid) * V;
+            if (c < a.D) {
+                float o[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaf((pick<T, V>(v[k], i) - mean) * rstd, w[k][i], b[k][i]);
+                store_f32<T, V>(y + c, o);
             }
-    }
-    const float rstd = 1.f / sqrtf(row_sum<WPR>(s, red) / a.D + a.eps);
-    T *y = reinterpret_cast<T *>(a.y) + row * a.D;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (k * 64 * WPR + tid) * V;
-        if (c < a.D) {
-            float w[V], b[V], o[V];
-            load_param<V>(a.w, c, 1.f, w);
-            load_param<V>(a.bias, c, 0.f, b);
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaf((pick<T, V>(v[k], i) - mean) * rstd, w[i], b[i]);
-            store_f32<T, V>(y + c, o);
         }
-    }
-    if (tid == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
+        if (tid == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        if (!norm_ahead<WPR>() && row + by < a.rows) load_row<T, V, K, WPR>(x + (row + by) * a.x_stride, a.D, tid, next);
     }
 }
 
@@ -148,20 +183,26 @@ __global__ __launch_bounds__(norm_threads<WPR>()) void norm_bwd_kernel(NormArgs 
             w[k][i] = (a.w && c < a.D) ? a.w[c + i] : 1.f;
         }
     }
-    for (int64_t row = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0); row < a.rows; row += (int64_t)gridDim.x * R) {
-        const T *x = reinterpret_cast<const T *>(a.x) + row * a.x_stride;
-        const T *dy = reinterpret_cast<const T *>(a.dy) + row * a.dy_stride;
-        const float mean = a.mean[row], rstd = a.rstd[row];
-        P xv[K], gv[K];
-        float s1 = 0.f, s2 = 0.f;
+    const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
+    const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0), by = (int64_t)gridDim.x * R;
+    P xv[K] = {}, gv[K] = {}, xn[K] = {}, gn[K] = {};
+    float mean_n = 0.f, rstd_n = 0.f;
+    auto fetch = [&](int64_t row) {
+        load_row<T, V, K, WPR>(x + row * a.x_stride, a.D, tid, xn);
+        load_row<T, V, K, WPR>(dy + row * a.dy_stride, a.D, tid, gn);
+        mean_n = a.mean[row];
+        rstd_n = a.rstd[row];
+    };
+    if (first < a.rows) fetch(first);
+    for (int64_t row = first; row < a.rows; row += by) {
+        const float mean = mean_n, rstd = rstd_n;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * 64 * WPR + tid) * V;
-            if (c < a.D) {
-                xv[k] = *reinterpret_cast<const P *>(x + c);
-                gv[k] = *reinterpret_cast<const P *>(dy + c);
-            }
+            xv[k] = xn[k];
+            gv[k] = gn[k];
         }
+        if (norm_ahead<WPR>() && row + by < a.rows) fetch(row + by);
+        float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if ((k * 64 * WPR + tid) * V < a.D)
@@ -190,6 +231,7 @@ __global__ __launch_bounds__(norm_threads<WPR>()) void norm_bwd_kernel(NormArgs 
                 store_f32<T, V>(dx + c, o);
             }
         }
+        if (!norm_ahead<WPR>() && row + by < a.rows) fetch(row + by);
     }
     float *part = a.part + (int64_t)blockIdx.x * 2 * a.D;
     if constexpr (WPR == 1) {
@@ -283,9 +325,9 @@ int64_t norm_bwd_blocks(int64_t rows, int64_t D) { return rows < kNormBwdBlocks 
 
 template <typename T, int V, int K, int WPR>
 static hipError_t norm_fwd_t(const NormArgs &a, hipStream_t s) {
-    constexpr int R = norm_rows<WPR>();
-    const int64_t n = (a.rows + R - 1) / R;
-    if (n > INT32_MAX) return hipErrorInvalidValue;
+    constexpr int R = norm_rows<WPR>(), cap = kNormFwdBlocks / (WPR == 16 ? 4 : 1);
+    int64_t n = (a.rows + R - 1) / R;
+    if (n > cap) n = cap;
     norm_fwd_kernel<T, V, K, WPR><<<(uint32_t)n, norm_threads<WPR>(), 0, s>>>(a);
     return hipGetLastError();
 }
@@ -337,7 +379,6 @@ static bool at16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
         if (a.D <= 256 * V * 2) return norm_##DIR##_t<T, V, 2, 4>(a, s);           \
         if (a.D <= 256 * V * 4) return norm_##DIR##_t<T, V, 4, 4>(a, s);           \
         if (a.D <= 1024 * V * 2) return norm_##DIR##_t<T, V, 2, 16>(a, s);         \
-        if (a.D <= 1024 * V * 4) return norm_##DIR##_t<T, V, 4, 16>(a, s);         \
     } while (0)
 #define NORM_ONE(DIR, T)                                                           \
     do {                                                                           \

@@ -39,7 +39,7 @@ struct ConvArgs {
 hipError_t launch_conv_fwd(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_step(const ConvArgs &a, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs &a, hipStream_t s);
-int64_t conv_bwd_rows(int64_t batch, int64_t L);
+int64_t conv_bwd_rows(int64_t batch, int64_t L, int64_t C, int32_t dtype);
 bool conv_supported(int W);
 
 struct NormArgs {
@@ -137,8 +137,11 @@ struct Pack<T, 1> {
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void load_f32(const T *p, float (&v)[V]) {
-    const auto q = *reinterpret_cast<const typename Pack<T, V>::type *>(p);
+__device__ __forceinline__ typename Pack<T, V>::type load_pack(const T *p) {
+    return *reinterpret_cast<const typename Pack<T, V>::type *>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const typename Pack<T, V>::type &q, float (&v)[V]) {
     if constexpr (V == 1) v[0] = to_f32(q);
     else {
 #pragma unroll
