@@ -63,10 +63,12 @@ struct SelTile {
 // lane's offset, so that the load or store takes a scalar base and one 32-bit vector offset
 // that serves all tensors, with no 64-bit vector arithmetic.
 template <typename T>
-__device__ __forceinline__ T *scalar_row(T *p) {
-    uint64_t a = (uint64_t)p;
+using Global = __attribute__((address_space(1))) T;
+template <typename T>
+__device__ __forceinline__ Global<T> *lane_address(T *row, uint32_t d) {
+    uint64_t a = (uint64_t)row;
     asm volatile("" : "+s"(a));
-    return reinterpret_cast<T *>(a);
+    return (Global<T> *)((Global<char> *)a + d * (uint32_t)sizeof(T));
 }
 // The rows of one batch row of a view: token t at p + t * ts bytes (the host has checked that
 // ts fits), two scalar multiplications and two additions.
@@ -82,11 +84,11 @@ struct Rows {
 };
 template <typename T>
 __device__ __forceinline__ T lane_load(const T *row, uint32_t d) {
-    return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(scalar_row(row)) + d * (uint32_t)sizeof(T));
+    return *lane_address(row, d);
 }
 template <typename T>
 __device__ __forceinline__ void lane_store(T *row, uint32_t d, T v) {
-    *reinterpret_cast<T *>(reinterpret_cast<char *>(scalar_row(row)) + d * (uint32_t)sizeof(T)) = v;
+    *lane_address(row, d) = v;
 }
 __device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int tt) {
     SelTile q;
