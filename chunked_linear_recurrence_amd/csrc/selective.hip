@@ -37,7 +37,8 @@ __device__ __forceinline__ bool sel_unit(const SelArgs &a, int nchunks, int64_t 
 
 // (1), and its mirror for the backward (REV): the carry a_t g_t that leaves the chunk's first
 // token when none enters at its end, g_t = C_t r_t + a_{t+1} g_{t+1}.
-template <typename T, int N, bool REV>
+// GATE (with REV): z is given.
+template <typename T, int N, bool REV, bool GATE>
 __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     int64_t b;
     int c, tt;
@@ -47,22 +48,22 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     const int len = row_length(a.lengths, b, a.L);
     const int begin = c * a.T, end = min(begin + a.T, len);
     const bool softplus = (a.flags & SSD_FLAG_SOFTPLUS) != 0;
-    const float bias = a.bias ? a.bias[q.d] : 0.f;
-    float A2[N], h[N], sum = 0.f;
-    sel_rates<N>(a, q.d, 0, A2);
+    const float bias2 = a.bias ? a.bias[q.d] * kLog2eF : 0.f;
+    float A[N], h[N], sum = 0.f;
+    sel_rates<N>(a, q.d, 0, 1.f, A);
 #pragma unroll
     for (int n = 0; n < N; ++n) h[n] = 0.f;
     const Rows<T> coef(REV ? a.C : a.B, b), val(REV ? a.dy : a.u, b), delta(a.delta, b), zr(a.z, b);
-    const bool gate = REV && a.z.p;
     // Step k is token begin + k, or end - 1 - k backwards.  Activations are fetched kAhead steps
     // early into a ring, coefficients one block of 16 states early.
     T dv[kRing], xv[kRing], zv[kRing];
     auto token = [&](int k) { return hidden(REV ? end - 1 - min(k, end - begin - 1) : begin + min(k, end - begin - 1)); };
+    uint32_t d = q.d;
     auto fetch = [&](int k, int slot) {
         const int t = token(k);
-        dv[slot] = lane_load(delta.at(t), q.d);
-        xv[slot] = lane_load(val.at(t), q.d);
-        if (gate) zv[slot] = lane_load(zr.at(t), q.d);
+        dv[slot] = lane_load(delta.at(t), d);
+        xv[slot] = lane_load(val.at(t), d);
+        if (GATE) zv[slot] = lane_load(zr.at(t), d);
     };
     Uniform<T, 16> cf, cn;
     auto coefficients = [&](int k, int n0) { cn.load(coef.at(token(k)) + q.g * N + n0); };
@@ -72,12 +73,11 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
         coefficients(0, 0);
     }
     auto step = [&](int k, int slot) {
-        float sig;
-        const float dt = sel_dt(to_f32(dv[slot]) + bias, softplus, &sig);
-        sum += dt;
+        const float dt2 = sel_dt2(to_f32(dv[slot]), bias2, softplus);
+        sum += dt2;
         float x = to_f32(xv[slot]);
-        if (!REV) x *= dt;
-        else if (gate) x *= silu_f32(to_f32(zv[slot]));
+        if (!REV) x = dt2 * (x * kLn2F);
+        else if (GATE) x *= silu_f32(to_f32(zv[slot]));
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 16) {
             cf = cn;
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
             else coefficients(k + 1, 0);
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-                const float e = exp2_fast(dt * A2[n0 + n]);
+                const float e = exp2_fast(dt2 * A[n0 + n]);
                 h[n0 + n] = REV ? e * fmaf(x, cf[n], h[n0 + n]) : fmaf(e, h[n0 + n], x * cf[n]);
             }
         }
@@ -94,6 +94,7 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     const int steps = max(end - begin, 0);
     int k0 = 0;
     for (; k0 + kRing <= steps; k0 += kRing) {
+        d = hidden_lane(d);      // known to be 32 bits here: a scalar base and a vector offset, no 64-bit sum
 #pragma unroll
         for (int i = 0; i < kRing; ++i) {
             fetch(k0 + i + kAhead, (i + kAhead) % kRing);
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
     const int n = blockIdx.x % a.N, tt = blockIdx.x / a.N % ntt;
     const int64_t b = blockIdx.x / a.N / ntt;
     const SelTile q = sel_tile(a, tt);
-    const float A2 = a.A[(int64_t)q.d * a.N + n] * kLog2eF;
+    const float A = a.A[(int64_t)q.d * a.N + n];
     const float *first = REV ? a.dfinal : a.init;
     const int64_t cs = (int64_t)ntt * a.N * 64, ds = (int64_t)ntt * 64;
     float *S = a.S + ((b * a.nc * ntt + tt) * (int64_t)a.N + n) * 64 + lane;
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
             for (int i = 0; i < U; ++i) {
                 if (c + i < c1) {
                     if (write) S[slot(c + i) * cs] = h;
-                    h = fmaf(exp2_fast(A2 * d[i]), h, s[i]);
+                    h = fmaf(exp2_fast(A * d[i]), h, s[i]);
                     total += d[i];
                 }
             }
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
         __syncthreads();
     }
     h = first ? first[(b * a.D + q.d) * (int64_t)a.N + n] : 0.f;
-    for (int w = 0; w < wave; ++w) h = fmaf(exp2_fast(A2 * part[w][1][lane]), h, part[w][0][lane]);
+    for (int w = 0; w < wave; ++w) h = fmaf(exp2_fast(A * part[w][1][lane]), h, part[w][0][lane]);
     walk(true);
 }
 
@@ -173,9 +174,9 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     const int len = row_length(a.lengths, b, a.L);
     const int begin = c * a.T, stop = min(begin + a.T, a.L), end = min(stop, len);
     const bool softplus = (a.flags & SSD_FLAG_SOFTPLUS) != 0;
-    const float bias = a.bias ? a.bias[q.d] : 0.f, skip = a.Dskip ? a.Dskip[q.d] : 0.f;
-    float A2[N], h[N];
-    sel_rates<N>(a, q.d, 0, A2);
+    const float bias2 = a.bias ? a.bias[q.d] * kLog2eF : 0.f, skip = a.Dskip ? a.Dskip[q.d] : 0.f;
+    float A[N], h[N];
+    sel_rates<N>(a, q.d, 0, 1.f, A);
     const float *S = a.S + sel_slot(a, b, c, tt, N);
     const float *h0 = a.init ? a.init + (b * a.D + q.d) * (int64_t)N : nullptr;
 #pragma unroll
@@ -184,11 +185,12 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     const Rows<T> delta(a.delta, b), u(a.u, b), z(a.z, b), B(a.B, b), C(a.C, b);
     T dv[kRing], uv[kRing], zv[kRing];
     auto token = [&](int t) { return hidden(min(t, end - 1)); };
+    uint32_t d = q.d;
     auto fetch = [&](int k, int slot) {
         const int t = token(k);
-        dv[slot] = lane_load(delta.at(t), q.d);
-        uv[slot] = lane_load(u.at(t), q.d);
-        if (GATE) zv[slot] = lane_load(z.at(t), q.d);
+        dv[slot] = lane_load(delta.at(t), d);
+        uv[slot] = lane_load(u.at(t), d);
+        if (GATE) zv[slot] = lane_load(z.at(t), d);
     };
     Uniform<T, 16> Bt, Ct, Bn, Cn;
     auto coefficients = [&](int k, int n0) {
@@ -202,9 +204,8 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
         coefficients(begin, 0);
     }
     auto step = [&](int t, int slot) {
-        float sig;
-        const float dt = sel_dt(to_f32(dv[slot]) + bias, softplus, &sig);
-        const float ut = to_f32(uv[slot]), x = dt * ut;
+        const float dt2 = sel_dt2(to_f32(dv[slot]), bias2, softplus);
+        const float ut = to_f32(uv[slot]), x = dt2 * (ut * kLn2F);
         float acc[2] = {skip * ut, 0.f};
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 16) {
@@ -214,13 +215,13 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
             else coefficients(t + 1, 0);
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-                h[n0 + n] = fmaf(exp2_fast(dt * A2[n0 + n]), h[n0 + n], x * Bt[n]);
+                h[n0 + n] = fmaf(exp2_fast(dt2 * A[n0 + n]), h[n0 + n], x * Bt[n]);
                 acc[n & 1] = fmaf(Ct[n], h[n0 + n], acc[n & 1]);
             }
         }
         float o = acc[0] + acc[1];
         if (GATE) o *= silu_f32(to_f32(zv[slot]));
-        if (q.live) lane_store(y + t * (int64_t)a.D, q.d, from_f32<T>(o));
+        lane_store(y + t * (int64_t)a.D, d, from_f32<T>(o));      // an idle lane: the same value in the same place
         __builtin_amdgcn_sched_barrier(0);
     };
     auto keep_state = [&](int t) {
@@ -233,6 +234,7 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
     static_assert(kKeep % kRing == 0, "states are kept between groups of kRing tokens");
     int t0 = begin;
     for (; t0 + kRing <= end; t0 += kRing) {
+        d = hidden_lane(d);
         keep_state(t0);
 #pragma unroll
         for (int i = 0; i < kRing; ++i) {
@@ -271,15 +273,14 @@ __global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
     const float *A = a.A + (int64_t)d * N + n0;
     const f32x4 s = *reinterpret_cast<const f32x4 *>(a.state_in + k * N + n0);
     const float u = to_f32(reinterpret_cast<const T *>(a.u)[b * a.u_bs + d]);
-    float sig;
-    const float dt = sel_dt(to_f32(reinterpret_cast<const T *>(a.delta)[b * a.delta_bs + d]) +
-                            (a.bias ? a.bias[d] : 0.f), softplus, &sig);
-    const float x = dt * u;
+    const float dt2 = sel_dt2(to_f32(reinterpret_cast<const T *>(a.delta)[b * a.delta_bs + d]),
+                              a.bias ? a.bias[d] * kLog2eF : 0.f, softplus);
+    const float x = dt2 * (u * kLn2F);
     f32x4 h;
     float part = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(exp2_fast(dt * (A[i] * kLog2eF)), s[i], x * to_f32(Bp[i]));
+        h[i] = fmaf(exp2_fast(dt2 * A[i]), s[i], x * to_f32(Bp[i]));
         part = fmaf(to_f32(Cp[i]), h[i], part);
     }
     *reinterpret_cast<f32x4 *>(a.state_out + k * N + n0) = h;
@@ -336,7 +337,7 @@ static hipError_t sel_fwd_t(const SelArgs &a, hipStream_t s) {
     hipError_t e;
     if (a.nc > 1) {
         if ((e = sel_grid(per * (a.nc - 1), &blocks)) != hipSuccess) return e;
-        sel_local_kernel<T, N, false><<<blocks, 256, 0, s>>>(a);
+        sel_local_kernel<T, N, false, false><<<blocks, 256, 0, s>>>(a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if ((e = launch_sel_pass(a, false, s)) != hipSuccess) return e;
     }
@@ -359,7 +360,8 @@ static hipError_t sel_rev_t(const SelArgs &a, hipStream_t s) {
     uint32_t blocks;
     hipError_t e = sel_grid(a.batch * a.G * a.tiles * (a.nc - 1), &blocks);
     if (e != hipSuccess) return e;
-    sel_local_kernel<T, N, true><<<blocks, 256, 0, s>>>(a);
+    if (a.z.p) sel_local_kernel<T, N, true, true><<<blocks, 256, 0, s>>>(a);
+    else sel_local_kernel<T, N, true, false><<<blocks, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

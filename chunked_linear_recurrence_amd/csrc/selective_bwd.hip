@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     const bool softplus = (a.flags & SSD_FLAG_SOFTPLUS) != 0;
     const float bias = a.bias ? a.bias[q.d] : 0.f, skip = a.Dskip ? a.Dskip[q.d] : 0.f;
     float A2[kSB], carry[kSB], dA[kSB], dD = 0.f, dbias = 0.f;
-    sel_rates<kSB>(a, q.d, n0, A2);
+    sel_rates<kSB>(a, q.d, n0, kLog2eF, A2);
     const float *S = a.S + sel_slot(a, b, c, q.tt, N) + n0 * 64;
     const float *f0 = a.dfinal ? a.dfinal + (b * a.D + q.d) * (int64_t)N + n0 : nullptr;
 #pragma unroll
@@ -63,6 +63,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
         carry[n] = a.nc > 1 ? S[n * 64] : (f0 ? f0[n] : 0.f);
         dA[n] = 0.f;
     }
+    const uint32_t d = q.d;
     const Rows<T> r_u(a.u, b), r_delta(a.delta, b), r_dy(a.dy, b), r_z(a.z, b), r_B(a.B, b), r_C(a.C, b);
     // row t of an output [batch, L, D]
     const int64_t out_first = b * a.L * (int64_t)a.D;
@@ -77,15 +78,15 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     // dz and dD of a token, given its y without the skip term
     auto finish_z = [&](int t, float u, float r, float gz, float y) {
         dD = fmaf(r, u, dD);
-        if (GATE && q.live && t < end) lane_store(out_row(a.dz, t), q.d, from_f32<T>(gz * fmaf(skip, u, y)));
+        if (GATE && q.live && t < end) lane_store(out_row(a.dz, t), d, from_f32<T>(gz * fmaf(skip, u, y)));
     };
     // du and ddelta of a token, given q and sum A w (base-2 rates)
     auto finish_u = [&](int t, float dt, float u, float sig, float r, float qq, float dw) {
         const float dl = fmaf(dw, kLn2F, u * qq) * sig;
         if (q.live && t < end) {
             dbias += dl;
-            lane_store(out_row(a.du, t), q.d, from_f32<T>(fmaf(dt, qq, skip * r)));
-            lane_store(out_row(a.ddelta, t), q.d, from_f32<T>(dl));
+            lane_store(out_row(a.du, t), d, from_f32<T>(fmaf(dt, qq, skip * r)));
+            lane_store(out_row(a.ddelta, t), d, from_f32<T>(dl));
         }
     };
     // r = dout silu(z) and dout d(silu)(z)
@@ -124,10 +125,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     // A token past the row's last is a copy of an earlier one: `in` is 0 for it.
     auto fetch = [&](int t0, int i) {
         const int t = hidden(min(t0 + i, end - 1));
-        dv[i % 3] = lane_load(r_delta.at(t), q.d);
-        uv[i % 3] = lane_load(r_u.at(t), q.d);
-        dyv[i % 3] = lane_load(r_dy.at(t), q.d);
-        if (GATE) zv[i % 3] = lane_load(r_z.at(t), q.d);
+        dv[i % 3] = lane_load(r_delta.at(t), d);
+        uv[i % 3] = lane_load(r_u.at(t), d);
+        dyv[i % 3] = lane_load(r_dy.at(t), d);
+        if (GATE) zv[i % 3] = lane_load(r_z.at(t), d);
     };
     auto coefficients = [&](int t0, int i, Uniform<T, kSB> &B, Uniform<T, kSB> &C) {
         const int t = hidden(min(t0 + i, end - 1));
@@ -245,8 +246,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
                     for (int k = 0; k < 3; ++k) s[k] += tok[wave - nb + w][i][4 + k][lane];
                 const int t = min(t0 + i, end - 1);
                 float r, gz;
-                T dy1 = lane_load(r_dy.at(t), q.d), z1 = dy1;
-                if (GATE) z1 = lane_load(r_z.at(t), q.d);
+                T dy1 = lane_load(r_dy.at(t), d), z1 = dy1;
+                if (GATE) z1 = lane_load(r_z.at(t), d);
                 upstream(dy1, z1, i < m ? live : 0.f, &r, &gz);
                 finish_z(t0 + i, tok[wave][i][1][lane], r, gz, s[0]);
                 finish_u(t0 + i, tok[wave][i][0][lane], tok[wave][i][1][lane], tok[wave][i][2][lane], r, s[1], s[2]);
@@ -256,9 +257,9 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     }
     if (q.live) {
         for (int t = max(begin, end) + nb; t < stop; t += NB) {
-            lane_store(out_row(a.du, t), q.d, from_f32<T>(0.f));
-            lane_store(out_row(a.ddelta, t), q.d, from_f32<T>(0.f));
-            if (GATE) lane_store(out_row(a.dz, t), q.d, from_f32<T>(0.f));
+            lane_store(out_row(a.du, t), d, from_f32<T>(0.f));
+            lane_store(out_row(a.ddelta, t), d, from_f32<T>(0.f));
+            if (GATE) lane_store(out_row(a.dz, t), d, from_f32<T>(0.f));
         }
         if (c == 0 && a.dinit) {
             float *o = a.dinit + (b * a.D + q.d) * (int64_t)N + n0;

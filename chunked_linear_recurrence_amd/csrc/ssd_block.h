@@ -175,14 +175,22 @@ __device__ __forceinline__ float dsilu_f32(float v) {
 
 // log(1 + e^v) and, in *sig, its derivative.  With w = fl(1 + e^v) the logarithm of w misses
 // what the addition rounded off; (e^v - (w - 1)) / w puts it back, so small results keep
-// their relative accuracy.  Above 20 the result is v to float32.
+// their relative accuracy.  Above 20 the result is v to float32.  NaN stays NaN.
 __device__ __forceinline__ float softplus_f32(float v, float *sig) {
-    const float e = exp2_fast(fminf(v, 30.f) * kLog2eF);
-    const float w = 1.f + e;
-    const float r = rcp_fast(w);
-    *sig = e * r;
+    const float e = exp2_fast(v * kLog2eF), w = 1.f + e, r = rcp_fast(w);
     const float l = fmaf(__builtin_amdgcn_logf(w), kLn2F, (e - (w - 1.f)) * r);
+    *sig = v > 20.f ? 1.f : e * r;
     return v > 20.f ? v : l;
+}
+
+// The same in base 2: log2(1 + 2^v) without its derivative and without a division.  What the
+// addition rounded off is at most 2^-24 where w < 2, where it is added undivided (1/w > 1/2
+// changes it by less than its own rounding of the logarithm's terms); where w is larger, that
+// bound is below the result's own rounding.  From 126 on the result is v.
+__device__ __forceinline__ float softplus2_f32(float v) {
+    const float e = exp2_fast(v), w = 1.f + e;
+    const float c = __builtin_amdgcn_fmed3f(e - (w - 1.f), -0x1p-24f, 0x1p-24f);
+    return v > 126.f ? v : fmaf(c, kLog2eF, __builtin_amdgcn_logf(w));
 }
 
 // Sum over `rows` values a stride apart, for the 64 columns of a workgroup of W waves (p: this

@@ -43,7 +43,8 @@ __device__ __forceinline__ int hidden(int v) {
     asm volatile("" : "+s"(v));
     return v;
 }
-__device__ __forceinline__ int hidden_lane(int v) {
+template <typename I>
+__device__ __forceinline__ I hidden_lane(I v) {
     asm volatile("" : "+v"(v));
     return v;
 }
@@ -102,13 +103,19 @@ __device__ __forceinline__ SelTile sel_tile(const SelArgs &a, int tt) {
 }
 
 template <int N>
-__device__ __forceinline__ void sel_rates(const SelArgs &a, uint32_t d, int n0, float (&A2)[N]) {
+__device__ __forceinline__ void sel_rates(const SelArgs &a, uint32_t d, int n0, float scale, float (&A)[N]) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) A2[n] = a.A[(int64_t)d * a.N + n0 + n] * kLog2eF;
+    for (int n = 0; n < N; ++n) A[n] = a.A[(int64_t)d * a.N + n0 + n] * scale;
 }
 
-// The step size of one token and its derivative by delta.  Chosen without a branch, which
-// would cut the unrolled tokens into blocks that cannot be scheduled together.
+// The step size of one token in base 2 (dt log2(e), so that its decays are 2^(dt2 A)), from
+// delta and the bias times log2(e).  Chosen without a branch, which would cut the unrolled
+// tokens into blocks that cannot be scheduled together.
+__device__ __forceinline__ float sel_dt2(float delta, float bias2, bool softplus) {
+    const float v = fmaf(delta, kLog2eF, bias2), l = softplus2_f32(v);
+    return softplus ? l : v;
+}
+// The step size itself, and its derivative by delta.
 __device__ __forceinline__ float sel_dt(float raw, bool softplus, float *sig) {
     float s;
     const float dt = softplus_f32(raw, &s);

@@ -252,3 +252,24 @@ def test_results_do_not_change_from_call_to_call():
         if first is not None:
             assert all(torch.equal(a, b) for a, b in zip(first, now))
         first = now
+
+
+def test_nan_stays_in_its_channel():
+    """A NaN step size or input reaches its own channel's later outputs and no other channel's."""
+    t = make(1, 30, 130, 16, 1, torch.float32, seed=21)
+    t["delta"][0, 10, 5] = float("nan")
+    t["uz"][0, 12, 70] = float("nan")
+    g = on_gpu(t)
+    keys = ("u", "delta", "A", "B", "C", "D", "z", "bias")
+    y, f = ssd.selective_fwd(*(g[k] for k in keys), g["st"])
+    clean = dict(g)
+    clean["delta"], clean["uz"] = g["delta"].clone(), g["uz"].clone()
+    clean["delta"][0, 10, 5], clean["uz"][0, 12, 70] = 0.0, 0.0
+    clean = views(clean)
+    yc, fc = ssd.selective_fwd(*(clean[k] for k in keys), g["st"])
+    torch.cuda.synchronize()
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[0, 10:, 5], bad[0, 12:, 70] = True, True
+    assert torch.equal(torch.isnan(y), bad)
+    assert torch.equal(y[~bad], yc[~bad])
+    assert torch.isnan(f[0, [5, 70]]).all() and torch.isfinite(f[0, [k for k in range(130) if k not in (5, 70)]]).all()
