@@ -37,9 +37,12 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     constexpr int NB = N / kSB, TPB = 4 / NB, K = kKeep;
     __shared__ __align__(16) float red[4][4 * kQuarter];
     __shared__ float comb[4][K][2][64];
-    // dt, u, d(softplus), r lane by lane and, where a tile has several blocks of states, a
-    // block's part of y, q and sum A w
-    __shared__ float tok[4][K][NB > 1 ? 7 : 4][64];
+    // dt, u, d(softplus) and r lane by lane.  A tile's NB waves each write the same values; the
+    // barriers around the end of a group keep its waves from writing the next group's before all
+    // have read this one's.
+    __shared__ float tok[TPB][K][4][64];
+    // where a tile has several blocks of states, each block's part of y, q and sum A w
+    __shared__ float cross[NB > 1 ? 4 : 1][NB > 1 ? K : 1][3][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int parts = (a.tiles + TPB - 1) / TPB;
     const int pg = blockIdx.x % (parts * a.G), g = pg / parts, part = pg % parts;
@@ -158,10 +161,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             const float dt = in * sel_dt(to_f32(dv[i % 3]) + bias, softplus, &sig);
             const float u = in * to_f32(uv[i % 3]), x = dt * u;
             upstream(dyv[i % 3], GATE ? zv[i % 3] : dyv[i % 3], in, &r, &gz);
-            tok[wave][i][0][lane] = dt;
-            tok[wave][i][1][lane] = u;
-            tok[wave][i][2][lane] = sig;
-            tok[wave][i][3][lane] = r;
+            tok[wave / NB][i][0][lane] = dt;
+            tok[wave / NB][i][1][lane] = u;
+            tok[wave / NB][i][2][lane] = sig;
+            tok[wave / NB][i][3][lane] = r;
             f32x4 p;
 #pragma unroll
             for (int n = 0; n < kSB; ++n) {
@@ -173,7 +176,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             if (i > 0) comb[wave][i - 1][1][lane] = column_sum();
             if constexpr (NB == 1) finish_z(t0 + i, u, r, gz, y);
             else {
-                tok[wave][i][4][lane] = y;
+                cross[wave][i][0][lane] = y;
             }
             Bt = Bn;
             Ct = Cn;
@@ -192,8 +195,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
                 fetch(tp, 1);
             }
             column_read();
-            const float dt = tok[wave][i][0][back], u = tok[wave][i][1][back], sig = tok[wave][i][2][back];
-            const float r = tok[wave][i][3][back], x = dt * u;
+            const float dt = tok[wave / NB][i][0][back], u = tok[wave / NB][i][1][back], sig = tok[wave / NB][i][2][back];
+            const float r = tok[wave / NB][i][3][back], x = dt * u;
             float qq = 0.f, dw = 0.f;
             f32x4 p;
 #pragma unroll
@@ -213,8 +216,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             else comb[wave][i + 1][0][lane] = s;
             if constexpr (NB == 1) finish_u(t0 + i, dt, u, sig, r, qq, dw);
             else {
-                tok[wave][i][5][lane] = qq;
-                tok[wave][i][6][lane] = dw;
+                cross[wave][i][1][lane] = qq;
+                cross[wave][i][2][lane] = dw;
             }
             Bt = Bn;
             Ct = Cn;
@@ -243,14 +246,14 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
 #pragma unroll
                 for (int w = 0; w < NB; ++w)
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) s[k] += tok[wave - nb + w][i][4 + k][lane];
+                    for (int k = 0; k < 3; ++k) s[k] += cross[wave - nb + w][i][k][lane];
                 const int t = min(t0 + i, end - 1);
                 float r, gz;
                 T dy1 = lane_load(r_dy.at(t), d), z1 = dy1;
                 if (GATE) z1 = lane_load(r_z.at(t), d);
                 upstream(dy1, z1, i < m ? live : 0.f, &r, &gz);
-                finish_z(t0 + i, tok[wave][i][1][lane], r, gz, s[0]);
-                finish_u(t0 + i, tok[wave][i][0][lane], tok[wave][i][1][lane], tok[wave][i][2][lane], r, s[1], s[2]);
+                finish_z(t0 + i, tok[wave / NB][i][1][lane], r, gz, s[0]);
+                finish_u(t0 + i, tok[wave / NB][i][0][lane], tok[wave / NB][i][1][lane], tok[wave / NB][i][2][lane], r, s[1], s[2]);
             }
         }
         __syncthreads();
