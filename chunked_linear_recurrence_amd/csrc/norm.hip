@@ -12,7 +12,8 @@
 // whose registers hold it; rows that 16 waves cannot hold are read again for each pass.
 // dw and db: each workgroup walks many rows with one running sum per column in float32,
 // leaves one row of partial sums, and a second kernel adds those rows in order, so results
-// do not depend on scheduling.
+// do not depend on scheduling.  32768 rows of 2048 channels in bfloat16: 50 us forward
+// (5.4 TB/s), 84 + 5 us backward (4.8).
 #include "ssd_block.h"
 
 namespace ssd {
@@ -82,8 +83,7 @@ __device__ __forceinline__ void load_row(const T *x, int D, int tid, typename Pa
 
 // A workgroup walks many rows with weight and bias in registers (read per row they are four
 // times a bfloat16 row's own traffic) and, where registers allow, the next row on its way while
-// one is reduced: 32768 rows of 2048 channels take 50 us (5.4 TB/s), against 71 with a row a
-// wave.
+// one is reduced: 32768 rows of 2048 channels take 50 us, against 71 with a row a wave.
 template <typename T, int V, int K, int WPR>
 __global__ __launch_bounds__(norm_threads<WPR>()) void norm_fwd_kernel(NormArgs a) {
     __shared__ float red[16];

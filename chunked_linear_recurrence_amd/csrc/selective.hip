@@ -5,10 +5,17 @@
 //     y_t = sum_n C_t[n] h_t[n] + D u_t;   out_t = y_t z_t sigmoid(z_t)   (or y_t)
 //
 // The decays differ for every (channel, state), so the products do not factor into matrix
-// products as they do with one decay per head: the work is N exponentials, 2 N
-// multiplications and 2 N fused multiply-adds per (token, channel) on the vector units,
-// against 4 activations moved.  At N = 16 that is about 26 cycles per state of a wave, and
-// the vector units, not memory, bound the scan.
+// products as they do with one decay per head: the work is, per (token, channel, state), an
+// exponential (two issue slots), two multiplications and two fused multiply-adds on the vector
+// units, against 4 activations moved per (token, channel).  A tile of 64 channels and 16 states
+// takes 96 slots of 4 cycles a token for that, 128 with step sizes, gate and conversions; the
+// counters show the vector units busy for all of (1)'s time and over 80% of (3)'s.  So memory
+// does not bound the scan (2 TB/s at 32768 tokens of 2048 channels: 184 us in (1), 239 in (3)),
+// and each slot counts: the step size is kept in base 2, so that a decay is one multiplication
+// and one 2^x; B and C are scalar operands; addresses are scalar; everything that would sit
+// between a load and its use is fetched 3 tokens early.  The float32 matrix instructions that
+// could form dt u B for 16 states at once were measured not to overlap with vector work on the
+// same SIMD, and bfloat16 ones would round the state.
 //
 // Chunks.  A tile of 64 channels is one wave, and few channels at batch 1 leave the GPU
 // empty, so the sequence is cut into chunks: (1) every chunk's end state from a zero state,
@@ -258,7 +265,7 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
 
 // One token.  The state, 8 bytes read and written per element, is the traffic: N/4 threads
 // share a channel, each with 4 states (one 16-byte access each way), and add their parts of
-// the sum over n with wave shuffles.
+// the sum over n with wave shuffles.  256 streams of 2048 channels: 15.5 us for 71 MB.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
     constexpr int Q = N / 4;
