@@ -195,18 +195,23 @@ size_t sel_kept(const ssd_selective_dims_t &d) {
     return (size_t)(d.batch * nsub * d.ngroups * ssd::sel_tiles(d.channels, d.ngroups) * d.dstate) * 64 * 4;
 }
 
-ssd_status_t sel_spans(const ssd_selective_dims_t &d, size_t out[6]) {
+// Bytes spanned by u, delta, z, B, C and dy, in this order; 0 for one that is not there, whose
+// strides are not looked at.  A step has no token strides.
+ssd_status_t sel_spans(const ssd_selective_dims_t &d, const void *z, const void *dy, bool step, size_t out[6]) {
     const int64_t e = act_bytes(d.dtype), gn = d.ngroups * d.dstate;
     const int64_t bs[] = {d.u_batch_stride, d.delta_batch_stride, d.z_batch_stride, d.B_batch_stride, d.C_batch_stride,
                           d.dy_batch_stride};
     const int64_t ts[] = {d.u_token_stride, d.delta_token_stride, d.z_token_stride, d.B_token_stride, d.C_token_stride,
                           d.dy_token_stride};
     for (int i = 0; i < 6; ++i) {
-        if (!span(d.batch, bs[i], d.seqlen, ts[i], i == 3 || i == 4 ? gn : d.channels, e, &out[i]))
+        out[i] = 0;
+        if ((i == 2 && !z) || (i == 5 && !dy)) continue;
+        const int64_t t = step ? 0 : ts[i];
+        const bool coef = i == 3 || i == 4;
+        if (!span(d.batch, bs[i], d.seqlen, t, coef ? gn : d.channels, e, &out[i]))
             return fail(SSD_ERR_BAD_SHAPE, "strides must be >= 0 and spans below 2^58 elements");
-        if (ts[i] > INT32_MAX / e)
-            return fail(SSD_ERR_UNSUPPORTED, "a token stride spans more than 2^31 bytes");
-        if ((i == 3 || i == 4) && e == 2 && ((bs[i] | ts[i]) & 1))
+        if (t > INT32_MAX / e) return fail(SSD_ERR_UNSUPPORTED, "a token stride spans more than 2^31 bytes");
+        if (coef && !step && e == 2 && ((bs[i] | t) & 1))
             return fail(SSD_ERR_MISALIGNED, "bfloat16 B and C need even strides (4-byte rows)");
     }
     return SSD_OK;
@@ -345,7 +350,7 @@ ssd_status_t ssd_selective_fwd(const ssd_selective_dims_t *dims, const void *u, 
         return fail(SSD_ERR_NULL_ARG, "u, delta, A, B, C and y must be non-NULL");
     if (flags & ~SSD_FLAG_SOFTPLUS) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
     size_t sp[6];
-    TRY(sel_spans(d, sp));
+    TRY(sel_spans(d, z, nullptr, false, sp));
     ssd::SelArgs a = sel_args(d, false);
     const SelLayout lo = sel_layout(a, false);
     if (lo.total && (!workspace || workspace_bytes < lo.total))
@@ -392,12 +397,12 @@ ssd_status_t ssd_selective_step(const ssd_selective_dims_t *dims, const void *u,
         return fail(SSD_ERR_NULL_ARG, "u, delta, A, B, C, state_in, state_out and y must be non-NULL");
     if (flags & ~SSD_FLAG_SOFTPLUS) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
     size_t sp[6];
-    TRY(sel_spans(d, sp));
+    TRY(sel_spans(d, z, nullptr, true, sp));
     const size_t e = (size_t)act_bytes(d.dtype), ch = (size_t)d.channels;
     const size_t ns = (size_t)(d.batch * d.channels * d.dstate) * 4;
     if (!aligned16(state_in)) return fail(SSD_ERR_MISALIGNED, "state_in is not 16-byte aligned");
-    const Tensor in[] = {{"u", u, sp[0], e}, {"delta", delta, sp[1], e}, {"z", z, sp[2], e}, {"B", B, sp[3], 4},
-                         {"C", C, sp[4], 4}, {"A", A, ch * d.dstate * 4, 4}, {"D", D, ch * 4, 4},
+    const Tensor in[] = {{"u", u, sp[0], e}, {"delta", delta, sp[1], e}, {"z", z, sp[2], e}, {"B", B, sp[3], e},
+                         {"C", C, sp[4], e}, {"A", A, ch * d.dstate * 4, 4}, {"D", D, ch * 4, 4},
                          {"delta_bias", delta_bias, ch * 4, 4},
                          {"state_in", state_in == state_out ? nullptr : state_in, ns, 16}};
     const Tensor out[] = {{"y", y, (size_t)d.batch * ch * e, e}, {"state_out", state_out, ns, 16}};
@@ -442,7 +447,7 @@ ssd_status_t ssd_selective_bwd(const ssd_selective_dims_t *dims, const void *dy,
     if ((z != nullptr) != (dz != nullptr)) return fail(SSD_ERR_NULL_ARG, "dz must be given exactly if z is");
     if (flags & ~SSD_FLAG_SOFTPLUS) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
     size_t sp[6];
-    TRY(sel_spans(d, sp));
+    TRY(sel_spans(d, z, dy, false, sp));
     ssd::SelArgs a = sel_args(d, true);
     const SelLayout lo = sel_layout(a, true);
     if (!workspace || workspace_bytes < lo.total)

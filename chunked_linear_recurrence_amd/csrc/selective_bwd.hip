@@ -79,7 +79,9 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     const int back = hidden_lane(lane);
     float *mine = red[wave] + (lane / 16) * kQuarter + (lane % 16) * kRow;
     const float *column = red[wave] + (lane / 16) * kQuarter + lane % 16;
-    const float live = q.live ? 1.f : 0.f;
+    // All ones, or zeros where a token or the lane's channel is a copy of another, whose values
+    // must add nothing to any sum (by bits: a product with 0 would keep infinities and NaN).
+    const uint32_t live = q.live ? ~0u : 0u;
 
     // dz and dD of a token, given its y without the skip term
     auto finish_z = [&](int t, float u, float r, float gz, float y) {
@@ -95,16 +97,17 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             lane_store(out_row(a.ddelta, t), d, from_f32<T>(dl));
         }
     };
-    // r = dout silu(z) and dout d(silu)(z)
-    auto upstream = [&](T dyv, T zv, float in, float *r, float *gz) {
-        *r = to_f32(dyv) * in;
+    // r = dout silu(z) and dout d(silu)(z), masked
+    auto upstream = [&](T dyv, T zv, uint32_t in, float *r, float *gz) {
+        *r = masked(to_f32(dyv), in);
         *gz = 0.f;
         if (GATE) {
-            const float z = to_f32(zv), s = sigmoid_f32(z);
+            const float z = masked(to_f32(zv), in), s = sigmoid_f32(z);
             *gz = *r * s * fmaf(z, 1.f - s, 1.f);
             *r *= z * s;
         }
     };
+
     // The lane's quarter of column lane % 16 of the products in the buffer.  Reads are started
     // before the next token's products are written (a wave's LDS operations run in order) and
     // added up after its arithmetic.
@@ -159,10 +162,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             if (i + 2 < K) fetch(t0, i + 2);
             if (i + 1 < K) coefficients(t0, i + 1, Bn, Cn);
             if (i > 0) column_read();
-            const float in = i < m ? live : 0.f;
+            const uint32_t in = i < m ? live : 0u;
             float sig, r, gz, y = 0.f;
-            const float dt = in * sel_dt(to_f32(dv[i % 3]) + bias, softplus, &sig);
-            const float u = in * to_f32(uv[i % 3]), x = dt * u;
+            const float dt = masked(sel_dt(to_f32(dv[i % 3]) + bias, softplus, &sig), in);
+            const float u = masked(to_f32(uv[i % 3]), in), x = dt * u;
             upstream(dyv[i % 3], GATE ? zv[i % 3] : dyv[i % 3], in, &r, &gz);
             tok[wave / NB][i][0][lane] = dt;
             tok[wave / NB][i][1][lane] = u;
@@ -184,6 +187,14 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
             Bt = Bn;
             Ct = Cn;
             __builtin_amdgcn_sched_barrier(0);
+        }
+        // A row that ends inside the group: the states from its last token on are what the copied
+        // tokens would multiply by 0.
+        if (m < K) {
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+#pragma unroll
+                for (int n = 0; n < kSB; ++n) hs[i][n] = masked(hs[i][n], i < m - 1 ? ~0u : 0u);
         }
         // And back: g, what follows from it, and dB's products.
         coefficients(t0, K - 1, Bt, Ct);
@@ -254,7 +265,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
                 float r, gz;
                 T dy1 = lane_load(r_dy.at(t), d), z1 = dy1;
                 if (GATE) z1 = lane_load(r_z.at(t), d);
-                upstream(dy1, z1, i < m ? live : 0.f, &r, &gz);
+                upstream(dy1, z1, i < m ? live : 0u, &r, &gz);
                 finish_z(t0 + i, tok[wave / NB][i][1][lane], r, gz, s[0]);
                 finish_u(t0 + i, tok[wave / NB][i][0][lane], tok[wave / NB][i][1][lane], tok[wave / NB][i][2][lane], r, s[1], s[2]);
             }

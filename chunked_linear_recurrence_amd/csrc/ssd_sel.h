@@ -49,6 +49,10 @@ __device__ __forceinline__ I hidden_lane(I v) {
     return v;
 }
 
+__device__ __forceinline__ float masked(float v, uint32_t bits) {
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & bits);
+}
+
 // Keeps a running sum where it is written: the compiler otherwise moves a chain of additions
 // whose result is used late past the branches in between, and holds all the terms until then.
 __device__ __forceinline__ void pinned(float &v) { asm volatile("" : "+v"(v)); }

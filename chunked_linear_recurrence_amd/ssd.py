@@ -426,6 +426,8 @@ def _param(name, t, shape, device, dtype=torch.float32):
 def _rows(name, t, shape, like):
     """An activation view: `like`'s dtype and device, contiguous channels.  Its pointer, batch
     stride and token stride (0 where the shape has no tokens)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a torch.Tensor (got %s)" % (name, type(t).__name__))
     if t.shape != shape:
         raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), shape))
     if t.dtype != like.dtype:
@@ -440,6 +442,8 @@ def _rows(name, t, shape, like):
 
 def _coef_rows(name, t, lead, like):
     """B or C [*lead, G, N]: as _rows, with [G, N] contiguous together."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a torch.Tensor (got %s)" % (name, type(t).__name__))
     if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
         raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), tuple(lead) + ("*", "*")))
     if t.dtype != like.dtype:
@@ -499,6 +503,12 @@ def _workspace(t, nbytes, device):
     return t
 
 
+def _taps(weight):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a torch.Tensor [channels, taps]")
+    return weight.shape[1]
+
+
 def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, y=None, final_state=None,
              want_final=True, stream=None):
     """Short causal convolution with an optional SiLU (ssd_conv_fwd): x [b, L, C], weight
@@ -508,7 +518,7 @@ def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, 
     L_ = lib()
     code = _activation("x", x, 3)
     b, L, C = x.shape
-    W = weight.shape[1] if weight.dim() == 2 else 0
+    W = _taps(weight)
     dev = x.device
     xp, xb, xt = _rows("x", x, (b, L, C), x)
     wp = _param("weight", weight, (C, W), dev)
@@ -535,7 +545,7 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stre
     L_ = lib()
     code = _activation("x", x, 2)
     b, C = x.shape
-    W = weight.shape[1] if weight.dim() == 2 else 0
+    W = _taps(weight)
     dev, shape = x.device, (b, W - 1, C)
     xp, xb, _ = _rows("x", x, (b, C), x)
     wp = _param("weight", weight, (C, W), dev)
@@ -567,7 +577,7 @@ def conv_bwd(dy, x, weight, bias=None, init_state=None, *, dfinal=None, lengths=
     L_ = lib()
     code = _activation("x", x, 3)
     b, L, C = x.shape
-    W = weight.shape[1] if weight.dim() == 2 else 0
+    W = _taps(weight)
     dev, st = x.device, (b, W - 1, C)
     xp, xb, xt = _rows("x", x, (b, L, C), x)
     gp, gb, gt = _rows("dy", dy, (b, L, C), x)

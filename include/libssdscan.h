@@ -239,7 +239,7 @@ ssd_status_t ssd_step(const ssd_dims_t *dims, const void *x, const void *dt, con
  *   batch and token stride (elements, >= 0), for example one half of a projection's output.
  *   The strides are fields of the dims.  Outputs, states and parameters are contiguous.
  * Alignment.  Pointers are aligned to their element size; B and C rows, in bfloat16, to 4
- *   bytes (even strides).  Where addresses and sizes allow 16-byte accesses, the
+ *   bytes (even strides) except for a single token.  Where addresses and sizes allow 16-byte accesses, the
  *   convolution and the norm use them; results are the same either way.  Single-token
  *   states of the scan must be 16-byte aligned.
  * Lengths.  `lengths` (device, int32 [batch], or NULL for seqlen everywhere) gives each

@@ -243,3 +243,25 @@ def test_selective_bwd_needs_the_forward_s_kept_states():
     with pytest.raises(ValueError, match="kept has shape"):
         ssd.selective_bwd(torch.zeros(2, 9, 8), s["u"], s["delta"], s["A"], s["B"], s["C"], s["D"], s["z"], s["delta_bias"],
                           torch.zeros(16, dtype=torch.uint8))
+
+
+def test_missing_tensors_are_named():
+    lib()
+    a, s = _conv(), _sel()
+    for call, msg in ((lambda: ssd.conv_fwd(None, a["weight"]), "x must be"),
+                      (lambda: ssd.conv_fwd(a["x"], None), "weight must be"),
+                      (lambda: ssd.conv_bwd(None, a["x"], a["weight"]), "dy must be"),
+                      (lambda: ssd.selective_fwd(s["u"], None, s["A"], s["B"], s["C"]), "delta must be"),
+                      (lambda: ssd.selective_fwd(s["u"], s["delta"], s["A"], None, s["C"]), "B must be"),
+                      (lambda: ssd.norm_bwd(None, a["x"][0], None, None, None), "dy must be")):
+        with pytest.raises(ValueError, match=msg):
+            call()
+
+
+def test_strides_of_absent_tensors_are_not_looked_at():
+    """z's and dy's strides mean nothing without them, and a step has no token strides."""
+    d = sel_dims(over={4: -1, 5: -1, 10: -1, 11: -1})
+    assert sel_fwd(d, z=None, n=0) == 6                       # past the strides: the workspace
+    assert sel_fwd(d, n=0) == 2
+    one = sel_dims(L=1, dtype=1, over={1: -1, 7: 3})
+    assert lib().ssd_selective_step(one, P[0], P[1], P[2], P[3] + 2, P[4], P[5], P[6], P[7], P[8] + 4, P[8], P[9], 16, None) == 5

@@ -273,3 +273,58 @@ def test_nan_stays_in_its_channel():
     assert torch.equal(torch.isnan(y), bad)
     assert torch.equal(y[~bad], yc[~bad])
     assert torch.isnan(f[0, [5, 70]]).all() and torch.isfinite(f[0, [k for k in range(130) if k not in (5, 70)]]).all()
+
+
+@pytest.mark.parametrize("L", [19, 24])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_last_token_s_input_reaches_no_earlier_gradient(L, bad):
+    """The last token's u enters no state that a gradient of A or of an earlier token reads, in
+    rows that end inside a group of 8 tokens too."""
+    t = make(1, L, 130, 16, 1, torch.float32, seed=22)
+    g = on_gpu(t)
+    keys = ("u", "delta", "A", "B", "C", "D", "z", "bias")
+    out = []
+    for value in (0.5, bad):
+        e = dict(g)
+        e["uz"] = g["uz"].clone()
+        e["uz"][0, L - 1, 7] = value
+        e = views(e)
+        _, _, kept = ssd.selective_fwd(*(e[k] for k in keys), g["st"], keep=True)
+        out.append(ssd.selective_bwd(g["dy"], *(e[k] for k in keys), kept))
+    torch.cuda.synchronize()
+    a, b = out
+    assert torch.equal(a.dA, b.dA) and torch.equal(a.dinit, b.dinit)
+    for name in ("du", "ddelta", "dz", "dB", "dC"):
+        assert torch.equal(getattr(a, name)[:, :L - 1], getattr(b, name)[:, :L - 1]), name
+
+
+def test_more_chunks_than_one_workgroup_holds_at_once():
+    """5000 tokens of one tile: over 300 chunks, whose states pass through a workgroup in several
+    rounds.  A state's memory reaches 1000 tokens here: 1000 * 4 * 2^-24 = 2.4e-4, doubled."""
+    t = make(1, 5000, 64, 16, 1, torch.float32, seed=23)
+    g, t = on_gpu(t), views(t)
+    keys = ("u", "delta", "A", "B", "C", "D", "z", "bias")
+    y, f, kept = ssd.selective_fwd(*(g[k] for k in keys), g["st"], keep=True)
+    r = ssd.selective_bwd(g["dy"], *(g[k] for k in keys), kept, dfinal=g["df"])
+    torch.cuda.synchronize()
+    yr, fr, gr = reference(t, ("D", "z", "bias", "st"), True)
+    R.check(y, yr, torch.float32, 5e-4, "y")
+    R.check(f, fr, torch.float32, 5e-4, "final_state")
+    for got, key in ((r.du, "u"), (r.ddelta, "delta"), (r.dz, "z"), (r.dB, "B"), (r.dC, "C"), (r.dA, "A"), (r.dD, "D"),
+                     (r.ddelta_bias, "bias"), (r.dinit, "st")):
+        R.check(got, gr[key], torch.float32, 5e-4, key)
+
+
+def test_single_token_views_at_any_element():
+    """A step takes B and C at any element's address."""
+    t = make(3, 1, 96, 16, 1, torch.bfloat16, seed=24)
+    g = on_gpu(t)
+    odd = torch.zeros(3, 35, dtype=torch.bfloat16, device=DEV)
+    odd[:, 1:33] = g["bc"][:, 0]
+    a = (g["u"][:, 0], g["delta"][:, 0], g["A"])
+    rest = (g["D"], g["z"][:, 0], g["bias"], g["st"])
+    out, out2 = torch.empty_like(g["st"]), torch.empty_like(g["st"])
+    y = ssd.selective_step(*a, g["B"][:, 0], g["C"][:, 0], *rest, state_out=out)
+    y2 = ssd.selective_step(*a, odd[:, None, 1:17], odd[:, None, 17:33], *rest, state_out=out2)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(out, out2)
