@@ -331,8 +331,7 @@ size_t ssd_selective_kept_bytes(const ssd_selective_dims_t *dims) {
 
 size_t ssd_selective_fwd_workspace_bytes(const ssd_selective_dims_t *dims) {
     if (check_sel(dims, false) != SSD_OK) return 0;
-    const size_t n = sel_layout(sel_args(*dims, false), false).total;
-    return n ? n : kAlign;
+    return sel_layout(sel_args(*dims, false), false).total;
 }
 
 size_t ssd_selective_bwd_workspace_bytes(const ssd_selective_dims_t *dims) {

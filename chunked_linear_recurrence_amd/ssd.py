@@ -423,35 +423,36 @@ def _param(name, t, shape, device, dtype=torch.float32):
     return t.data_ptr()
 
 
-def _rows(name, t, shape, like):
-    """An activation view: `like`'s dtype and device, contiguous channels.  Its pointer, batch
-    stride and token stride (0 where the shape has no tokens)."""
+def _rows(name, t, shape, dtype, device):
+    """An activation view with contiguous channels.  Its pointer, batch stride and token stride
+    (0 where the shape has no tokens)."""
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a torch.Tensor (got %s)" % (name, type(t).__name__))
     if t.shape != shape:
         raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), shape))
-    if t.dtype != like.dtype:
-        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, like.dtype))
-    if t.device != like.device:
-        raise ValueError("%s is on %s; expected %s" % (name, t.device, like.device))
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s; expected %s" % (name, t.device, device))
     st = t.stride()
     if st[-1] != 1 and shape[-1] != 1:
         raise ValueError("%s must have contiguous channels" % name)
     return t.data_ptr(), st[0], (st[1] if len(shape) == 3 else 0)
 
 
-def _coef_rows(name, t, lead, like):
+def _coef_rows(name, t, lead, dtype, device):
     """B or C [*lead, G, N]: as _rows, with [G, N] contiguous together."""
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a torch.Tensor (got %s)" % (name, type(t).__name__))
-    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
-        raise ValueError("%s has shape %s; expected %s" % (name, tuple(t.shape), tuple(lead) + ("*", "*")))
-    if t.dtype != like.dtype:
-        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, like.dtype))
-    if t.device != like.device:
-        raise ValueError("%s is on %s; expected %s" % (name, t.device, like.device))
+    shape = t.shape
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead:
+        raise ValueError("%s has shape %s; expected %s" % (name, tuple(shape), tuple(lead) + ("*", "*")))
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s; expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s; expected %s" % (name, t.device, device))
     st = t.stride()
-    if st[-1] != 1 or (st[-2] != t.shape[-1] and t.shape[-2] != 1):
+    if st[-1] != 1 or (st[-2] != shape[-1] and shape[-2] != 1):
         raise ValueError("%s must have contiguous groups of states" % name)
     return t.data_ptr(), st[0], (st[1] if len(lead) == 2 else 0)
 
@@ -477,7 +478,7 @@ def _elsewhere(t, stream):
         if stream.device != t.device:
             raise ValueError("the stream is on %s and the tensors are on %s" % (stream.device, t.device))
         return torch.cuda.stream(stream)
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _current(t):
@@ -494,8 +495,21 @@ def _out(name, t, shape, dtype, device):
     return t
 
 
+def _out_like(name, t, x):
+    """The same for an output of x's shape and type (the quicker of torch's allocations where x
+    is contiguous, whose layout it takes)."""
+    if t is None and x.is_contiguous():
+        return torch.empty_like(x)
+    return _out(name, t, tuple(x.shape), x.dtype, x.device)
+
+
+_NO_WORKSPACE = torch.empty(0, dtype=torch.uint8)
+
+
 def _workspace(t, nbytes, device):
-    """A caller's workspace or a fresh one; the tensor and its size in bytes."""
+    """A caller's workspace or, where one is needed, a fresh one."""
+    if t is None and nbytes == 0:
+        return _NO_WORKSPACE
     if t is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != device:
@@ -520,7 +534,7 @@ def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, 
     b, L, C = x.shape
     W = _taps(weight)
     dev = x.device
-    xp, xb, xt = _rows("x", x, (b, L, C), x)
+    xp, xb, xt = _rows("x", x, (b, L, C), x.dtype, dev)
     wp = _param("weight", weight, (C, W), dev)
     bp = _param("bias", bias, (C,), dev)
     ip = _param("init_state", init_state, (b, W - 1, C), dev, x.dtype)
@@ -530,7 +544,7 @@ def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, 
         with ctx:
             return conv_fwd(x, weight, bias, init_state, lengths=lengths, silu=silu, y=y, final_state=final_state,
                             want_final=want_final)
-    y = _out("y", y, (b, L, C), x.dtype, dev)
+    y = _out_like("y", y, x)
     if final_state is not None or (want_final and W > 1):
         final_state = _out("final_state", final_state, (b, W - 1, C), x.dtype, dev)
     dims = ConvDims(b, L, C, W, code, xb, xt, 0, 0)
@@ -547,7 +561,7 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stre
     b, C = x.shape
     W = _taps(weight)
     dev, shape = x.device, (b, W - 1, C)
-    xp, xb, _ = _rows("x", x, (b, C), x)
+    xp, xb, _ = _rows("x", x, (b, C), x.dtype, dev)
     wp = _param("weight", weight, (C, W), dev)
     bp = _param("bias", bias, (C,), dev)
     ip = _param("state", state, shape, dev, x.dtype)
@@ -556,7 +570,7 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stre
     if ctx is not None:
         with ctx:
             return conv_step(x, weight, bias, state, silu=silu, y=y, state_out=state_out)
-    y = _out("y", y, (b, C), x.dtype, dev)
+    y = _out_like("y", y, x)
     dims = ConvDims(b, 1, C, W, code, xb, 0, 0, 0)
     _check(L_.ssd_conv_step(dims, xp, wp, bp, ip, op, y.data_ptr(), SSD_FLAG_SILU if silu else 0, _current(x)))
     return y
@@ -579,8 +593,8 @@ def conv_bwd(dy, x, weight, bias=None, init_state=None, *, dfinal=None, lengths=
     b, L, C = x.shape
     W = _taps(weight)
     dev, st = x.device, (b, W - 1, C)
-    xp, xb, xt = _rows("x", x, (b, L, C), x)
-    gp, gb, gt = _rows("dy", dy, (b, L, C), x)
+    xp, xb, xt = _rows("x", x, (b, L, C), x.dtype, dev)
+    gp, gb, gt = _rows("dy", dy, (b, L, C), x.dtype, dev)
     wp = _param("weight", weight, (C, W), dev)
     bp = _param("bias", bias, (C,), dev)
     ip = _param("init_state", init_state, st, dev, x.dtype)
@@ -606,17 +620,17 @@ def _selective_inputs(u, delta, A, B, C, D, z, delta_bias, step, dy=None):
     """Checks of the selective scan's inputs; (dims, pointers in the C ABI's order up to
     delta_bias, pointer of dy)."""
     code = _activation("u", u, 2 if step else 3)
-    shape, dev = tuple(u.shape), u.device
+    shape, dtype, dev = tuple(u.shape), u.dtype, u.device
     lead, d = shape[:-1], shape[-1]
-    up, ub, ut = _rows("u", u, shape, u)
-    ep, eb, et = _rows("delta", delta, shape, u)
-    Bp, Bb, Bt = _coef_rows("B", B, lead, u)
-    Cp, Cb, Ct = _coef_rows("C", C, lead, u)
+    up, ub, ut = _rows("u", u, shape, dtype, dev)
+    ep, eb, et = _rows("delta", delta, shape, dtype, dev)
+    Bp, Bb, Bt = _coef_rows("B", B, lead, dtype, dev)
+    Cp, Cb, Ct = _coef_rows("C", C, lead, dtype, dev)
     G, N = B.shape[-2:]
     if C.shape[-2:] != (G, N):
         raise ValueError("C has shape %s; expected %s" % (tuple(C.shape), tuple(B.shape)))
-    zp, zb, zt = _rows("z", z, shape, u) if z is not None else (None, 0, 0)
-    gp, gb, gt = _rows("dy", dy, shape, u) if dy is not None else (None, 0, 0)
+    zp, zb, zt = _rows("z", z, shape, dtype, dev) if z is not None else (None, 0, 0)
+    gp, gb, gt = _rows("dy", dy, shape, dtype, dev) if dy is not None else (None, 0, 0)
     ptrs = (up, ep, _param("A", A, (d, N), dev), Bp, Cp, _param("D", D, (d,), dev), zp,
             _param("delta_bias", delta_bias, (d,), dev))
     dims = SelectiveDims(lead[0], 1 if step else lead[1], d, N, G, code, 0, ub, ut, eb, et, zb, zt, Bb, Bt, Cb, Ct,
@@ -644,7 +658,7 @@ def selective_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state
             return selective_fwd(u, delta, A, B, C, D, z, delta_bias, init_state, lengths=lengths, softplus=softplus,
                                  y=y, final_state=final_state, keep=keep, workspace=workspace)
     ws = _workspace(workspace, L_.ssd_selective_fwd_workspace_bytes(dims), dev)
-    y = _out("y", y, (b, L, d), u.dtype, dev)
+    y = _out_like("y", y, u)
     final_state = _out("final_state", final_state, st, torch.float32, dev)
     kept = torch.empty(L_.ssd_selective_kept_bytes(dims), dtype=torch.uint8, device=dev) if keep else None
     _check(L_.ssd_selective_fwd(dims, *ptrs, ip, lp, y.data_ptr(), final_state.data_ptr(), _ptr(kept),
@@ -667,7 +681,7 @@ def selective_step(u, delta, A, B, C, D, z, delta_bias, state, *, softplus=True,
         with ctx:
             return selective_step(u, delta, A, B, C, D, z, delta_bias, state, softplus=softplus, y=y,
                                   state_out=state_out)
-    y = _out("y", y, (b, d), u.dtype, dev)
+    y = _out_like("y", y, u)
     _check(L_.ssd_selective_step(dims, *ptrs, ip, op, y.data_ptr(), SSD_FLAG_SOFTPLUS if softplus else 0,
                                  _current(u)))
     return y
@@ -726,14 +740,14 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, want_stats=False, s
     code = _activation("x", x, 2)
     rows, d = x.shape
     dev = x.device
-    xp, xs, _ = _rows("x", x, (rows, d), x)
+    xp, xs, _ = _rows("x", x, (rows, d), x.dtype, dev)
     wp = _param("weight", weight, (d,), dev)
     bp = _param("bias", bias, (d,), dev)
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
             return norm_fwd(x, weight, bias, eps, y=y, want_stats=want_stats)
-    y = _out("y", y, (rows, d), x.dtype, dev)
+    y = _out_like("y", y, x)
     mean = rstd = None
     if want_stats:
         mean = torch.empty((rows,), dtype=torch.float32, device=dev)
@@ -755,8 +769,8 @@ def norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
     code = _activation("x", x, 2)
     rows, d = x.shape
     dev = x.device
-    xp, xs, _ = _rows("x", x, (rows, d), x)
-    gp, gs, _ = _rows("dy", dy, (rows, d), x)
+    xp, xs, _ = _rows("x", x, (rows, d), x.dtype, dev)
+    gp, gs, _ = _rows("dy", dy, (rows, d), x.dtype, dev)
     wp = _param("weight", weight, (d,), dev)
     mp = _param("mean", mean, (rows,), dev)
     rp = _param("rstd", rstd, (rows,), dev)

@@ -317,6 +317,8 @@ typedef struct ssd_selective_dims {
  *   init_state      [batch, channels, dstate] float32 or NULL (zeros)
  *   y               [batch, seqlen, channels] (act)
  *   final_state     [batch, channels, dstate] float32 or NULL; may be init_state
+ *   workspace       ssd_selective_fwd_workspace_bytes (0 where enough batch rows and channels
+ *                   make one pass over the sequence the faster way: it may then be NULL)
  *   kept            NULL, or ssd_selective_kept_bytes of device memory: the states before
  *                   every 8th token, which ssd_selective_bwd needs
  * Any finite A and dt whose exp(dt A) does not overflow; dt A <= 0 makes decays. */
