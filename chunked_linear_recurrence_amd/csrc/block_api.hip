@@ -150,6 +150,8 @@ ssd_status_t check_sel(const ssd_selective_dims_t *d, bool step) {
 // which its large kernel holds 2 at a time) come to.  Measured forward, 32768 tokens of 2048
 // channels in bfloat16: 747 us with 2048 waves, 535 with 4096, 479 with 8192, 473 with 12288;
 // forward and backward of 2 x 4096 tokens: 583, 530, 538, 574.
+// Up to 32 tokens the forward is one pass: 16.6 us for 32 tokens of 1536 channels, launch and
+// allocations included, against 20.5 in two chunks (48 tokens: 23.4 and 20.2).
 constexpr int64_t kSelFwdWaves = 8192, kSelBwdWaves = 4096;
 
 ssd::SelArgs sel_args(const ssd_selective_dims_t &d, bool backward) {
@@ -164,7 +166,7 @@ ssd::SelArgs sel_args(const ssd_selective_dims_t &d, bool backward) {
     a.tiles = ssd::sel_tiles(d.channels, d.ngroups);
     const int64_t waves = backward ? d.batch * d.ngroups * ssd::sel_bwd_parts(d.channels, d.ngroups, d.dstate) * 4
                                    : d.batch * d.ngroups * a.tiles;
-    ssd::sel_chunks(waves, backward ? kSelBwdWaves : kSelFwdWaves, d.seqlen, &a.nc, &a.T);
+    ssd::sel_chunks(waves, backward ? kSelBwdWaves : kSelFwdWaves, backward ? 16 : 32, d.seqlen, &a.nc, &a.T);
     return a;
 }
 

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
     for (int n = 0; n < N; ++n) h[n] = 0.f;
     const Rows<T> coef(REV ? a.C : a.B, b), val(REV ? a.dy : a.u, b), delta(a.delta, b), zr(a.z, b);
     // Step k is token begin + k, or end - 1 - k backwards.  Activations are fetched kAhead steps
-    // early into a ring, coefficients one block of 16 states early.
+    // early into a ring, coefficients one batch early.
     T dv[kRing], xv[kRing], zv[kRing];
     auto token = [&](int k) { return hidden(REV ? end - 1 - min(k, end - begin - 1) : begin + min(k, end - begin - 1)); };
     uint32_t d = q.d;
@@ -72,12 +72,13 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
         xv[slot] = lane_load(val.at(t), d);
         if (GATE) zv[slot] = lane_load(zr.at(t), d);
     };
-    Uniform<T, 16> cf, cn;
-    auto coefficients = [&](int k, int n0) { cn.load(coef.at(token(k)) + q.g * N + n0); };
+    typedef Batch<T, N> Coef;
+    Coef cf, cn;
+    auto row = [&](int k) { return coef.at(token(k)) + q.g * N; };
     if (begin < end) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) fetch(k, k);
-        coefficients(0, 0);
+        cn.load(row, 0, 0);
     }
     auto step = [&](int k, int slot) {
         const float dt2 = sel_dt2(to_f32(dv[slot]), bias2, softplus);
@@ -87,13 +88,16 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
         else if (GATE) x *= silu_f32(to_f32(zv[slot]));
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 16) {
-            cf = cn;
-            if (n0 + 16 < N) coefficients(k, n0 + 16);
-            else coefficients(k + 1, 0);
+            const int u = Coef::kTokens > 1 ? slot % Coef::kTokens : n0 / 16 % Coef::kBlocks;
+            if (u == 0) {
+                cf = cn;
+                if (n0 + 16 * Coef::kBlocks < N) cn.load(row, k, n0 + 16 * Coef::kBlocks);
+                else cn.load(row, k + Coef::kTokens, 0);
+            }
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-                const float e = exp2_fast(dt2 * A[n0 + n]);
-                h[n0 + n] = REV ? e * fmaf(x, cf[n], h[n0 + n]) : fmaf(e, h[n0 + n], x * cf[n]);
+                const float e = exp2_fast(dt2 * A[n0 + n]), c = cf.u[u][n];
+                h[n0 + n] = REV ? e * fmaf(x, c, h[n0 + n]) : fmaf(e, h[n0 + n], x * c);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -199,11 +203,11 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
         uv[slot] = lane_load(u.at(t), d);
         if (GATE) zv[slot] = lane_load(z.at(t), d);
     };
-    Uniform<T, 16> Bt, Ct, Bn, Cn;
+    typedef Batch<T, N> Coef;
+    Coef Bt, Ct, Bn, Cn;
     auto coefficients = [&](int k, int n0) {
-        const int t = token(k);
-        Bn.load(B.at(t) + q.g * N + n0);
-        Cn.load(C.at(t) + q.g * N + n0);
+        Bn.load([&](int t) { return B.at(token(t)) + q.g * N; }, k, n0);
+        Cn.load([&](int t) { return C.at(token(t)) + q.g * N; }, k, n0);
     };
     if (begin < end) {
 #pragma unroll
@@ -216,14 +220,17 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
         float acc[2] = {skip * ut, 0.f};
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += 16) {
-            Bt = Bn;
-            Ct = Cn;
-            if (n0 + 16 < N) coefficients(t, n0 + 16);
-            else coefficients(t + 1, 0);
+            const int u = Coef::kTokens > 1 ? slot % Coef::kTokens : n0 / 16 % Coef::kBlocks;
+            if (u == 0) {
+                Bt = Bn;
+                Ct = Cn;
+                if (n0 + 16 * Coef::kBlocks < N) coefficients(t, n0 + 16 * Coef::kBlocks);
+                else coefficients(t + Coef::kTokens, 0);
+            }
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-                h[n0 + n] = fmaf(exp2_fast(dt2 * A[n0 + n]), h[n0 + n], x * Bt[n]);
-                acc[n & 1] = fmaf(Ct[n], h[n0 + n], acc[n & 1]);
+                h[n0 + n] = fmaf(exp2_fast(dt2 * A[n0 + n]), h[n0 + n], x * Bt.u[u][n]);
+                acc[n & 1] = fmaf(Ct.u[u][n], h[n0 + n], acc[n & 1]);
             }
         }
         float o = acc[0] + acc[1];
@@ -303,10 +310,11 @@ __global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
 bool sel_supported(int64_t N) { return N == 16 || N == 32 || N == 64; }
 
 // Chunks so that about `target` waves run, of at least 16 tokens.  One chunk, and so a single
-// pass, where its waves already come to two for each of the 1024 SIMDs: a pass with 2 waves a
-// SIMD takes 1.5 times one with 8, but the two passes over chunks take 1.8 times one.
-void sel_chunks(int64_t waves, int64_t target, int64_t L, int *nc, int *T) {
-    const int64_t n = waves >= 2048 ? 1 : (target + waves - 1) / waves;
+// pass, up to `single` tokens and where its waves already come to two for each of the 1024
+// SIMDs: a pass with 2 waves a SIMD takes 1.4 times one with 8, but the two passes over chunks
+// take 1.8 times one.
+void sel_chunks(int64_t waves, int64_t target, int64_t single, int64_t L, int *nc, int *T) {
+    const int64_t n = waves >= 2048 || L <= single ? 1 : (target + waves - 1) / waves;
     int64_t t = (L + n - 1) / n;
     t = (t + kKeep - 1) / kKeep * kKeep;
     if (t < 16) t = 16;

@@ -101,8 +101,8 @@ inline int sel_bwd_parts(int64_t D, int64_t G, int64_t N) {
     return (sel_tiles(D, G) + sel_bwd_tiles(N) - 1) / sel_bwd_tiles(N);
 }
 // Chunks of the sequence: *nc chunks of *T tokens, for `waves` waves per chunk and about
-// `target` waves in all.
-void sel_chunks(int64_t waves, int64_t target, int64_t L, int *nc, int *T);
+// `target` waves in all; one chunk up to `single` tokens.
+void sel_chunks(int64_t waves, int64_t target, int64_t single, int64_t L, int *nc, int *T);
 hipError_t launch_sel_fwd(const SelArgs &a, hipStream_t s);
 hipError_t launch_sel_bwd(const SelArgs &a, hipStream_t s);
 hipError_t launch_sel_pass(const SelArgs &a, bool reverse, hipStream_t s);

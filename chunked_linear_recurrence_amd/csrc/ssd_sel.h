@@ -37,6 +37,23 @@ struct Uniform<bf16, N> {
     }
 };
 
+// Coefficients (rows of B or C) fetched together, one batch while the last is used.  A use of
+// scalar loads waits for all that are in flight, so a batch cannot run further ahead than one;
+// in bfloat16 it holds 32 states: 2 tokens of 16, or one token of 32, or half of one of 64
+// (float32 batches of 16 states take as many scalar registers).
+template <typename T, int N>
+struct Batch {
+    static constexpr int kBlocks = sizeof(T) == 2 ? 2 : 1;            // of 16 states
+    static constexpr int kTokens = N == 16 ? kBlocks : 1;
+    Uniform<T, 16> u[kBlocks];
+    // row(k): the address of token k's coefficients; the batch that starts at token k, state n0
+    template <typename F>
+    __device__ __forceinline__ void load(F row, int k, int n0) {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) u[i].load(kTokens > 1 ? row(k + i) : row(k) + n0 + 16 * i);
+    }
+};
+
 // The same value, unknown to the compiler: addresses of unrolled tokens are then formed where
 // they are used instead of all at once, which the scalar registers cannot hold.
 __device__ __forceinline__ int hidden(int v) {
