@@ -146,13 +146,17 @@ ssd_status_t check_sel(const ssd_selective_dims_t *d, bool step) {
     return SSD_OK;
 }
 
-// Waves that the chunks of the forward (8 on each of 1024 SIMDs) and of the backward (4, of
-// which its large kernel holds 2 at a time) come to.  Measured forward, 32768 tokens of 2048
-// channels in bfloat16: 747 us with 2048 waves, 535 with 4096, 479 with 8192, 473 with 12288;
-// forward and backward of 2 x 4096 tokens: 583, 530, 538, 574.
-// Up to 32 tokens the forward is one pass: 16.6 us for 32 tokens of 1536 channels, launch and
-// allocations included, against 20.5 in two chunks (48 tokens: 23.4 and 20.2).
-constexpr int64_t kSelFwdWaves = 8192, kSelBwdWaves = 4096;
+// How a sequence is cut into chunks: waves that the chunks come to together (8 on each of 1024
+// SIMDs in the forward, 4 in the backward, of which its large kernel holds 2 at a time), and
+// from how many waves of a single pass on, and up to how many tokens, one pass is taken.
+// Measured, 16 states, bfloat16.  Waves: 32768 tokens of 2048 channels take 572 us with 2048
+// waves, 443 with 4096, 401 with 8192, 406 with 12288; forward and backward of 2 x 4096 tokens
+// 464, 433, 434, 440 by the forward's, and 443, 434, - and 444 by the backward's.  One pass, 256
+// and 1024 tokens of 2048 channels: 143 and 562 us with 1280 waves against 137 and 467 in chunks,
+// 142 and 562 with 1536 against 176 and 556, 144 and 564 with 1792 against 190 and 621; with the
+// backward 604 and 2355 with 1536 against 653 and 2155, 612 and 2405 with 1792 against 721 and
+// 2475.  32 tokens of 1536 channels: 16.6 us in one pass against 20.5 (48 tokens: 23.4, 20.2).
+constexpr ssd::SelCut kSelFwd = {8192, 1536, 32}, kSelBwd = {4096, 1792, 16};
 
 ssd::SelArgs sel_args(const ssd_selective_dims_t &d, bool backward) {
     ssd::SelArgs a;
@@ -166,7 +170,7 @@ ssd::SelArgs sel_args(const ssd_selective_dims_t &d, bool backward) {
     a.tiles = ssd::sel_tiles(d.channels, d.ngroups);
     const int64_t waves = backward ? d.batch * d.ngroups * ssd::sel_bwd_parts(d.channels, d.ngroups, d.dstate) * 4
                                    : d.batch * d.ngroups * a.tiles;
-    ssd::sel_chunks(waves, backward ? kSelBwdWaves : kSelFwdWaves, backward ? 16 : 32, d.seqlen, &a.nc, &a.T);
+    ssd::sel_chunks(waves, backward ? kSelBwd : kSelFwd, d.seqlen, &a.nc, &a.T);
     return a;
 }
 

@@ -309,12 +309,8 @@ __global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
 
 bool sel_supported(int64_t N) { return N == 16 || N == 32 || N == 64; }
 
-// Chunks so that about `target` waves run, of at least 16 tokens.  One chunk, and so a single
-// pass, up to `single` tokens and where its waves already come to two for each of the 1024
-// SIMDs: a pass with 2 waves a SIMD takes 1.4 times one with 8, but the two passes over chunks
-// take 1.8 times one.
-void sel_chunks(int64_t waves, int64_t target, int64_t single, int64_t L, int *nc, int *T) {
-    const int64_t n = waves >= 2048 || L <= single ? 1 : (target + waves - 1) / waves;
+void sel_chunks(int64_t waves, const SelCut &cut, int64_t L, int *nc, int *T) {
+    const int64_t n = waves >= cut.enough || L <= cut.single ? 1 : (cut.target + waves - 1) / waves;
     int64_t t = (L + n - 1) / n;
     t = (t + kKeep - 1) / kKeep * kKeep;
     if (t < 16) t = 16;

@@ -100,9 +100,13 @@ inline int sel_bwd_tiles(int64_t N) { return (int)(64 / N); }
 inline int sel_bwd_parts(int64_t D, int64_t G, int64_t N) {
     return (sel_tiles(D, G) + sel_bwd_tiles(N) - 1) / sel_bwd_tiles(N);
 }
-// Chunks of the sequence: *nc chunks of *T tokens, for `waves` waves per chunk and about
-// `target` waves in all; one chunk up to `single` tokens.
-void sel_chunks(int64_t waves, int64_t target, int64_t single, int64_t L, int *nc, int *T);
+// Chunks of the sequence: *nc chunks of *T tokens (at least 16) so that about cut.target waves
+// run, for `waves` waves per chunk; one chunk, and so a single pass, from cut.enough waves on
+// and up to cut.single tokens.
+struct SelCut {
+    int64_t target, enough, single;
+};
+void sel_chunks(int64_t waves, const SelCut &cut, int64_t L, int *nc, int *T);
 hipError_t launch_sel_fwd(const SelArgs &a, hipStream_t s);
 hipError_t launch_sel_bwd(const SelArgs &a, hipStream_t s);
 hipError_t launch_sel_pass(const SelArgs &a, bool reverse, hipStream_t s);
