@@ -13,7 +13,7 @@
 // the last W-1 inputs in registers, so that an input is read from memory once, plus W-1
 // tokens per TS that the caches hold; the loads of 8 tokens (4 in the backward) are started
 // together, as a store in between may touch what a later load reads as far as the compiler
-// knows.  8 x 4096 tokens of 2048 channels in bfloat16: 58 us, 4.6 TB/s (a copy of the same
+// knows.  8 x 4096 tokens of 2048 channels in bfloat16: 59 us, 4.6 TB/s (a copy of the same
 // size reaches 4.8).
 #include "ssd_block.h"
 
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int TS) {
 }
 
 // One token: y from the state and x, and the state moved on by one (in place or not).  Its few
-// kilobytes are latency alone (2.6 us at 1536 channels): one access a thread, one wave a workgroup.
+// kilobytes are latency alone (2.4 us at 1536 channels): one access a thread, one wave a workgroup.
 template <typename T, int W, int V>
 __global__ __launch_bounds__(64) void conv_step_kernel(ConvArgs a) {
     const int nt = (a.C + V - 1) / V;

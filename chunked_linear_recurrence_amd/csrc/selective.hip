@@ -10,7 +10,7 @@
 // units, against 4 activations moved per (token, channel).  A tile of 64 channels and 16 states
 // takes 96 slots of 4 cycles a token for that, 128 with step sizes, gate and conversions; the
 // counters show the vector units busy for all of (1)'s time and over 80% of (3)'s.  So memory
-// does not bound the scan (2 TB/s at 32768 tokens of 2048 channels: 184 us in (1), 239 in (3)),
+// does not bound the scan (2 TB/s at 32768 tokens of 2048 channels: 177-194 us in (1), 232-259 in (3)),
 // and each slot counts: the step size is kept in base 2, so that a decay is one multiplication
 // and one 2^x; B and C are scalar operands; addresses are scalar; everything that would sit
 // between a load and its use is fetched 3 tokens early.  The float32 matrix instructions that
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(SelArgs a) {
 
 // One token.  The state, 8 bytes read and written per element, is the traffic: N/4 threads
 // share a channel, each with 4 states (one 16-byte access each way), and add their parts of
-// the sum over n with wave shuffles.  256 streams of 2048 channels: 15.5 us for 71 MB.
+// the sum over n with wave shuffles.  256 streams of 2048 channels: 16 us for 71 MB.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void sel_step_kernel(SelStepArgs a) {
     constexpr int Q = N / 4;

@@ -24,7 +24,7 @@
 // to memory, added up in order by a last kernel, so that results do not depend on scheduling.
 //
 // 336 vector instructions a (token, 64 channels, 16 states) bound it: 2 x 4096 tokens of 2048
-// channels take 230 us, the vector units busy for 77% of them with two waves a SIMD.
+// channels take 235 us, the vector units busy for 76% of them with two waves a SIMD.
 #include "ssd_sel.h"
 
 namespace ssd {
