@@ -14,6 +14,7 @@ import math
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 from . import ssd
 
@@ -33,6 +34,7 @@ class _Norm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         g = ssd.norm_bwd(_rows(dy, x), x, weight, mean, rstd)
@@ -48,6 +50,7 @@ class _Conv(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dfinal):
         x, weight, bias, init_state, lengths = ctx.saved_tensors
         g = ssd.conv_bwd(_rows(dy, x), x, weight, bias, init_state,
@@ -65,6 +68,7 @@ class _Selective(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dfinal):
         u, delta, A, B, C, D, z, delta_bias, kept, lengths = ctx.saved_tensors
         g = ssd.selective_bwd(_rows(dy, u), u, delta, A, B, C, D, z, delta_bias, kept,
@@ -137,6 +141,7 @@ class SelectiveBlock(torch.nn.Module):
     @torch.no_grad()
     def step(self, x, state):
         """One token x [b, width]; state is moved on in place.  Returns y [b, width]."""
+        torch.autograd.graph.increment_version(state)      # a backward that still needs its old values then says so
         d, n, r = self.channels, self.dstate, self.rank
         h = ssd.norm_fwd(x, self.norm_weight, self.norm_bias)
         xz = F.linear(h, self.in_proj)

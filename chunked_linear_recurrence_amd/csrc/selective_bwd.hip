@@ -23,7 +23,7 @@
 // times N/16 blocks of states; their sums meet in LDS, and one partial sum per workgroup goes
 // to memory, added up in order by a last kernel, so that results do not depend on scheduling.
 //
-// 336 vector instructions a (token, 64 channels, 16 states) bound it: 2 x 4096 tokens of 2048
+// 340 vector instructions a (token, 64 channels, 16 states) bound it: 2 x 4096 tokens of 2048
 // channels take 235 us, the vector units busy for 76% of them with two waves a SIMD.
 #include "ssd_sel.h"
 

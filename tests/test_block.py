@@ -122,3 +122,21 @@ def test_decode_step_in_a_graph():
         assert torch.equal(out, ref[k]), k
     for a, b in zip(static, ref_state):
         assert torch.equal(a, b)
+
+
+def test_stale_state_and_second_derivatives_are_refused():
+    """A backward whose incoming state a step has overwritten since, and a derivative of a
+    gradient, which the kernels do not have, raise instead of giving wrong values."""
+    torch.manual_seed(7)
+    block = SelectiveBlock(32, rank=2, dtype=torch.float32, device=DEV)
+    x = torch.randn(2, 9, 32, device=DEV)
+    with torch.no_grad():
+        _, state = block(x)
+    y, _ = block(x, state)
+    block.step(x[:, 0], state)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    xg = x.clone().requires_grad_(True)
+    (dx,) = torch.autograd.grad(block(xg)[0].square().sum(), xg, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
