@@ -141,7 +141,6 @@ class SelectiveBlock(torch.nn.Module):
     @torch.no_grad()
     def step(self, x, state):
         """One token x [b, width]; state is moved on in place.  Returns y [b, width]."""
-        torch.autograd.graph.increment_version(state)      # a backward that still needs its old values then says so
         d, n, r = self.channels, self.dstate, self.rank
         h = ssd.norm_fwd(x, self.norm_weight, self.norm_bias)
         xz = F.linear(h, self.in_proj)

@@ -138,6 +138,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()      # ctypes passes ints as void *
 
 
+def _wrote(*tensors):
+    """The caller's tensors that a call has written (None: not given).  Autograd does not see a
+    write behind a pointer; with its version moved on, a backward that saved such a tensor raises
+    instead of reading the new values."""
+    written = [t for t in tensors if t is not None]
+    if written:
+        torch.autograd.graph.increment_version(written)
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -302,6 +311,7 @@ def fwd(x, dt, A, B, C, D=None, init_state=None, chunk=256, *, y=None, final_sta
                                         chunk, None, None, 0, None, 0, None))
     if workspace is None:
         workspace = alloc_workspace(nbytes, x.device)
+    given = (y, final_state)
     if y is None:
         y = torch.empty_like(x)
     if final_state is None and want_final:
@@ -314,6 +324,7 @@ def fwd(x, dt, A, B, C, D=None, init_state=None, chunk=256, *, y=None, final_sta
         _check(lib().ssd_chunk_scan_fwd(*args))
     else:
         _check(lib().ssd_chunk_scan_stages(*args, first_stage, last_stage))
+    _wrote(*given)
     return y, final_state
 
 
@@ -330,6 +341,7 @@ def fwd_noalloc(x, dt, A, B, C, D=None, init_state=None, chunk=256, *, y, final_
     _check(lib().ssd_chunk_scan_fwd_noalloc(ctypes.byref(dims), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
                                             _ptr(D), _ptr(init_state), chunk, _ptr(y), _ptr(final_state),
                                             flags, _stream(stream)))
+    _wrote(y, final_state)
     return y, final_state
 
 
@@ -345,12 +357,14 @@ def segmented(x0, dt, A, B, C, D, layer_states, V, chunk=256, *, y=None, residua
     nbytes = segmented_workspace_bytes(dims, chunk, V, n_layers, wavefront)
     if workspace is None:
         workspace = alloc_workspace(nbytes, x0.device)
+    given = y
     if y is None:
         y = torch.empty_like(x0)
     flags = (SSD_FLAG_RESIDUAL if residual else 0) | (SSD_FLAG_WAVEFRONT if wavefront else 0)
     _check(lib().ssd_chunk_scan_segmented(ctypes.byref(dims), n_layers, V, _ptr(x0), _ptr(dt), _ptr(A),
                                           _ptr(B), _ptr(C), _ptr(D), _ptr(layer_states), chunk, flags,
                                           _ptr(y), _ptr(workspace), workspace.numel(), _stream(stream)))
+    _wrote(given, layer_states)
     return y, layer_states
 
 
@@ -379,11 +393,13 @@ def step(x, dt, A, B, C, D, state, *, y=None, residual=False, stream=None):
     G, N = B.shape[1], B.shape[2]
     dtype = SSD_BF16 if x.dtype == torch.bfloat16 else SSD_F32
     dims = Dims(b, 1, H, P, N, G, dtype, 0)
+    given = y
     if y is None:
         y = torch.empty_like(x)
     flags = SSD_FLAG_RESIDUAL if residual else 0
     _check(lib().ssd_step(ctypes.byref(dims), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                           _ptr(state), _ptr(y), flags, _stream(stream)))
+    _wrote(given, state)
     return y
 
 
@@ -544,12 +560,14 @@ def conv_fwd(x, weight, bias=None, init_state=None, *, lengths=None, silu=True, 
         with ctx:
             return conv_fwd(x, weight, bias, init_state, lengths=lengths, silu=silu, y=y, final_state=final_state,
                             want_final=want_final)
+    given = (y, final_state)
     y = _out_like("y", y, x)
     if final_state is not None or (want_final and W > 1):
         final_state = _out("final_state", final_state, (b, W - 1, C), x.dtype, dev)
     dims = ConvDims(b, L, C, W, code, xb, xt, 0, 0)
     _check(L_.ssd_conv_fwd(dims, xp, wp, bp, ip, lp, y.data_ptr(), _ptr(final_state), SSD_FLAG_SILU if silu else 0,
                            _current(x)))
+    _wrote(*given)
     return y, final_state
 
 
@@ -570,9 +588,11 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stre
     if ctx is not None:
         with ctx:
             return conv_step(x, weight, bias, state, silu=silu, y=y, state_out=state_out)
+    given = y
     y = _out_like("y", y, x)
     dims = ConvDims(b, 1, C, W, code, xb, 0, 0, 0)
     _check(L_.ssd_conv_step(dims, xp, wp, bp, ip, op, y.data_ptr(), SSD_FLAG_SILU if silu else 0, _current(x)))
+    _wrote(given, state if state_out is None else state_out)
     return y
 
 
@@ -658,11 +678,13 @@ def selective_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state
             return selective_fwd(u, delta, A, B, C, D, z, delta_bias, init_state, lengths=lengths, softplus=softplus,
                                  y=y, final_state=final_state, keep=keep, workspace=workspace)
     ws = _workspace(workspace, L_.ssd_selective_fwd_workspace_bytes(dims), dev)
+    given = (y, final_state)
     y = _out_like("y", y, u)
     final_state = _out("final_state", final_state, st, torch.float32, dev)
     kept = torch.empty(L_.ssd_selective_kept_bytes(dims), dtype=torch.uint8, device=dev) if keep else None
     _check(L_.ssd_selective_fwd(dims, *ptrs, ip, lp, y.data_ptr(), final_state.data_ptr(), _ptr(kept),
                                 SSD_FLAG_SOFTPLUS if softplus else 0, ws.data_ptr(), ws.numel(), _current(u)))
+    _wrote(*given)
     return (y, final_state, kept) if keep else (y, final_state)
 
 
@@ -681,9 +703,11 @@ def selective_step(u, delta, A, B, C, D, z, delta_bias, state, *, softplus=True,
         with ctx:
             return selective_step(u, delta, A, B, C, D, z, delta_bias, state, softplus=softplus, y=y,
                                   state_out=state_out)
+    given = y
     y = _out_like("y", y, u)
     _check(L_.ssd_selective_step(dims, *ptrs, ip, op, y.data_ptr(), SSD_FLAG_SOFTPLUS if softplus else 0,
                                  _current(u)))
+    _wrote(given, state if state_out is None else state_out)
     return y
 
 
@@ -747,6 +771,7 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, want_stats=False, s
     if ctx is not None:
         with ctx:
             return norm_fwd(x, weight, bias, eps, y=y, want_stats=want_stats)
+    given = y
     y = _out_like("y", y, x)
     mean = rstd = None
     if want_stats:
@@ -754,6 +779,7 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, want_stats=False, s
         rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
     dims = NormDims(rows, d, code, 0, xs, 0)
     _check(L_.ssd_norm_fwd(dims, xp, wp, bp, eps, y.data_ptr(), _ptr(mean), _ptr(rstd), _current(x)))
+    _wrote(given)
     return (y, mean, rstd) if want_stats else y
 
 
