@@ -31,6 +31,7 @@ class _Norm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = ssd.norm_fwd(x, weight, bias, eps, want_stats=True)
         ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.has_bias = bias is not None
         return y
 
     @staticmethod
@@ -38,7 +39,7 @@ class _Norm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         g = ssd.norm_bwd(_rows(dy, x), x, weight, mean, rstd)
-        return g.dx, g.dweight, g.dbias, None
+        return g.dx, None if weight is None else g.dweight, g.dbias if ctx.has_bias else None, None
 
 
 class _Conv(torch.autograd.Function):
@@ -76,7 +77,7 @@ class _Selective(torch.autograd.Function):
         return (g.du, g.ddelta, g.dA, g.dB, g.dC, g.dD, g.dz, g.ddelta_bias, g.dinit if ctx.has_init else None, None)
 
 
-def norm(x, weight, bias, eps=1e-5):
+def norm(x, weight=None, bias=None, eps=1e-5):
     """ssd.norm_fwd with gradients: x [rows, channels]."""
     return _Norm.apply(x, weight, bias, eps)
 
