@@ -127,6 +127,17 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
 // carry) that enters it.  W is such that a wave has at most 16 chunks, whose values it then
 // holds in registers; it waits for memory once.
 constexpr int kPassChunks = 16;
+
+// 2^x h + s, x the exponent of many tokens' decays together.  Where rates are positive 2^x may be
+// beyond float32 although every token's decay and every state is within it: a state of zero stays
+// zero, and the product with another is formed in two steps, each factor within range unless the
+// result is not.
+__device__ __forceinline__ float joined(float x, float h, float s) {
+    const bool big = x > 126.f;
+    const float e = exp2_fast(big ? 0.5f * x : x);
+    return h == 0.f ? s : fmaf(e, big ? e * h : h, s);
+}
+
 template <bool REV, int W>
 __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
     constexpr int U = kPassChunks;
@@ -158,7 +169,7 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
             for (int i = 0; i < U; ++i) {
                 if (c + i < c1) {
                     if (write) S[slot(c + i) * cs] = h;
-                    h = fmaf(exp2_fast(A * d[i]), h, s[i]);
+                    h = joined(A * d[i], h, s[i]);
                     total += d[i];
                 }
             }
@@ -171,7 +182,7 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
         __syncthreads();
     }
     h = first ? first[(b * a.D + q.d) * (int64_t)a.N + n] : 0.f;
-    for (int w = 0; w < wave; ++w) h = fmaf(exp2_fast(A * part[w][1][lane]), h, part[w][0][lane]);
+    for (int w = 0; w < wave; ++w) h = joined(A * part[w][1][lane], h, part[w][0][lane]);
     walk(true);
 }
 
