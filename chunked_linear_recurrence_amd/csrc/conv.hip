@@ -314,7 +314,7 @@ static hipError_t conv_fwd_t(const ConvArgs &a, hipStream_t s) {
     const int TS = conv_tokens(a.batch, a.L, a.C, a.dtype, kConvFwdTokens);
     const int64_t nct = (a.C + 64 * V - 1) / (64 * V), ntb = (a.L + kConvWaves * TS - 1) / (kConvWaves * TS);
     const int64_t n = a.batch * ntb * nct;
-    if (n > INT32_MAX) return hipErrorInvalidValue;
+    if (!grid_fits(n, 256)) return hipErrorInvalidValue;
     conv_fwd_kernel<T, W, V><<<(uint32_t)n, 256, 0, s>>>(a, TS);
     return hipGetLastError();
 }
@@ -322,7 +322,7 @@ static hipError_t conv_fwd_t(const ConvArgs &a, hipStream_t s) {
 template <typename T, int W, int V>
 static hipError_t conv_step_t(const ConvArgs &a, hipStream_t s) {
     const int64_t n = (a.batch * ((a.C + V - 1) / V) + 63) / 64;
-    if (n > INT32_MAX) return hipErrorInvalidValue;
+    if (!grid_fits(n, 64)) return hipErrorInvalidValue;
     conv_step_kernel<T, W, V><<<(uint32_t)n, 64, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -330,12 +330,12 @@ static hipError_t conv_step_t(const ConvArgs &a, hipStream_t s) {
 template <typename T, int W, int V>
 static hipError_t conv_bwd_t(const ConvArgs &a, hipStream_t s) {
     const int64_t nct = (a.C + 64 * V - 1) / (64 * V), rows = conv_bwd_rows(a.batch, a.L, a.C, a.dtype);
-    if (rows * nct > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t sums = ((int64_t)(W + 1) * a.C + 63) / 64;
+    if (!grid_fits(rows * nct, 256) || !grid_fits(sums, 1024)) return hipErrorInvalidValue;
     conv_bwd_kernel<T, W, V><<<(uint32_t)(rows * nct), 256, 0, s>>>(a, conv_bwd_tokens(a.batch, a.L, a.C, a.dtype));
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t cols = (int64_t)(W + 1) * a.C;
-    conv_bwd_sum_kernel<<<(uint32_t)((cols + 63) / 64), 1024, 0, s>>>(a.part, rows, a.C, W, a.dw, a.dbias);
+    conv_bwd_sum_kernel<<<(uint32_t)sums, 1024, 0, s>>>(a.part, rows, a.C, W, a.dw, a.dbias);
     return hipGetLastError();
 }
 

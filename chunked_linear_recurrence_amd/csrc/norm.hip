@@ -332,9 +332,13 @@ static hipError_t norm_fwd_t(const NormArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Workgroups of the sums over rows; rows that registers hold have far fewer columns than a launch.
+static int64_t norm_sum_blocks(const NormArgs &a) { return (2 * (int64_t)a.D + 63) / 64; }
+static bool norm_sum_fits(const NormArgs &a) { return (!a.dw && !a.db) || grid_fits(norm_sum_blocks(a), 1024); }
+
 static hipError_t norm_bwd_sum(const NormArgs &a, int64_t blocks, hipStream_t s) {
     if (!a.dw && !a.db) return hipSuccess;
-    norm_bwd_sum_kernel<<<(uint32_t)((2 * (int64_t)a.D + 63) / 64), 1024, 0, s>>>(a.part, (int)blocks, a.D, a.dw, a.db);
+    norm_bwd_sum_kernel<<<(uint32_t)norm_sum_blocks(a), 1024, 0, s>>>(a.part, (int)blocks, a.D, a.dw, a.db);
     return hipGetLastError();
 }
 
@@ -351,14 +355,14 @@ static hipError_t norm_bwd_t(const NormArgs &a, hipStream_t s) {
 
 template <typename T>
 static hipError_t norm_fwd_wide_t(const NormArgs &a, hipStream_t s) {
-    if (a.rows > INT32_MAX) return hipErrorInvalidValue;
+    if (!grid_fits(a.rows, 1024)) return hipErrorInvalidValue;
     norm_fwd_wide_kernel<T><<<(uint32_t)a.rows, 1024, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t norm_bwd_wide_t(const NormArgs &a, hipStream_t s) {
-    if (a.rows > INT32_MAX) return hipErrorInvalidValue;
+    if (!grid_fits(a.rows, 1024) || !norm_sum_fits(a)) return hipErrorInvalidValue;
     norm_bwd_wide_kernel<T><<<(uint32_t)a.rows, 1024, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!a.dw && !a.db)) return e;

@@ -331,14 +331,15 @@ void sel_chunks(int64_t waves, const SelCut &cut, int64_t L, int *nc, int *T) {
 
 static hipError_t sel_grid(int64_t units, uint32_t *blocks) {
     const int64_t n = (units + kSelWaves - 1) / kSelWaves;
-    if (n < 1 || n > INT32_MAX) return hipErrorInvalidValue;
+    if (n < 1 || !grid_fits(n, 64 * kSelWaves)) return hipErrorInvalidValue;
     *blocks = (uint32_t)n;
     return hipSuccess;
 }
 
+// Several chunks are cut only where a chunk has fewer than 2048 waves, so the grids of (1) and (2)
+// are far below a launch's limit.
 hipError_t launch_sel_pass(const SelArgs &a, bool reverse, hipStream_t s) {
     const int64_t n = a.batch * a.G * a.tiles * a.N;
-    if (n > INT32_MAX) return hipErrorInvalidValue;
 #define SEL_PASS(W)                                                                        \
     do {                                                                                   \
         if (reverse) sel_pass_kernel<true, W><<<(uint32_t)n, 64 * W, 0, s>>>(a);           \
@@ -372,7 +373,7 @@ static hipError_t sel_fwd_t(const SelArgs &a, hipStream_t s) {
 template <typename T, int N>
 static hipError_t sel_step_t(const SelStepArgs &a, hipStream_t s) {
     const int64_t n = (a.batch * a.D * (N / 4) + 255) / 256;
-    if (n > INT32_MAX) return hipErrorInvalidValue;
+    if (!grid_fits(n, 256)) return hipErrorInvalidValue;
     sel_step_kernel<T, N><<<(uint32_t)n, 256, 0, s>>>(a);
     return hipGetLastError();
 }

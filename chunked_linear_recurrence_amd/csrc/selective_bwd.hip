@@ -338,15 +338,15 @@ __global__ __launch_bounds__(1024) void sel_bwd_par_kernel(SelArgs a) {
 template <typename T, int N>
 static hipError_t sel_bwd_t(const SelArgs &a, hipStream_t s) {
     const int parts = sel_bwd_parts(a.D, a.G, N);
+    const int64_t blocks = a.batch * a.nc * a.G * parts;
+    const int64_t sums = (a.batch * a.L * a.G * a.N * 2 + 255) / 256;
+    const int64_t pars = (int64_t)a.G * a.tiles * (N + 2);
+    if (!grid_fits(blocks, 256) || !grid_fits(sums, 256) || !grid_fits(pars, 1024)) return hipErrorInvalidValue;
     hipError_t e;
     if (a.nc > 1) {
         if ((e = launch_sel_local_reverse(a, s)) != hipSuccess) return e;
         if ((e = launch_sel_pass(a, true, s)) != hipSuccess) return e;
     }
-    const int64_t blocks = a.batch * a.nc * a.G * parts;
-    const int64_t sums = (a.batch * a.L * a.G * a.N * 2 + 255) / 256;
-    const int64_t pars = (int64_t)a.G * a.tiles * (N + 2);
-    if (blocks > INT32_MAX || sums > INT32_MAX || pars > INT32_MAX) return hipErrorInvalidValue;
     if (a.z.p) sel_bwd_kernel<T, N, true><<<(uint32_t)blocks, 256, 0, s>>>(a);
     else sel_bwd_kernel<T, N, false><<<(uint32_t)blocks, 256, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;

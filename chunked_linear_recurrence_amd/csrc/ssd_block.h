@@ -19,6 +19,10 @@ __device__ __forceinline__ const T *row_of(const View &v, int64_t b, int64_t t) 
     return reinterpret_cast<const T *>(v.p) + b * v.bs + t * v.ts;
 }
 
+// A launch holds fewer than 2^32 threads along a dimension.  A call of several launches checks
+// all of them before the first.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 struct ConvArgs {
     int64_t batch;
     int L, C, W, dtype;

@@ -246,6 +246,8 @@ ssd_status_t ssd_step(const ssd_dims_t *dims, const void *x, const void *dt, con
  *   row's own tokens, clamped to 0..seqlen.  Tokens past a row's length are not read into
  *   any result (whatever they hold), their outputs and gradients are 0, and the final state
  *   is the one after the row's last token (the initial state of an empty row).
+ * Range.  A call whose work exceeds one launch of the device (2^32 threads) is refused with
+ *   SSD_ERR_UNSUPPORTED.
  * Arithmetic.  Everything is computed in float32 and rounded once when stored in the
  *   activation dtype; parameters, their gradients and the scan's states are float32.
  *   Sums over tokens, rows and channels are added in a fixed order: results do not change
