@@ -59,6 +59,27 @@ ssd_status_t check_tensors(const Tensor *in, int nin, const Tensor *out, int nou
     return SSD_OK;
 }
 
+// The dims with the strides over dimensions of one element, which nothing uses, as 0: they are
+// neither checked nor looked at where a kernel is chosen.
+ssd_conv_dims_t used(ssd_conv_dims_t d) {
+    if (d.batch == 1) d.x_batch_stride = d.dy_batch_stride = 0;
+    if (d.seqlen == 1) d.x_token_stride = d.dy_token_stride = 0;
+    return d;
+}
+ssd_selective_dims_t used(ssd_selective_dims_t d) {
+    if (d.batch == 1)
+        d.u_batch_stride = d.delta_batch_stride = d.z_batch_stride = d.B_batch_stride = d.C_batch_stride =
+            d.dy_batch_stride = 0;
+    if (d.seqlen == 1)
+        d.u_token_stride = d.delta_token_stride = d.z_token_stride = d.B_token_stride = d.C_token_stride =
+            d.dy_token_stride = 0;
+    return d;
+}
+ssd_norm_dims_t used(ssd_norm_dims_t d) {
+    if (d.rows == 1) d.x_row_stride = d.dy_row_stride = 0;
+    return d;
+}
+
 ssd_status_t check_dtype(int32_t dtype) {
     if (dtype != SSD_F32 && dtype != SSD_BF16)
         return fail(SSD_ERR_BAD_DTYPE, "dtype %d is not SSD_F32 (0) or SSD_BF16 (1)", dtype);
@@ -202,7 +223,7 @@ size_t sel_kept(const ssd_selective_dims_t &d) {
 }
 
 // Bytes spanned by u, delta, z, B, C and dy, in this order; 0 for one that is not there, whose
-// strides are not looked at.  A step has no token strides.
+// strides are not looked at.
 ssd_status_t sel_spans(const ssd_selective_dims_t &d, const void *z, const void *dy, bool step, size_t out[6]) {
     const int64_t e = act_bytes(d.dtype), gn = d.ngroups * d.dstate;
     const int64_t bs[] = {d.u_batch_stride, d.delta_batch_stride, d.z_batch_stride, d.B_batch_stride, d.C_batch_stride,
@@ -212,7 +233,7 @@ ssd_status_t sel_spans(const ssd_selective_dims_t &d, const void *z, const void 
     for (int i = 0; i < 6; ++i) {
         out[i] = 0;
         if ((i == 2 && !z) || (i == 5 && !dy)) continue;
-        const int64_t t = step ? 0 : ts[i];
+        const int64_t t = ts[i];
         const bool coef = i == 3 || i == 4;
         if (!span(d.batch, bs[i], d.seqlen, t, coef ? gn : d.channels, e, &out[i]))
             return fail(SSD_ERR_BAD_SHAPE, "strides must be >= 0 and spans below 2^58 elements");
@@ -249,7 +270,7 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_dims_t *dims, const void *x, const floa
                           const void *init_state, const int32_t *lengths, void *y, void *final_state, uint32_t flags,
                           void *stream) {
     TRY(check_conv(dims, false));
-    const ssd_conv_dims_t &d = *dims;
+    const ssd_conv_dims_t d = used(*dims);
     if (!x || !weight || !y) return fail(SSD_ERR_NULL_ARG, "x, weight and y must be non-NULL");
     if (flags & ~SSD_FLAG_SILU) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
     const size_t e = (size_t)act_bytes(d.dtype), C = (size_t)d.channels;
@@ -272,7 +293,7 @@ ssd_status_t ssd_conv_fwd(const ssd_conv_dims_t *dims, const void *x, const floa
 ssd_status_t ssd_conv_step(const ssd_conv_dims_t *dims, const void *x, const float *weight, const float *bias,
                            const void *state_in, void *state_out, void *y, uint32_t flags, void *stream) {
     TRY(check_conv(dims, true));
-    const ssd_conv_dims_t &d = *dims;
+    const ssd_conv_dims_t d = used(*dims);
     if (!x || !weight || !state_in || !state_out || !y)
         return fail(SSD_ERR_NULL_ARG, "x, weight, state_in, state_out and y must be non-NULL");
     if (flags & ~SSD_FLAG_SILU) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
@@ -300,7 +321,7 @@ ssd_status_t ssd_conv_bwd(const ssd_conv_dims_t *dims, const void *dy, const voi
                           void *dx, float *dweight, float *dbias, void *dinit, uint32_t flags, void *workspace,
                           size_t workspace_bytes, void *stream) {
     TRY(check_conv(dims, false));
-    const ssd_conv_dims_t &d = *dims;
+    const ssd_conv_dims_t d = used(*dims);
     if (!dy || !x || !weight || !dx || !dweight)
         return fail(SSD_ERR_NULL_ARG, "dy, x, weight, dx and dweight must be non-NULL");
     if (flags & ~SSD_FLAG_SILU) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
@@ -350,7 +371,7 @@ ssd_status_t ssd_selective_fwd(const ssd_selective_dims_t *dims, const void *u, 
                                const float *init_state, const int32_t *lengths, void *y, float *final_state, void *kept,
                                uint32_t flags, void *workspace, size_t workspace_bytes, void *stream) {
     TRY(check_sel(dims, false));
-    const ssd_selective_dims_t &d = *dims;
+    const ssd_selective_dims_t d = used(*dims);
     if (!u || !delta || !A || !B || !C || !y)
         return fail(SSD_ERR_NULL_ARG, "u, delta, A, B, C and y must be non-NULL");
     if (flags & ~SSD_FLAG_SOFTPLUS) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
@@ -397,7 +418,7 @@ ssd_status_t ssd_selective_step(const ssd_selective_dims_t *dims, const void *u,
                                 const void *B, const void *C, const float *D, const void *z, const float *delta_bias,
                                 const float *state_in, float *state_out, void *y, uint32_t flags, void *stream) {
     TRY(check_sel(dims, true));
-    const ssd_selective_dims_t &d = *dims;
+    const ssd_selective_dims_t d = used(*dims);
     if (!u || !delta || !A || !B || !C || !state_in || !state_out || !y)
         return fail(SSD_ERR_NULL_ARG, "u, delta, A, B, C, state_in, state_out and y must be non-NULL");
     if (flags & ~SSD_FLAG_SOFTPLUS) return fail(SSD_ERR_BAD_SHAPE, "unknown flag bits 0x%x", flags);
@@ -446,7 +467,7 @@ ssd_status_t ssd_selective_bwd(const ssd_selective_dims_t *dims, const void *dy,
                                float *ddelta_bias, float *dinit, uint32_t flags, void *workspace,
                                size_t workspace_bytes, void *stream) {
     TRY(check_sel(dims, false));
-    const ssd_selective_dims_t &d = *dims;
+    const ssd_selective_dims_t d = used(*dims);
     if (!dy || !u || !delta || !A || !B || !C || !kept || !du || !ddelta || !dA || !dB || !dC)
         return fail(SSD_ERR_NULL_ARG, "dy, u, delta, A, B, C, kept, du, ddelta, dA, dB and dC must be non-NULL");
     if ((z != nullptr) != (dz != nullptr)) return fail(SSD_ERR_NULL_ARG, "dz must be given exactly if z is");
@@ -503,7 +524,7 @@ ssd_status_t ssd_selective_bwd(const ssd_selective_dims_t *dims, const void *dy,
 ssd_status_t ssd_norm_fwd(const ssd_norm_dims_t *dims, const void *x, const float *weight, const float *bias, float eps,
                           void *y, float *mean, float *rstd, void *stream) {
     TRY(check_norm(dims));
-    const ssd_norm_dims_t &d = *dims;
+    const ssd_norm_dims_t d = used(*dims);
     if (!x || !y) return fail(SSD_ERR_NULL_ARG, "x and y must be non-NULL");
     if (!(eps >= 0.f) || isinf(eps)) return fail(SSD_ERR_BAD_SHAPE, "eps must be finite and >= 0");
     const size_t e = (size_t)act_bytes(d.dtype), ch = (size_t)d.channels, rows = (size_t)d.rows;
@@ -537,7 +558,7 @@ ssd_status_t ssd_norm_bwd(const ssd_norm_dims_t *dims, const void *dy, const voi
                           const float *mean, const float *rstd, void *dx, float *dweight, float *dbias,
                           void *workspace, size_t workspace_bytes, void *stream) {
     TRY(check_norm(dims));
-    const ssd_norm_dims_t &d = *dims;
+    const ssd_norm_dims_t d = used(*dims);
     if (!dy || !x || !mean || !rstd || !dx) return fail(SSD_ERR_NULL_ARG, "dy, x, mean, rstd and dx must be non-NULL");
     const size_t need = norm_ws(d);
     if (!workspace || workspace_bytes < need)

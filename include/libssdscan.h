@@ -237,7 +237,8 @@ ssd_status_t ssd_step(const ssd_dims_t *dims, const void *x, const void *dt, con
  *
  * Strides.  An activation input may be a view: rows of contiguous channels at any
  *   batch and token stride (elements, >= 0), for example one half of a projection's output.
- *   The strides are fields of the dims.  Outputs, states and parameters are contiguous.
+ *   The strides are fields of the dims; those over a dimension of one element, and those of a
+ *   tensor that is not given, are not looked at.  Outputs, states and parameters are contiguous.
  * Alignment.  Pointers are aligned to their element size; B and C rows, in bfloat16, to 4
  *   bytes (even strides) except for a single token.  Where addresses and sizes allow 16-byte accesses, the
  *   convolution and the norm use them; results are the same either way.  Single-token
