@@ -123,12 +123,16 @@ class SelectiveBlock(torch.nn.Module):
         self.out_proj = matrix(width, d)
 
     def forward(self, x, state=None, lengths=None):
-        """x [b, L, width]; state as returned (None: zeros); lengths [b] int32.  Returns
-        (y [b, L, width], state)."""
+        """x [b, L, width]; state as returned (None: zeros); lengths [b] int32: each row's own
+        tokens.  What x holds past them reaches no result and no gradient but the residual's own.
+        Returns (y [b, L, width], state)."""
         b, L, _ = x.shape
         d, n, r = self.channels, self.dstate, self.rank
         conv_state, scan_state = state if state is not None else (None, None)
-        h = norm(x.reshape(b * L, self.width), self.norm_weight, self.norm_bias)
+        own = x
+        if lengths is not None:      # the norm and the projections take every row; 0 x NaN would reach their weights
+            own = x.masked_fill((torch.arange(L, device=x.device) >= lengths[:, None])[..., None], 0)
+        h = norm(own.reshape(b * L, self.width), self.norm_weight, self.norm_bias)
         xz = F.linear(h, self.in_proj).view(b, L, 2 * d)
         u, conv_state = conv(xz[..., :d], self.conv_weight, self.conv_bias, conv_state, lengths)
         p = F.linear(u.view(b * L, d), self.x_proj)

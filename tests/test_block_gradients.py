@@ -44,3 +44,29 @@ def test_norm_with_and_without_parameters(weight, bias):
     for name, t, tol in zip(("x", "weight", "bias"), leaves, (2e-5, 1e-4, 1e-4)):
         if t is not None:
             R.check(t.grad, next(grads), torch.float32, tol, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad", [float("nan"), float("inf")])
+def test_what_lies_past_a_row_s_end_reaches_nothing(pad, dtype):
+    """A ragged batch's padding may hold anything: outputs and states of the rows' own tokens and
+    every gradient are those of a batch padded with zeros, bit for bit."""
+    torch.manual_seed(8)
+    m = block.SelectiveBlock(48, rank=4, dtype=dtype, device=DEV)
+    lengths = torch.tensor([40, 0, 23], dtype=torch.int32, device=DEV)
+    inside = torch.arange(40, device=DEV)[None] < lengths[:, None]
+    x, dy = torch.randn(3, 40, 48, device=DEV).to(dtype), torch.randn(3, 40, 48, device=DEV).to(dtype)
+    dy[~inside] = 0
+    got = []
+    for value in (0.0, pad):
+        xp = x.clone()
+        xp[~inside] = value
+        xp.requires_grad_(True)
+        m.zero_grad()
+        y, state = m(xp, lengths=lengths)
+        y.backward(dy)
+        got.append([y[inside], *state, xp.grad] + [p.grad.clone() for p in m.parameters()])
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
