@@ -22,6 +22,8 @@
 // and the sum of its dt; (2) the states passed from chunk to chunk,
 // h <- exp(A sum dt) h + S; (3) every chunk again from the state that enters it.  (1) and (2)
 // are skipped where there are waves enough without.
+#include <type_traits>
+
 #include "ssd_sel.h"
 
 namespace ssd {
@@ -129,13 +131,15 @@ __global__ __launch_bounds__(256) void sel_local_kernel(SelArgs a) {
 constexpr int kPassChunks = 16;
 
 // 2^x h + s, x the exponent of many tokens' decays together.  Where rates are positive 2^x may be
-// beyond float32 although every token's decay and every state is within it: a state of zero stays
-// zero, and the product with another is formed in two steps, each factor within range unless the
-// result is not.
+// beyond float32 although every token's decay and every state is within it.  BIG: some lane's x is
+// above 127, and 2^x is taken as two finite factors: a state of zero stays zero, and another
+// overflows only where the result does.
+template <bool BIG>
 __device__ __forceinline__ float joined(float x, float h, float s) {
-    const bool big = x > 126.f;
-    const float e = exp2_fast(big ? 0.5f * x : x);
-    return h == 0.f ? s : fmaf(e, big ? e * h : h, s);
+    if (!BIG) return fmaf(exp2_fast(x), h, s);
+    const bool big = x > 127.f;
+    const float e = exp2_fast(big ? 127.f : x), more = exp2_fast(big ? fminf(x - 127.f, 127.f) : 0.f);
+    return fmaf(e, more * h, s);
 }
 
 template <bool REV, int W>
@@ -165,14 +169,21 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
                     d[i] = sd[at * ds];
                 }
             }
+            bool big = false;
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (c + i < c1) {
-                    if (write) S[slot(c + i) * cs] = h;
-                    h = joined(A * d[i], h, s[i]);
-                    total += d[i];
+            for (int i = 0; i < U; ++i) big |= A * d[i] > 127.f;
+            auto steps = [&](auto any_big) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    if (c + i < c1) {
+                        if (write) S[slot(c + i) * cs] = h;
+                        h = joined<any_big()>(A * d[i], h, s[i]);
+                        total += d[i];
+                    }
                 }
-            }
+            };
+            if (__any(big)) steps(std::true_type());
+            else steps(std::false_type());
         }
     };
     if (W > 1) {
@@ -182,7 +193,7 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
         __syncthreads();
     }
     h = first ? first[(b * a.D + q.d) * (int64_t)a.N + n] : 0.f;
-    for (int w = 0; w < wave; ++w) h = joined(A * part[w][1][lane], h, part[w][0][lane]);
+    for (int w = 0; w < wave; ++w) h = joined<true>(A * part[w][1][lane], h, part[w][0][lane]);
     walk(true);
 }
 
