@@ -142,9 +142,7 @@ def _wrote(*tensors):
     """The caller's tensors that a call has written (None: not given).  Autograd does not see a
     write behind a pointer; with its version moved on, a backward that saved such a tensor raises
     instead of reading the new values."""
-    written = [t for t in tensors if t is not None]
-    if written:
-        torch.autograd.graph.increment_version(written)
+    torch._C._increment_version([t for t in tensors if t is not None])
 
 
 def _stream(stream):
@@ -779,7 +777,8 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, want_stats=False, s
         rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
     dims = NormDims(rows, d, code, 0, xs, 0)
     _check(L_.ssd_norm_fwd(dims, xp, wp, bp, eps, y.data_ptr(), _ptr(mean), _ptr(rstd), _current(x)))
-    _wrote(given)
+    if given is not None:
+        _wrote(given)
     return (y, mean, rstd) if want_stats else y
 
 
