@@ -35,6 +35,14 @@ constexpr int kSB = 16;                  // states per wave
 // row and the reads down a column are free of bank conflicts.
 constexpr int kRow = 20, kQuarter = 16 * kRow + 16;
 
+// Orders a wave's LDS operations in the program, where its lanes read what other lanes wrote: the
+// wave issues them in order, and this keeps the compiler from moving one past another.  No
+// instruction.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <typename T, int N, bool GATE>
 __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     constexpr int NB = N / kSB, TPB = 4 / NB, K = kKeep;
@@ -113,8 +121,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(SelArgs a) {
     // added up after its arithmetic.
     float col[16];
     auto column_read = [&]() {
+        wave_order();
 #pragma unroll
         for (int k = 0; k < 16; ++k) col[k] = column[k * kRow];
+        wave_order();
     };
     auto column_sum = [&]() {
         float s[4];
