@@ -56,3 +56,70 @@ def test_growth_beyond_float32_s_range_of_a_small_state():
     yr, fr, _ = reference(t, ("D", "z", "bias", "st"), False, want=False)
     R.check(f, fr, torch.float32, TOL, "final_state")
     R.check(y, yr, torch.float32, TOL, "y")
+
+
+# ---- which way a sequence is cut: one pass by its waves, and chunks longer than the shortest
+def chunks(b, L, d, N, G, dims):
+    """Chunks of the forward's cut, from the workspace it asks for (0: one pass)."""
+    tiles = G * -(-(d // G) // 64)
+    return ssd.lib().ssd_selective_fwd_workspace_bytes(dims) // (b * tiles * 64 * 4 * (N + 1))
+
+
+def backward_in_one_pass(b, L, d, N, G, dims):
+    """Whether the backward's workspace is that of its partial sums alone."""
+    up = lambda v: -(-v // 256) * 256
+    tiles = -(-(d // G) // 64)
+    parts = -(-tiles // (64 // N))
+    return ssd.lib().ssd_selective_bwd_workspace_bytes(dims) == (
+        up(parts * b * L * G * 2 * N * 4) + up(b * G * tiles * 64 * 4 * (N + 2)))
+
+
+def check_sampled_rows(shape, dtype, one_pass):
+    """Every output and gradient against float64.  Upstream gradients are zero in all rows but
+    four, which then give the whole of dA, dD and ddelta_bias.  delta and dy are views into wider
+    rows, each with strides of its own."""
+    b, L, d, N, G = shape
+    t = make(b, L, d, N, G, dtype, seed=b + L, ragged=True, pad=float("nan"), extra=2)
+    rows = [0, 1, b // 2, b - 1]
+    t["lengths"][b // 2] = L - 5
+    other = [i for i in range(b) if i not in rows]
+    t["dy"][other], t["df"][other] = 0, 0
+    for i in rows:
+        t["dy"][i] = torch.randn(L, d, generator=torch.Generator().manual_seed(i)).to(dtype)
+        t["delta"][i] = torch.nan_to_num(t["delta"][i], nan=0.25)
+        t["uz"][i], t["bc"][i] = torch.nan_to_num(t["uz"][i], nan=0.5), torch.nan_to_num(t["bc"][i], nan=0.5)
+    g = on_gpu(t)
+    for key, extra in (("delta", 6), ("dy", 10)):
+        wide = torch.zeros(b, L, d + extra, dtype=dtype, device=DEV)
+        wide[..., extra // 2:extra // 2 + d] = g[key]
+        g[key] = wide[..., extra // 2:extra // 2 + d]
+    dims = ssd._selective_inputs(*(g[k] for k in KEYS), False, g["dy"])[0]
+    n = chunks(b, L, d, N, G, dims)
+    if one_pass:
+        assert n == 0 and L > 32 and backward_in_one_pass(b, L, d, N, G, dims)
+    else:
+        assert n > 1 and n * 16 < L and not backward_in_one_pass(b, L, d, N, G, dims)
+    y, f, kept = ssd.selective_fwd(*(g[k] for k in KEYS), g["st"], lengths=g["lengths"], keep=True)
+    r = ssd.selective_bwd(g["dy"], *(g[k] for k in KEYS), kept, dfinal=g["df"], lengths=g["lengths"])
+    torch.cuda.synchronize()
+    sub = {k: (v[rows].contiguous() if k in ("uz", "delta", "bc", "st", "dy", "df", "lengths") else v)
+           for k, v in t.items() if k not in ("u", "z", "B", "C")}
+    yr, fr, gr = reference(views(sub), ("D", "z", "bias", "st"), True)
+    R.check(y[rows], yr, dtype, TOL, "y")
+    R.check(f[rows], fr, torch.float32, TOL, "final_state")
+    for name, key in GRADS:
+        got = getattr(r, name)
+        whole = name in ("dA", "dD", "ddelta_bias")
+        R.check(got if whole else got[rows], gr[key], torch.float32 if whole or name == "dinit" else dtype, TOL, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(800, 57, 128, 16, 1), (790, 45, 130, 32, 2), (520, 70, 192, 64, 1)], ids=str)
+def test_one_pass_by_the_number_of_waves(shape, dtype):
+    check_sampled_rows(shape, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(30, 450, 1600, 16, 2), (40, 500, 1110, 32, 2), (44, 400, 640, 64, 1)], ids=str)
+def test_chunks_longer_than_the_shortest(shape, dtype):
+    check_sampled_rows(shape, dtype, False)
