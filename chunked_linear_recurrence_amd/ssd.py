@@ -138,11 +138,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()      # ctypes passes ints as void *
 
 
+# Moves the versions of the tensors of a sequence on (torch.autograd.graph.increment_version
+# without its own checks: a single-token call counts in tenths of a microsecond).
+_move_on = torch._C._increment_version
+
+
 def _wrote(*tensors):
     """The caller's tensors that a call has written (None: not given).  Autograd does not see a
     write behind a pointer; with its version moved on, a backward that saved such a tensor raises
     instead of reading the new values."""
-    torch._C._increment_version([t for t in tensors if t is not None])
+    _move_on([t for t in tensors if t is not None])
 
 
 def _stream(stream):
@@ -397,7 +402,7 @@ def step(x, dt, A, B, C, D, state, *, y=None, residual=False, stream=None):
     flags = SSD_FLAG_RESIDUAL if residual else 0
     _check(lib().ssd_step(ctypes.byref(dims), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                           _ptr(state), _ptr(y), flags, _stream(stream)))
-    _wrote(given, state)
+    _move_on((state,) if given is None else (state, given))
     return y
 
 
@@ -590,7 +595,8 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, state_out=None, stre
     y = _out_like("y", y, x)
     dims = ConvDims(b, 1, C, W, code, xb, 0, 0, 0)
     _check(L_.ssd_conv_step(dims, xp, wp, bp, ip, op, y.data_ptr(), SSD_FLAG_SILU if silu else 0, _current(x)))
-    _wrote(given, state if state_out is None else state_out)
+    moved = state if state_out is None else state_out
+    _move_on((moved,) if given is None else (moved, given))
     return y
 
 
@@ -705,7 +711,8 @@ def selective_step(u, delta, A, B, C, D, z, delta_bias, state, *, softplus=True,
     y = _out_like("y", y, u)
     _check(L_.ssd_selective_step(dims, *ptrs, ip, op, y.data_ptr(), SSD_FLAG_SOFTPLUS if softplus else 0,
                                  _current(u)))
-    _wrote(given, state if state_out is None else state_out)
+    moved = state if state_out is None else state_out
+    _move_on((moved,) if given is None else (moved, given))
     return y
 
 
