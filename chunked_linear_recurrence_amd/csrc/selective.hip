@@ -169,9 +169,10 @@ __global__ __launch_bounds__(64 * W) void sel_pass_kernel(SelArgs a) {
                     d[i] = sd[at * ds];
                 }
             }
+            const float again = hidden_lane(A);      // the products are formed where they are used, not held
             bool big = false;
 #pragma unroll
-            for (int i = 0; i < U; ++i) big |= A * d[i] > 127.f;
+            for (int i = 0; i < U; ++i) big |= again * d[i] > 127.f;
             auto steps = [&](auto any_big) {
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
