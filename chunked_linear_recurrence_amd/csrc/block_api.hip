@@ -259,7 +259,7 @@ ssd_status_t check_norm(const ssd_norm_dims_t *d) {
 }
 
 size_t norm_ws(const ssd_norm_dims_t &d) {
-    return align_up((size_t)ssd::norm_bwd_blocks(d.rows, d.channels) * 2 * (size_t)d.channels * 4);
+    return align_up((size_t)ssd::norm_bwd_blocks(d.rows) * 2 * (size_t)d.channels * 4);
 }
 
 }  // namespace

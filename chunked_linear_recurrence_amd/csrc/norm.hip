@@ -321,7 +321,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_sum_kernel(const float *part, i
     } else if (db) db[col - D] = s;
 }
 
-int64_t norm_bwd_blocks(int64_t rows, int64_t D) { return rows < kNormBwdBlocks ? rows : kNormBwdBlocks; }
+int64_t norm_bwd_blocks(int64_t rows) { return rows < kNormBwdBlocks ? rows : kNormBwdBlocks; }
 
 template <typename T, int V, int K, int WPR>
 static hipError_t norm_fwd_t(const NormArgs &a, hipStream_t s) {
@@ -346,7 +346,7 @@ template <typename T, int V, int K, int WPR>
 static hipError_t norm_bwd_t(const NormArgs &a, hipStream_t s) {
     constexpr int R = norm_rows<WPR>();
     int64_t n = (a.rows + R - 1) / R;
-    const int64_t cap = norm_bwd_blocks(a.rows, a.D);
+    const int64_t cap = norm_bwd_blocks(a.rows);
     if (n > cap) n = cap;
     norm_bwd_kernel<T, V, K, WPR><<<(uint32_t)n, norm_threads<WPR>(), 0, s>>>(a);
     hipError_t e = hipGetLastError();
@@ -366,7 +366,7 @@ static hipError_t norm_bwd_wide_t(const NormArgs &a, hipStream_t s) {
     norm_bwd_wide_kernel<T><<<(uint32_t)a.rows, 1024, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (!a.dw && !a.db)) return e;
-    const int64_t n = norm_bwd_blocks(a.rows, a.D);
+    const int64_t n = norm_bwd_blocks(a.rows);
     norm_bwd_cols_kernel<T><<<dim3((a.D + 255) / 256, (uint32_t)n), 256, 0, s>>>(a);
     e = hipGetLastError();
     return e != hipSuccess ? e : norm_bwd_sum(a, n, s);

@@ -65,7 +65,7 @@ struct NormArgs {
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s);
-int64_t norm_bwd_blocks(int64_t rows, int64_t D);
+int64_t norm_bwd_blocks(int64_t rows);
 
 // Tokens between two kept states of the selective scan.
 constexpr int kKeep = 8;
@@ -81,7 +81,7 @@ struct SelArgs {
     const int32_t *lengths;       // [batch] or null
     void *y;                      // [batch, L, D]
     float *final_state;           // [batch, D, N] or null
-    float *keep;                  // kept states or null (see sel_keep_floats)
+    float *keep;                  // kept states or null (where each lies: sel_keep_slot)
     int tiles;                    // tiles of 64 channels per group
     int nc, T;                    // chunks and tokens per chunk (T a multiple of kKeep)
     float *S;                     // workspace [batch, nc, G*tiles, N, 64]
