@@ -88,7 +88,9 @@ def conv(x, weight, bias=None, init_state=None, lengths=None):
 
 
 def selective(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state=None, lengths=None):
-    """ssd.selective_fwd with gradients; (y, final_state)."""
+    """ssd.selective_fwd with gradients; (y, final_state).  The states that the backward needs are
+    kept by every call (dstate / 2 bytes a token and channel), with gradients switched off too;
+    ssd.selective_fwd by itself keeps none."""
     return _Selective.apply(u, delta, A, B, C, D, z, delta_bias, init_state, lengths)
 
 

@@ -167,10 +167,12 @@ ssd_status_t check_sel(const ssd_selective_dims_t *d, bool step) {
     return SSD_OK;
 }
 
-// How a sequence is cut into chunks: waves that the chunks come to together (8 on each of 1024
-// SIMDs in the forward, 4 in the backward, of which its large kernel holds 2 at a time), and
-// from how many waves of a single pass on, and up to how many tokens, one pass is taken.
-// Measured, 16 states, bfloat16.  Waves: 32768 tokens of 2048 channels take 572 us with 2048
+// How a sequence is cut into chunks: waves that the chunks come to together (8 for each of 1024
+// SIMDs in the forward, 4 in the backward), and from how many waves of a single pass on, and up
+// to how many tokens, one pass is taken.  Fewer are resident at a time: (3) takes 72 registers
+// with 16 states in bfloat16 (7 waves a SIMD; 5 in float32), 108 to 123 with 32 (4) and 188 to
+// 219 with 64 (2); the backward's large kernel holds 2.  Measured with 16 states in bfloat16
+// alone, and taken for the other sizes as it is.  Waves: 32768 tokens of 2048 channels take 572 us with 2048
 // waves, 443 with 4096, 401 with 8192, 406 with 12288; forward and backward of 2 x 4096 tokens
 // 464, 433, 434, 440 by the forward's, and 443, 434, - and 444 by the backward's.  One pass, 256
 // and 1024 tokens of 2048 channels: 143 and 562 us with 1280 waves against 137 and 467 in chunks,

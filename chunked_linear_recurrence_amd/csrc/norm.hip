@@ -13,7 +13,8 @@
 // dw and db: each workgroup walks many rows with one running sum per column in float32,
 // leaves one row of partial sums, and a second kernel adds those rows in order, so results
 // do not depend on scheduling.  32768 rows of 2048 channels in bfloat16: 50 us forward
-// (5.4 TB/s), 84 + 5 us backward (4.8).
+// (5.4 TB/s), 84 + 5 us backward (4.8).  2048 rows of 32768, which no registers hold: 165 us
+// forward, 156 + 105 + 22 backward, where the copy rate gives 56 and 84.
 #include "ssd_block.h"
 
 namespace ssd {

@@ -10,9 +10,10 @@
 // units, against 4 activations moved per (token, channel).  A tile of 64 channels and 16 states
 // takes 96 slots of 4 cycles a token for that, 128 with step sizes, gate and conversions; the
 // counters show the vector units busy for all of (1)'s time and over 80% of (3)'s.  So memory
-// does not bound the scan (2 TB/s at 32768 tokens of 2048 channels: 177-194 us in (1), 232-259 in (3)),
-// and each slot counts: the step size is kept in base 2, so that a decay is one multiplication
-// and one 2^x; B and C are scalar operands; addresses are scalar; everything that would sit
+// does not bound the scan (2 TB/s at 32768 tokens of 2048 channels: 177-194 us in (1), 232-259 in
+// (3); 312 and 411 with 32 states, 648 and 933 with 64), and each slot counts: the step size is
+// kept in base 2, so that a decay is one multiplication and one 2^x; B and C are scalar operands;
+// addresses are scalar; everything that would sit
 // between a load and its use is fetched 3 tokens early.  The float32 matrix instructions that
 // could form dt u B for 16 states at once were measured not to overlap with vector work on the
 // same SIMD, and bfloat16 ones would round the state.

@@ -24,7 +24,8 @@
 // to memory, added up in order by a last kernel, so that results do not depend on scheduling.
 //
 // 340 vector instructions a (token, 64 channels, 16 states) bound it: 2 x 4096 tokens of 2048
-// channels take 235 us, the vector units busy for 76% of them with two waves a SIMD.
+// channels take 226 to 246 us on different machines, the vector units busy for 76% of them with
+// two waves a SIMD (240 registers and none in memory; 34 to 98 scalars are held in lanes).
 #include "ssd_sel.h"
 
 namespace ssd {
