@@ -1,0 +1,220 @@
+// Matrix products with what follows them in one kernel: arguments, launch functions and the
+// arithmetic that their kernels share.
+//
+//     linear   pre = A B^T + bias;              y = act(pre) + residual
+//     gated    [g | u] = A B^T + bias;          h = act(g) u         (B: F rows of g, F of u)
+//     plain    c = A B^T
+//
+// Every sum over k is held in float32 in the matrix units' accumulators; results are rounded
+// once, when they are stored.
+#pragma once
+
+#include "ssd_block.h"
+
+namespace ssd {
+
+enum Act { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+
+// An operand [rows, K] of a product: element (r, k) at p + r * ld + k, or, where the rows are
+// the contiguous axis (the transposed operands of a backward pass), at p + k * ld + r.
+struct Operand {
+    const void *p;
+    int64_t ld;
+};
+
+enum ProductKind { kLinear, kGated, kPlain };
+
+struct ProductArgs {
+    int64_t M, N, K;              // c [M, N]; gated: N = F, and B has 2 F rows
+    int dtype;
+    ProductKind kind;
+    bool a_rows, b_rows;          // the operand's rows are its contiguous axis
+    Operand a, b;
+    const void *bias;             // [N], gated [2 F]; act dtype, or null
+    const void *residual;         // [M, N] at residual_ld, or null (linear)
+    int64_t residual_ld;
+    int act;
+    void *y;                      // [M, N]
+    void *pre;                    // linear [M, N], gated [M, 2 F]; or null
+    float *part;                  // workspace of a product whose K is split: [splits, M, N or 2 F]
+};
+
+// How one launch cuts its product: tiles in m and n, splits of K, steps of K in each split.
+struct ProductGrid {
+    int tiles_m, tiles_n, splits, steps;
+};
+
+bool product_fits(const ProductArgs &a);                  // its work is within a launch
+size_t product_workspace_bytes(const ProductArgs &a);
+hipError_t launch_product(const ProductArgs &a, hipStream_t s);
+
+// product_bf16.hip, product_f32.hip: operands copied to LDS directly; _any: from any address
+hipError_t launch_tiles_bf16(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
+hipError_t launch_tiles_bf16_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
+hipError_t launch_tiles_f32(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
+hipError_t launch_tiles_f32_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
+
+// The elementwise part of a backward and the sums over its rows
+struct ProductActArgs {
+    int64_t M, N;
+    int dtype;
+    bool gated;
+    const void *dy;               // [M, N] at dy_ld
+    int64_t dy_ld;
+    const void *pre;              // linear [M, N] (null without an activation), gated [M, 2 N]
+    int act;
+    void *dpre;                   // like pre
+    float *part;                  // workspace [product_act_rows, N or 2 N], null without dbias
+    void *dbias;                  // [N or 2 N] (act dtype) or null
+};
+int64_t product_act_rows(int64_t M, int64_t N, int32_t dtype);
+bool product_act_fits(const ProductActArgs &a);
+hipError_t launch_product_act(const ProductActArgs &a, hipStream_t s);
+
+// ---------------------------------------------------------------------------------
+// Activations
+// ---------------------------------------------------------------------------------
+// The normal distribution's function Phi(v) = erfc(-v / sqrt 2) / 2.  erfc by the Chebyshev fit
+// of Press, Teukolsky, Vetterling and Flannery (Numerical Recipes, 6.2), whose fractional error
+// is below 1.2e-7 everywhere; its exponent is taken in two parts, so that the far tail keeps its
+// relative accuracy too.
+__device__ __forceinline__ float normal_cdf(float v) {
+    const float z = fabsf(v) * 0.70710678118654752440f;
+    const float t = rcp_fast(fmaf(0.5f, z, 1.f));
+    float q = 0.17087277f;
+    q = fmaf(q, t, -0.82215223f);
+    q = fmaf(q, t, 1.48851587f);
+    q = fmaf(q, t, -1.13520398f);
+    q = fmaf(q, t, 0.27886807f);
+    q = fmaf(q, t, -0.18628806f);
+    q = fmaf(q, t, 0.09678418f);
+    q = fmaf(q, t, 0.37409196f);
+    q = fmaf(q, t, 1.00002368f);
+    q = fmaf(q, t, -1.26551223f);
+    // e^(-z^2 + q): the square and its product with log2(e) / 2 = kHalfLog2e + kHalfLog2eRest, each
+    // with what its rounding left off
+    constexpr float kHalfLog2e = 0.72134751f, kHalfLog2eRest = 9.62981495e-09f;
+    const float v2 = v * v, x = kHalfLog2e * v2;
+    const float rest = fmaf(kHalfLog2e, v2, -x) + fmaf(kHalfLog2eRest, v2, kHalfLog2e * fmaf(v, v, -v2));
+    const float e = exp2_fast(-x) * exp2_fast(fmaf(kLog2eF, q, -rest));
+    const float c = v2 < 3.0e4f ? 0.5f * t * e : 0.f;           // beyond, 0 x infinity; NaN takes the sum below
+    return v != v ? v : (v < 0.f ? c : 1.f - c);
+}
+
+__device__ __forceinline__ float act_f32(float v, int act) {
+    if (act == kActNone) return v;
+    const float c = act == kActSilu ? sigmoid_f32(v) : normal_cdf(v);
+    return c == 0.f ? 0.f : v * c;                              // 0 at -infinity too
+}
+// act(v) and, in *d, its derivative
+__device__ __forceinline__ float act_d_f32(float v, int act, float *d) {
+    if (act == kActNone) {
+        *d = 1.f;
+        return v;
+    }
+    const bool silu = act == kActSilu;
+    const float c = silu ? sigmoid_f32(v) : normal_cdf(v);
+    // c'(v): s (1 - s) or the normal density
+    const float e = silu ? c * (1.f - c) : 0.39894228040143267794f * exp2_fast(-0.5f * kLog2eF * v * v);
+    *d = e == 0.f ? c : fmaf(v, e, c);
+    return c == 0.f ? 0.f : v * c;
+}
+
+// ---------------------------------------------------------------------------------
+// Epilogues: V consecutive columns of one row
+// ---------------------------------------------------------------------------------
+template <typename T> constexpr int product_vec() { return 16 / (int)sizeof(T); }
+
+// Loads of V values at p that may not lie on 16 bytes or reach past the row's end
+template <typename T, int V>
+__device__ __forceinline__ void load_some(const T *p, int n, bool whole, float (&v)[V]) {
+    if (whole) {
+        unpack<T, V>(load_pack<T, V>(p), v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_some(T *p, int n, bool whole, const float (&v)[V]) {
+    if (whole) {
+        store_f32<T, V>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < n) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+// The epilogue's flags that are the same for all of a launch: rows and pointers on 16 bytes.
+inline bool rows_at16(const void *p, int64_t ld, int64_t e) { return ((uintptr_t)p & 15u) == 0 && ld * e % 16 == 0; }
+
+struct Epilogue {
+    int64_t M, N;
+    const void *bias, *residual;
+    int64_t residual_ld;
+    int act;
+    void *y, *pre;
+    bool vec;                     // every row of the tensors above starts on 16 bytes
+};
+
+inline Epilogue epilogue_of(const ProductArgs &a) {
+    const int64_t e = a.dtype == 1 ? 2 : 4;
+    Epilogue r = {a.M, a.N, a.bias, a.residual, a.residual_ld, a.act, a.y, a.pre, false};
+    r.vec = rows_at16(a.y, a.N, e) && (!a.bias || rows_at16(a.bias, a.N, e)) &&
+            (!a.residual || rows_at16(a.residual, a.M > 1 ? a.residual_ld : 0, e)) &&
+            (!a.pre || rows_at16(a.pre, a.N, e));
+    return r;
+}
+
+// v: the product's values at row m, columns n .. n + V - 1
+template <typename T, int V>
+__device__ __forceinline__ void finish_linear(const Epilogue &p, int64_t m, int64_t n, float (&v)[V]) {
+    const int left = (int)min(p.N - n, (int64_t)V);
+    if (left <= 0) return;
+    const bool whole = p.vec && left == V;
+    float b[V];
+    if (p.bias) {
+        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + n, left, whole, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += b[i];
+    }
+    if (p.pre) store_some<T, V>(reinterpret_cast<T *>(p.pre) + m * p.N + n, left, whole, v);
+    if (p.act != kActNone) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = act_f32(v[i], p.act);
+    }
+    if (p.residual) {
+        load_some<T, V>(reinterpret_cast<const T *>(p.residual) + m * p.residual_ld + n, left, whole, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += b[i];
+    }
+    store_some<T, V>(reinterpret_cast<T *>(p.y) + m * p.N + n, left, whole, v);
+}
+
+// g and u: both products' values at row m, columns n .. n + V - 1 of each half
+template <typename T, int V>
+__device__ __forceinline__ void finish_gated(const Epilogue &p, int64_t m, int64_t n, float (&g)[V], float (&u)[V]) {
+    const int left = (int)min(p.N - n, (int64_t)V);
+    if (left <= 0) return;
+    const bool whole = p.vec && left == V;
+    float b[V];
+    if (p.bias) {
+        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + n, left, whole, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] += b[i];
+        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + p.N + n, left, whole, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[i] += b[i];
+    }
+    if (p.pre) {
+        T *pre = reinterpret_cast<T *>(p.pre) + 2 * m * p.N + n;
+        store_some<T, V>(pre, left, whole, g);
+        store_some<T, V>(pre + p.N, left, whole, u);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = act_f32(g[i], p.act) * u[i];
+    store_some<T, V>(reinterpret_cast<T *>(p.y) + m * p.N + n, left, whole, g);
+}
+
+}  // namespace ssd

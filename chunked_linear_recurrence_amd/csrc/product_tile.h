@@ -1,0 +1,342 @@
+// The tiled matrix product of product.h on the matrix units (gfx950).
+//
+// A workgroup computes a tile of BM x BN results in steps of 128 bytes of k for each row (64
+// bfloat16 or 32 float32 values).  A step's tiles of A and B lie in LDS, two steps' in turn:
+// while one is multiplied the next is on its way.  A step is two slices of 64 bytes of k, and
+// the next slice's fragments are read while a slice is multiplied, also across the step's
+// only barrier, so the matrix units wait for neither LDS nor the barrier:
+//
+//     read slice 1 | multiply slice 0 | next step landed, barrier | start the copy of the step
+//     after the next | read the next step's slice 0 | multiply slice 1
+//
+// Products are computed transposed, (B rows) x (A rows)^T, and the B rows of a wave's matrix
+// tiles are interleaved, so that a lane ends with 4 NT consecutive columns of each of its rows
+// and stores (and loads the residual) in whole 16-byte pieces.
+//
+// LDS layouts.  An operand whose k is contiguous: rows of 128 bytes, 16-byte piece q of row r
+// at place q ^ key(r).  An operand whose rows are contiguous: lines of one k, BM or BN values,
+// 16-byte piece q of line k at place q ^ key(k); bfloat16 fragments are transpose reads
+// (ds_read_b64_tr_b16), float32 ones single values.  The keys spread the lanes of one LDS
+// cycle over its banks.
+//
+// Rows and columns past the result's end repeat the last row's or hold what lies beside it:
+// they meet no result that is stored.  Values past K are zeros in both operands.
+#pragma once
+
+#include "product.h"
+#include "ssd_tile.h"
+
+namespace ssd {
+
+constexpr int kStepBytes = 128;
+
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+// One operand's tile of R rows in LDS, and how a wave's fragments take its rows: row i of
+// fragment j is 4 NT (i / 4) + 4 j + i % 4 (INTER, NT fragments) or 16 j + i.
+template <typename T, int R, bool ROWS_, bool INTER, int NT>
+struct TileLayout {
+    static constexpr bool ROWS = ROWS_;
+    static constexpr int E = (int)sizeof(T), V = 16 / E, KS = kStepBytes / E, SIZE = R;
+    static constexpr int BYTES = R * kStepBytes;
+    static constexpr int PIECES = ROWS ? R / V : 8;         // 16-byte pieces per LDS line
+    static constexpr int PITCH = PIECES * 16;
+    // what the places of a line's pieces are XORed with
+    __host__ __device__ static constexpr int key(int line) {
+        if (!ROWS) return INTER ? (line & 3) | ((((line >> 3) ^ (line >> 4)) & 1) << 2) : line & 7;
+        if (E == 2) return INTER ? (line & 1) | (((line >> 1) & 1) << 3) : (line & 3) << 1;
+        return INTER ? (line >> 2) & 3 : ((line >> 2) & 3) << 2;
+    }
+    __host__ __device__ static constexpr int row_of(int j, int i) {
+        return INTER ? 4 * NT * (i >> 2) + 4 * j + (i & 3) : 16 * j + i;
+    }
+    __host__ __device__ static constexpr int at(int line, int piece) { return line * PITCH + (piece ^ key(line)) * 16; }
+    // The line and piece of the source that belong at the 16 bytes `slot` of the tile
+    __host__ __device__ static constexpr int slot_line(int slot) { return slot / PIECES; }
+    __host__ __device__ static constexpr int slot_piece(int slot) { return (slot % PIECES) ^ key(slot / PIECES); }
+};
+
+template <typename T> struct Frag;
+template <> struct Frag<bf16> { typedef bf16x8 type; };
+template <> struct Frag<float> { typedef f32x4 type; };
+
+// Fragment j of slice s of the wave whose first row is r0: lane (i, g) holds row_of(j, i),
+// k = 8 g + 0..7 of the slice's 32 (bfloat16) or 4 g + 0..3 of its 16 (float32).
+template <class L, typename T>
+__device__ __forceinline__ typename Frag<T>::type read_frag(const unsigned char *m, int r0, int j, int s, int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (!L::ROWS) {
+        return *reinterpret_cast<const typename Frag<T>::type *>(m + L::at(r0 + L::row_of(j, i), 4 * s + g));
+    } else if constexpr (sizeof(T) == 2) {
+        // lane i of 16 reads 4 values of line i / 4 and receives column i of the 4 lines
+        const int n = r0 + L::row_of(j, 4 * (i & 3)), line = 32 * s + 8 * g + (i >> 2);
+        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+            (lds_bf16x4_t *)(m + L::at(line, n / 8) + (n & 4) * 2));
+        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+            (lds_bf16x4_t *)(m + L::at(line + 4, n / 8) + (n & 4) * 2));
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+        const int n = r0 + L::row_of(j, i);
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = *reinterpret_cast<const float *>(m + L::at(16 * s + 4 * g + e, n / 4) + (n & 3) * 4);
+        return v;
+    }
+}
+
+__device__ __forceinline__ f32x4 multiply(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply(f32x4 a, f32x4 b, f32x4 c) { return mma_one(a, b, c); }
+
+// BM x BN results by WM x WN waves.  DMA: operands copied to LDS directly (every piece of 16
+// bytes lies on 16 and inside a row), otherwise by way of registers from any address.
+template <typename T_, int BM_, int BN_, int WM_, int WN_, bool A_ROWS, bool B_ROWS, bool DMA_, ProductKind KIND_>
+struct ProductCfg {
+    typedef T_ T;
+    static constexpr ProductKind KIND = KIND_;
+    static constexpr bool DMA = DMA_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN, THREADS = NW * 64;
+    static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
+    static constexpr int NT = KIND == kGated ? TN / 2 : TN;       // fragments of one interleaved group
+    static constexpr int BCOLS = KIND == kGated ? BN / 2 : BN;    // result columns of a tile
+    typedef TileLayout<T, BM, A_ROWS, false, TM> LA;
+    typedef TileLayout<T, BN, B_ROWS, true, NT> LB;
+    static constexpr int KS = kStepBytes / (int)sizeof(T);
+    static constexpr int QA = LA::BYTES / 1024 / NW, QB = LB::BYTES / 1024 / NW;   // copies per wave and step
+    static_assert(QA * 1024 * NW == LA::BYTES && QB * 1024 * NW == LB::BYTES, "whole waves of 16-byte pieces");
+    static_assert(KIND != kGated || (TN % 2 == 0 && !B_ROWS), "gate and up rows side by side");
+};
+
+// Row of B that row r of a tile stands for, from the tile's first column n0, before clamping:
+// in a gated product the tile's second half is the other half of B.
+template <class C>
+__device__ __forceinline__ int64_t b_row(const ProductArgs &p, int64_t n0, int r) {
+    if constexpr (C::KIND == kGated)
+        return r < C::BN / 2 ? min(n0 + r, p.N - 1) : p.N + min(n0 + r - C::BN / 2, p.N - 1);
+    return min(n0 + r, p.N - 1);
+}
+
+// Tile of a workgroup.  Consecutive workgroups go to the 8 XCDs in turn; each XCD (own L2) takes
+// a contiguous range of the order below: columns of tiles in groups of 4, and within a group
+// row by row, so that the 32 tiles an XCD holds at a time share their operands.
+struct TileAt {
+    int m, n;
+};
+__device__ __forceinline__ TileAt tile_at(int bid, const ProductGrid &g) {
+    const int n = g.tiles_m * g.tiles_n, per = n / 8, more = n % 8, x = bid % 8;
+    const int id = x * per + min(x, more) + bid / 8;
+    constexpr int G = 4;
+    const int group = id / (G * g.tiles_m), first = group * G, width = min(G, g.tiles_n - first);
+    const int in = id - group * G * g.tiles_m;
+    return {in / width, first + in % width};
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, Epilogue ep, ProductGrid grid) {
+    typedef typename C::T T;
+    typedef typename Frag<T>::type F;
+    typedef typename C::LA LA;
+    typedef typename C::LB LB;
+    constexpr int E = (int)sizeof(T), V = 16 / E;
+    __shared__ __align__(16) unsigned char A0[LA::BYTES], B0[LB::BYTES], A1[LA::BYTES], B1[LB::BYTES];
+
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w / C::WN, wn = w % C::WN;
+    const TileAt tile = tile_at(blockIdx.x, grid);
+    const int64_t m0 = (int64_t)tile.m * C::BM, n0 = (int64_t)tile.n * C::BCOLS;
+    const int64_t first = (int64_t)blockIdx.y * grid.steps;       // this split's steps
+    const int64_t all = (p.K + C::KS - 1) / C::KS;
+    const int steps = (int)min((int64_t)grid.steps, all - first);
+    const int64_t k_first = first * C::KS;
+
+    // ---- copies
+    // DMA: 32-bit offsets from a scalar base that moves with k
+    uint32_t offa[C::QA], offb[C::QB];
+    if constexpr (C::DMA) {
+#pragma unroll
+        for (int q = 0; q < C::QA; ++q) {
+            const int slot = (w * C::QA + q) * 64 + lane, line = LA::slot_line(slot), piece = LA::slot_piece(slot);
+            const int64_t r = LA::ROWS ? line : min(m0 + line, p.M - 1) - m0;
+            offa[q] = (uint32_t)(r * p.a.ld * E) + piece * 16;
+        }
+#pragma unroll
+        for (int q = 0; q < C::QB; ++q) {
+            const int slot = (w * C::QB + q) * 64 + lane, line = LB::slot_line(slot), piece = LB::slot_piece(slot);
+            const int64_t r = LB::ROWS ? line : b_row<C>(p, n0, line) - n0;
+            offb[q] = (uint32_t)(r * p.b.ld * E) + piece * 16;
+        }
+    }
+    u32x4 ra[C::DMA ? 1 : C::QA], rb[C::DMA ? 1 : C::QB];
+    // an operand's copies of the step at k: `rows` is where the operand's tile begins and `size`
+    // how many rows there are
+    auto copy = [&](auto layout, const Operand &o, int64_t at, int64_t size, int64_t k, int Q, const uint32_t *off,
+                    unsigned char *to) {
+        typedef decltype(layout) L;
+        const int64_t left = p.K - k;
+        constexpr int64_t kMost = 0x7fffffff;
+        const unsigned char *base = reinterpret_cast<const unsigned char *>(o.p) +
+                                    (L::ROWS ? k * o.ld + at : at * o.ld + k) * E;
+        const int64_t bytes = L::ROWS ? ((left - 1) * o.ld + size - at) * E : ((size - 1 - at) * o.ld + left) * E;
+        const rsrc_t rs = make_rsrc(base, (uint32_t)min(bytes, kMost));
+        for (int q = 0; q < Q; ++q) {
+            uint32_t v = off[q];
+            if (!L::ROWS && left < L::KS) {
+                const int piece = L::slot_piece((w * Q + q) * 64 + lane);
+                if (piece * V >= left) v = 0x80000000u;           // past K: zeros
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(to + (w * Q + q) * 1024), 16, v, 0, 0, 0);
+        }
+    };
+    auto fetch = [&](auto layout, const Operand &o, int64_t at, int64_t size, bool is_b, int64_t k, int Q, u32x4 *reg) {
+        typedef decltype(layout) L;
+        for (int q = 0; q < Q; ++q) {
+            const int slot = (w * Q + q) * 64 + lane, line = L::slot_line(slot), piece = L::slot_piece(slot);
+            const T *src;
+            int64_t have;
+            if (L::ROWS) {
+                have = k + line < p.K ? size - (at + piece * V) : 0;
+                src = reinterpret_cast<const T *>(o.p) + (k + line) * o.ld + at + piece * V;
+            } else {
+                const int64_t r = is_b ? b_row<C>(p, at, line) : min(at + line, size - 1);
+                have = p.K - (k + piece * V);
+                src = reinterpret_cast<const T *>(o.p) + r * o.ld + k + piece * V;
+            }
+            u32x4 v = {0, 0, 0, 0};
+            if (have >= V) {
+                __builtin_memcpy(&v, src, 16);
+            } else if (have > 0) {
+                T t[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) t[i] = i < have ? src[i] : from_f32<T>(0.f);
+                __builtin_memcpy(&v, t, 16);
+            }
+            reg[q] = v;
+        }
+    };
+    auto place = [&](int Q, const u32x4 *reg, unsigned char *to) {
+        for (int q = 0; q < Q; ++q) *reinterpret_cast<u32x4 *>(to + ((w * Q + q) * 64 + lane) * 16) = reg[q];
+    };
+    const int64_t a_size = p.M, b_size = C::KIND == kGated ? 2 * p.N : p.N;
+    // DMA: the copy of step t into (a, b).  Registers: what was fetched (step t) goes there, and
+    // the step after it is fetched.
+    auto start = [&](int t, unsigned char *a, unsigned char *b) {
+        const int64_t k = k_first + (int64_t)t * C::KS;
+        if constexpr (C::DMA) {
+            copy(LA{}, p.a, m0, a_size, k, C::QA, offa, a);
+            copy(LB{}, p.b, n0, b_size, k, C::QB, offb, b);
+        } else {
+            place(C::QA, ra, a);
+            place(C::QB, rb, b);
+            if (t + 1 < steps) {
+                fetch(LA{}, p.a, m0, a_size, false, k + C::KS, C::QA, ra);
+                fetch(LB{}, p.b, n0, b_size, true, k + C::KS, C::QB, rb);
+            }
+        }
+    };
+
+    // ---- products
+    f32x4 acc[C::TM][C::TN];
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    F a[2][C::TM], b[2][C::TN];
+    auto read = [&](int s, const unsigned char *ma, const unsigned char *mb) {
+#pragma unroll
+        for (int j = 0; j < C::TN; ++j)
+            b[s][j] = read_frag<LB, T>(mb, (j / C::NT) * (C::BN / 2) + wn * 16 * C::NT, j % C::NT, s, lane);
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i) a[s][i] = read_frag<LA, T>(ma, wm * 16 * C::TM, i, s, lane);
+    };
+    auto products = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j) acc[i][j] = multiply(b[s][j], a[s][i], acc[i][j]);
+    };
+    // this wave's copies have landed and its LDS reads are done, then every wave's; the compiler
+    // moves no access of memory across it
+    auto landed = [&] {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    auto step = [&](int t, unsigned char *a_cur, unsigned char *b_cur, unsigned char *a_next, unsigned char *b_next) {
+        read(1, a_cur, b_cur);
+        products(0);
+        landed();
+        if (t + 2 < steps) start(t + 2, a_cur, b_cur);
+        if (t + 1 < steps) read(0, a_next, b_next);
+        products(1);
+    };
+    if constexpr (!C::DMA) {
+        fetch(LA{}, p.a, m0, a_size, false, k_first, C::QA, ra);
+        fetch(LB{}, p.b, n0, b_size, true, k_first, C::QB, rb);
+    }
+    start(0, A0, B0);
+    if constexpr (C::DMA) landed();
+    if (steps > 1) start(1, A1, B1);
+    if constexpr (!C::DMA) landed();
+    read(0, A0, B0);
+    for (int t = 0; t < steps; t += 2) {
+        step(t, A0, B0, A1, B1);
+        if (t + 1 < steps) step(t + 1, A1, B1, A0, B0);
+    }
+
+    // ---- results: this lane's columns are n .. n + 4 NT - 1 of each half
+    const int i16 = lane & 15, g = lane >> 4;
+    const int64_t n = n0 + wn * 16 * C::NT + 4 * C::NT * g;
+#pragma unroll
+    for (int i = 0; i < C::TM; ++i) {
+        const int64_t m = m0 + wm * 16 * C::TM + 16 * i + i16;
+        if (m >= p.M) continue;
+        if (grid.splits > 1) {
+            const int64_t cols = b_size;
+            float *part = p.part + ((int64_t)blockIdx.y * p.M + m) * cols;
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j) {
+                const int64_t c = n + 4 * (j % C::NT);
+                const int left = (int)min(p.N - c, (int64_t)4);
+                float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                if (left > 0) store_some<float, 4>(part + c + (j / C::NT) * p.N, left, left == 4 && p.N % 4 == 0, v);
+            }
+            continue;
+        }
+#pragma unroll
+        for (int c = 0; c < 4 * C::NT; c += V) {
+            float v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = acc[i][(c + e) / 4][e % 4];
+            if constexpr (C::KIND == kGated) {
+                float u[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) u[e] = acc[i][C::NT + (c + e) / 4][e % 4];
+                finish_gated<T, V>(ep, m, n + c, v, u);
+            } else {
+                finish_linear<T, V>(ep, m, n + c, v);
+            }
+        }
+    }
+}
+
+template <class C>
+hipError_t launch_tiles(const ProductArgs &a, const ProductGrid &g, hipStream_t s) {
+    product_kernel<C><<<dim3((uint32_t)(g.tiles_m * g.tiles_n), (uint32_t)g.splits), C::THREADS, 0, s>>>(
+        a, epilogue_of(a), g);
+    return hipGetLastError();
+}
+
+// The launch of one shape of tile for each form of product that there is: k contiguous in both
+// operands (linear, gated), the rows contiguous in B (a gradient by x), in both (by a weight).
+template <typename T, int BM, int BN, int WM, int WN, bool DMA>
+hipError_t launch_tiles_of(const ProductArgs &a, const ProductGrid &g, hipStream_t s) {
+    if (a.kind == kGated) return launch_tiles<ProductCfg<T, BM, BN, WM, WN, false, false, DMA, kGated>>(a, g, s);
+    if (a.kind == kLinear) return launch_tiles<ProductCfg<T, BM, BN, WM, WN, false, false, DMA, kLinear>>(a, g, s);
+    if (a.a_rows) return launch_tiles<ProductCfg<T, BM, BN, WM, WN, true, true, DMA, kPlain>>(a, g, s);
+    return launch_tiles<ProductCfg<T, BM, BN, WM, WN, false, true, DMA, kPlain>>(a, g, s);
+}
+
+}  // namespace ssd

@@ -1,0 +1,515 @@
+// The norms after and before a block with its gate, its scale and the residual, and their
+// backward.  Each row of D channels, rms(v) = v / sqrt(mean(v^2) + eps):
+//
+//     t = branch silu(gate);   p = rms(t) post;   s = residual + scale p;   y = rms(s) pre
+//
+//     ds = dtotal + rs (g - shat mean(g shat)),  g = dy pre, shat = s rs
+//     dp = ds scale;   dt = rt (h - that mean(h that)),  h = dp post, that = t rt
+//     dresidual = ds;  dbranch = dt silu(gate);  dgate = dt branch silu'(gate)
+//     dpre = sum over rows of dy shat;  dscale = of ds p;  dpost = of dp that
+//
+// What is not given drops out.  A stream of up to 5 elements in the forward and 8 in the
+// backward per channel; a row is read once and held in registers between its sums (1, 4 or 8
+// waves, the fewest that hold it; rows wider than that are read again for each sum).  s is
+// formed again in the backward in float32, from the same reads that its rounded copy would
+// cost, so no rounding of s enters a gradient.  The three column sums are kept in registers
+// over a workgroup's rows, leave it as one row of partial sums, and a second kernel adds those
+// in order, so results do not depend on scheduling.
+#include "residual_norm.h"
+
+namespace ssd {
+
+constexpr int kRnFwdBlocks = 1024, kRnBwdBlocks = 512;   // workgroups at most
+
+template <int WPR> constexpr int rn_threads() { return WPR == 8 ? 512 : 256; }
+// Whether registers hold the next row beside the backward's current one
+template <typename T, int V, int K> constexpr bool rn_ahead() { return K * (V == 1 ? 1 : V * (int)sizeof(T) / 4) <= 8; }
+template <int WPR> constexpr int rn_rows() { return WPR == 1 ? 4 : 1; }       // rows a workgroup holds at a time
+
+template <typename T, int V, int K, int WPR>
+struct RowRegs {
+    typename Pack<T, V>::type v[K];
+    // this thread's accesses of a row (null: none); those past the row are left alone
+    __device__ __forceinline__ void load(const T *x, int D, int tid) {
+        if (!x) return;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * 64 * WPR + tid) * V;
+            if (c < D) v[k] = load_pack<T, V>(x + c);
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ const T *row_at(const void *p, int64_t row, int64_t stride) {
+    return p ? reinterpret_cast<const T *>(p) + row * stride : nullptr;
+}
+
+template <int V, int K, int WPR>
+__device__ __forceinline__ void load_params(const float *p, int D, int tid, float (&v)[K][V]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (k * 64 * WPR + tid) * V;
+            v[k][i] = p && c < D ? p[c + i] : 1.f;
+        }
+}
+
+template <typename T, int V, int K, int WPR>
+__global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(ResidualNormArgs a) {
+    __shared__ float red[16];
+    constexpr int R = rn_rows<WPR>();
+    const int tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? threadIdx.x / 64 : 0), by = (int64_t)gridDim.x * R;
+    float post[K][V], scale[K][V], pre[K][V];
+    load_params<V, K, WPR>(a.post, a.D, tid, post);
+    load_params<V, K, WPR>(a.scale, a.D, tid, scale);
+    load_params<V, K, WPR>(a.pre, a.D, tid, pre);
+    RowRegs<T, V, K, WPR> bn = {}, zn = {}, rn = {};
+    auto fetch = [&](int64_t row) {
+        bn.load(row_at<T>(a.branch, row, a.branch_stride), a.D, tid);
+        zn.load(row_at<T>(a.gate, row, a.gate_stride), a.D, tid);
+        rn.load(row_at<T>(a.residual, row, a.residual_stride), a.D, tid);
+    };
+    if (first < a.rows) fetch(first);
+    for (int64_t row = first; row < a.rows; row += by) {
+        const RowRegs<T, V, K, WPR> b = bn, z = zn, r = rn;
+        if (row + by < a.rows) fetch(row + by);
+        float v[K][V];
+        float sq = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            unpack<T, V>(b.v[k], v[k]);
+            if (a.gate) {
+                float g[V];
+                unpack<T, V>(z.v[k], g);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[k][i] *= silu_f32(g[i]);
+            }
+            if ((k * 64 * WPR + tid) * V < a.D)
+#pragma unroll
+                for (int i = 0; i < V; ++i) sq = fmaf(v[k][i], v[k][i], sq);
+        }
+        float rt = 1.f;
+        if (a.post) rt = 1.f / sqrtf(row_sum<WPR>(sq, red) / a.D + a.eps);
+        sq = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float res[V];
+            unpack<T, V>(r.v[k], res);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = fmaf(v[k][i] * rt * post[k][i], scale[k][i], a.residual ? res[i] : 0.f);
+            const int c = (k * 64 * WPR + tid) * V;
+            if (c < a.D) {
+                store_f32<T, V>(reinterpret_cast<T *>(a.total) + row * a.D + c, v[k]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) sq = fmaf(v[k][i], v[k][i], sq);
+            }
+        }
+        float rs = 1.f;
+        if (a.pre) {
+            rs = 1.f / sqrtf(row_sum<WPR>(sq, red) / a.D + a.eps);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int c = (k * 64 * WPR + tid) * V;
+                if (c < a.D) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * rs * pre[k][i];
+                    store_f32<T, V>(reinterpret_cast<T *>(a.y) + row * a.D + c, v[k]);
+                }
+            }
+        }
+        if (a.stats && tid == 0) {
+            a.stats[row] = rt;
+            a.stats[a.rows + row] = rs;
+        }
+    }
+}
+
+// Rows wider than registers: one workgroup a row, a pass over it for each sum and one to store.
+template <typename T>
+struct WideRow {
+    const T *b, *z, *r;
+    const ResidualNormArgs &a;
+    __device__ __forceinline__ WideRow(const ResidualNormArgs &args, int64_t row)
+        : b(row_at<T>(args.branch, row, args.branch_stride)), z(row_at<T>(args.gate, row, args.gate_stride)),
+          r(row_at<T>(args.residual, row, args.residual_stride)), a(args) {}
+    __device__ __forceinline__ float t(int c) const { return z ? to_f32(b[c]) * silu_f32(to_f32(z[c])) : to_f32(b[c]); }
+    __device__ __forceinline__ float p(float t, float rt, int c) const { return a.post ? t * rt * a.post[c] : t; }
+    __device__ __forceinline__ float s(float p, int c) const {
+        return fmaf(p, a.scale ? a.scale[c] : 1.f, r ? to_f32(r[c]) : 0.f);
+    }
+};
+
+template <typename T>
+__global__ __launch_bounds__(1024) void residual_norm_fwd_wide_kernel(ResidualNormArgs a) {
+    __shared__ float red[16];
+    const int64_t row = blockIdx.x;
+    const WideRow<T> w(a, row);
+    float rt = 1.f, rs = 1.f, sq = 0.f;
+    if (a.post) {
+        for (int c = threadIdx.x; c < a.D; c += 1024) {
+            const float t = w.t(c);
+            sq = fmaf(t, t, sq);
+        }
+        rt = 1.f / sqrtf(row_sum<16>(sq, red) / a.D + a.eps);
+    }
+    if (a.pre) {
+        sq = 0.f;
+        for (int c = threadIdx.x; c < a.D; c += 1024) {
+            const float s = w.s(w.p(w.t(c), rt, c), c);
+            sq = fmaf(s, s, sq);
+        }
+        rs = 1.f / sqrtf(row_sum<16>(sq, red) / a.D + a.eps);
+    }
+    for (int c = threadIdx.x; c < a.D; c += 1024) {
+        const float s = w.s(w.p(w.t(c), rt, c), c);      // before the store: total may be residual
+        reinterpret_cast<T *>(a.total)[row * a.D + c] = from_f32<T>(s);
+        if (a.pre) reinterpret_cast<T *>(a.y)[row * a.D + c] = from_f32<T>(s * rs * a.pre[c]);
+    }
+    if (a.stats && threadIdx.x == 0) {
+        a.stats[row] = rt;
+        a.stats[a.rows + row] = rs;
+    }
+}
+
+template <typename T, int V, int K, int WPR>
+__global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(ResidualNormArgs a) {
+    __shared__ float red[16];
+    __shared__ float cols[WPR == 1 ? 3 * 64 * V * K : 1];
+    constexpr int R = rn_rows<WPR>();
+    const int wave = threadIdx.x / 64, tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0), by = (int64_t)gridDim.x * R;
+    float post[K][V], scale[K][V], pre[K][V], sums[3][K][V];
+    load_params<V, K, WPR>(a.post, a.D, tid, post);
+    load_params<V, K, WPR>(a.scale, a.D, tid, scale);
+    load_params<V, K, WPR>(a.pre, a.D, tid, pre);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) sums[q][k][i] = 0.f;
+    RowRegs<T, V, K, WPR> bn = {}, zn = {}, rn = {}, yn = {}, tn = {};
+    float rt_n = 1.f, rs_n = 1.f;
+    auto fetch = [&](int64_t row) {
+        bn.load(row_at<T>(a.branch, row, a.branch_stride), a.D, tid);
+        zn.load(row_at<T>(a.gate, row, a.gate_stride), a.D, tid);
+        yn.load(row_at<T>(a.dy, row, a.dy_stride), a.D, tid);
+        if (a.dy) rn.load(row_at<T>(a.residual, row, a.residual_stride), a.D, tid);     // s is needed for its norm alone
+        tn.load(row_at<T>(a.dtotal, row, a.dtotal_stride), a.D, tid);
+        rt_n = a.stats[row];
+        rs_n = a.stats[a.rows + row];
+    };
+    if (first < a.rows) fetch(first);
+    for (int64_t row = first; row < a.rows; row += by) {
+        const RowRegs<T, V, K, WPR> bq = bn, zq = zn, rq = rn, yq = yn, tq = tn;
+        const float rt = rt_n, rs = rs_n;
+        if (rn_ahead<T, V, K>() && row + by < a.rows) fetch(row + by);
+        float that[K][V], d[K][V], s[K][V];
+        float dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            unpack<T, V>(bq.v[k], that[k]);
+            if (a.gate) {
+                float z[V];
+                unpack<T, V>(zq.v[k], z);
+#pragma unroll
+                for (int i = 0; i < V; ++i) that[k][i] *= silu_f32(z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) that[k][i] *= rt;
+            unpack<T, V>(tq.v[k], d[k]);                       // zeros where dtotal is not given
+            if (a.dy) {
+                float r[V], dy[V];
+                unpack<T, V>(rq.v[k], r);
+                unpack<T, V>(yq.v[k], dy);
+                const bool on = (k * 64 * WPR + tid) * V < a.D;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[k][i] = fmaf(that[k][i] * post[k][i], scale[k][i], r[i]) * rs;      // shat
+                    if (on) {
+                        dot = fmaf(dy[i] * pre[k][i], s[k][i], dot);
+                        sums[0][k][i] = fmaf(dy[i], s[k][i], sums[0][k][i]);
+                    }
+                }
+            }
+        }
+        if (a.dy) {
+            dot = row_sum<WPR>(dot, red) / a.D;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float dy[V];
+                unpack<T, V>(yq.v[k], dy);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[k][i] = fmaf(rs, dy[i] * pre[k][i] - s[k][i] * dot, d[k][i]);
+            }
+        }
+        dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * 64 * WPR + tid) * V;
+            if (c < a.D) {
+                if (a.dresidual) store_f32<T, V>(reinterpret_cast<T *>(a.dresidual) + row * a.D + c, d[k]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    sums[1][k][i] = fmaf(d[k][i], that[k][i] * post[k][i], sums[1][k][i]);
+                    d[k][i] *= scale[k][i];                    // dp
+                    sums[2][k][i] = fmaf(d[k][i], that[k][i], sums[2][k][i]);
+                    d[k][i] *= post[k][i];
+                    dot = fmaf(d[k][i], that[k][i], dot);
+                }
+            }
+        }
+        if (a.post) {
+            dot = row_sum<WPR>(dot, red) / a.D;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[k][i] = rt * (d[k][i] - that[k][i] * dot);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * 64 * WPR + tid) * V;
+            if (c >= a.D) continue;
+            if (a.gate) {
+                float z[V], b[V], dz[V];
+                unpack<T, V>(zq.v[k], z);
+                unpack<T, V>(bq.v[k], b);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float sg = sigmoid_f32(z[i]);
+                    dz[i] = d[k][i] * b[i] * sg * fmaf(z[i], 1.f - sg, 1.f);
+                    d[k][i] *= z[i] * sg;
+                }
+                store_f32<T, V>(reinterpret_cast<T *>(a.dgate) + row * a.D + c, dz);
+            }
+            store_f32<T, V>(reinterpret_cast<T *>(a.dbranch) + row * a.D + c, d[k]);
+        }
+        if (!rn_ahead<T, V, K>() && row + by < a.rows) fetch(row + by);
+    }
+    if (!a.part) return;
+    float *part = a.part + (int64_t)blockIdx.x * 3 * a.D;
+    if constexpr (WPR == 1) {
+        // the 4 waves add their sums in wave order
+        constexpr int M = 64 * V * K;
+        for (int w = 0; w < 4; ++w) {
+            if (wave == w) {
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            float &at = cols[q * M + (k * V + i) * 64 + tid];      // lanes side by side
+                            at = (w ? at : 0.f) + sums[q][k][i];
+                        }
+            }
+            __syncthreads();
+        }
+        for (int m = threadIdx.x; m < 3 * M; m += 256) {
+            const int q = m / M, l = m % 64, ki = m % M / 64;
+            const int c = ((ki / V) * 64 + l) * V + ki % V;
+            if (c < a.D) part[(int64_t)q * a.D + c] = cols[m];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * 64 * WPR + tid) * V;
+            if (c < a.D)
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) part[(int64_t)q * a.D + c + i] = sums[q][k][i];
+        }
+    }
+}
+
+// Rows wider than registers: the same sums by passes over the row; the terms of the three
+// column sums are left to the kernel below, which needs each row's two means (rows of `mean`).
+template <typename T>
+__device__ __forceinline__ void wide_terms(const ResidualNormArgs &a, const WideRow<T> &w, int64_t row, int c, float rt,
+                                           float rs, float mean_s, float &that, float &p, float &shat, float &dy, float &ds) {
+    that = w.t(c) * rt;
+    p = a.post ? that * a.post[c] : that;
+    ds = a.dtotal ? to_f32(row_at<T>(a.dtotal, row, a.dtotal_stride)[c]) : 0.f;
+    shat = dy = 0.f;
+    if (a.dy) {
+        shat = w.s(p, c) * rs;
+        dy = to_f32(row_at<T>(a.dy, row, a.dy_stride)[c]);
+        ds = fmaf(rs, dy * a.pre[c] - shat * mean_s, ds);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void residual_norm_bwd_wide_kernel(ResidualNormArgs a) {
+    __shared__ float red[16];
+    const int64_t row = blockIdx.x;
+    const WideRow<T> w(a, row);
+    const float rt = a.stats[row], rs = a.stats[a.rows + row];
+    float that, p, shat, dy, ds, mean_s = 0.f, mean_t = 0.f, dot = 0.f;
+    if (a.dy) {
+        for (int c = threadIdx.x; c < a.D; c += 1024) {
+            wide_terms(a, w, row, c, rt, rs, 0.f, that, p, shat, dy, ds);
+            dot = fmaf(dy * a.pre[c], shat, dot);
+        }
+        mean_s = row_sum<16>(dot, red) / a.D;
+    }
+    if (a.post) {
+        dot = 0.f;
+        for (int c = threadIdx.x; c < a.D; c += 1024) {
+            wide_terms(a, w, row, c, rt, rs, mean_s, that, p, shat, dy, ds);
+            dot = fmaf(ds * (a.scale ? a.scale[c] : 1.f) * a.post[c], that, dot);
+        }
+        mean_t = row_sum<16>(dot, red) / a.D;
+    }
+    for (int c = threadIdx.x; c < a.D; c += 1024) {
+        wide_terms(a, w, row, c, rt, rs, mean_s, that, p, shat, dy, ds);
+        if (a.dresidual) reinterpret_cast<T *>(a.dresidual)[row * a.D + c] = from_f32<T>(ds);
+        float d = ds * (a.scale ? a.scale[c] : 1.f);
+        if (a.post) d = rt * (d * a.post[c] - that * mean_t);
+        if (a.gate) {
+            const float z = to_f32(w.z[c]), sg = sigmoid_f32(z);
+            reinterpret_cast<T *>(a.dgate)[row * a.D + c] = from_f32<T>(d * to_f32(w.b[c]) * sg * fmaf(z, 1.f - sg, 1.f));
+            d *= z * sg;
+        }
+        reinterpret_cast<T *>(a.dbranch)[row * a.D + c] = from_f32<T>(d);
+    }
+    if (threadIdx.x == 0) a.mean[row] = mean_s;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void residual_norm_bwd_cols_kernel(ResidualNormArgs a) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= a.D) return;
+    float sums[3] = {0.f, 0.f, 0.f};
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        const WideRow<T> w(a, row);
+        float that, p, shat, dy, ds;
+        wide_terms(a, w, row, c, a.stats[row], a.stats[a.rows + row], a.mean[row], that, p, shat, dy, ds);
+        sums[0] = fmaf(dy, shat, sums[0]);
+        sums[1] = fmaf(ds, p, sums[1]);
+        sums[2] = fmaf(ds * (a.scale ? a.scale[c] : 1.f), that, sums[2]);
+    }
+    float *part = a.part + (int64_t)blockIdx.y * 3 * a.D + c;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) part[(int64_t)q * a.D] = sums[q];
+}
+
+__global__ __launch_bounds__(1024) void residual_norm_sum_kernel(ResidualNormArgs a, int rows) {
+    __shared__ float red[16][64];
+    const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x % 64, cols = 3 * (int64_t)a.D;
+    const float s = rows_sum<16>(a.part + min(col, cols - 1), rows, cols, red);
+    if (threadIdx.x >= 64 || col >= cols) return;
+    float *out = col < a.D ? a.dpre : col < 2 * (int64_t)a.D ? a.dscale : a.dpost;
+    if (out) out[col % a.D] = s;
+}
+
+// Rows that registers hold: 8192 channels, 4096 where accesses take one value.
+constexpr int kRnMost = 8192, kRnMostOne = 4096;
+
+int64_t residual_norm_bwd_blocks(int64_t rows) { return rows < kRnBwdBlocks ? rows : kRnBwdBlocks; }
+size_t residual_norm_mean_rows(int64_t rows, int64_t D) { return D > kRnMostOne ? (size_t)rows : 0; }
+
+static bool rn_sums(const ResidualNormArgs &a) { return a.dpre || a.dscale || a.dpost; }
+
+// Every row that the call reads or writes starts on 16 bytes and is a whole number of them.
+static bool rn_vec(const ResidualNormArgs &a) {
+    const int64_t e = a.dtype == 1 ? 2 : 4;
+    auto at = [&](const void *p, int64_t stride) { return ((uintptr_t)p & 15u) == 0 && (!p || stride * e % 16 == 0); };
+    return a.D * e % 16 == 0 && at(a.branch, a.branch_stride) && at(a.gate, a.gate_stride) &&
+           at(a.residual, a.residual_stride) && at(a.dy, a.dy_stride) && at(a.dtotal, a.dtotal_stride) && at(a.y, a.D) &&
+           at(a.total, a.D) && at(a.dbranch, a.D) && at(a.dgate, a.D) && at(a.dresidual, a.D);
+}
+
+bool residual_norm_fits(const ResidualNormArgs &a) {
+    return a.D <= (rn_vec(a) ? kRnMost : kRnMostOne) || (grid_fits(a.rows, 1024) && grid_fits((3 * (int64_t)a.D + 63) / 64, 1024));
+}
+
+template <typename T, int V, int K, int WPR>
+static hipError_t rn_fwd(const ResidualNormArgs &a, hipStream_t s) {
+    constexpr int R = rn_rows<WPR>();
+    const int64_t n = min((a.rows + R - 1) / R, (int64_t)kRnFwdBlocks);
+    residual_norm_fwd_kernel<T, V, K, WPR><<<(uint32_t)n, rn_threads<WPR>(), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+static hipError_t rn_sum(const ResidualNormArgs &a, int64_t blocks, hipStream_t s) {
+    if (!rn_sums(a)) return hipSuccess;
+    residual_norm_sum_kernel<<<(uint32_t)((3 * (int64_t)a.D + 63) / 64), 1024, 0, s>>>(a, (int)blocks);
+    return hipGetLastError();
+}
+
+template <typename T, int V, int K, int WPR>
+static hipError_t rn_bwd(const ResidualNormArgs &a0, hipStream_t s) {
+    constexpr int R = rn_rows<WPR>();
+    ResidualNormArgs a = a0;
+    if (!rn_sums(a)) a.part = nullptr;
+    const int64_t n = min((a.rows + R - 1) / R, residual_norm_bwd_blocks(a.rows));
+    residual_norm_bwd_kernel<T, V, K, WPR><<<(uint32_t)n, rn_threads<WPR>(), 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : rn_sum(a, n, s);
+}
+
+template <typename T>
+static hipError_t rn_fwd_wide(const ResidualNormArgs &a, hipStream_t s) {
+    residual_norm_fwd_wide_kernel<T><<<(uint32_t)a.rows, 1024, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t rn_bwd_wide(const ResidualNormArgs &a, hipStream_t s) {
+    residual_norm_bwd_wide_kernel<T><<<(uint32_t)a.rows, 1024, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !rn_sums(a)) return e;
+    const int64_t n = residual_norm_bwd_blocks(a.rows);
+    residual_norm_bwd_cols_kernel<T><<<dim3((a.D + 255) / 256, (uint32_t)n), 256, 0, s>>>(a);
+    e = hipGetLastError();
+    return e != hipSuccess ? e : rn_sum(a, n, s);
+}
+
+// The fewest waves that hold a row of D channels at 16 bytes (16 values at most) or one value
+// an access.
+#define RN_BF16(DIR)                                                     \
+    do {                                                                 \
+        if (a.D <= 512) return rn_##DIR<bf16, 8, 1, 1>(a, s);            \
+        if (a.D <= 1024) return rn_##DIR<bf16, 8, 2, 1>(a, s);           \
+        if (a.D <= 2048) return rn_##DIR<bf16, 8, 1, 4>(a, s);           \
+        if (a.D <= 4096) return rn_##DIR<bf16, 8, 2, 4>(a, s);           \
+        if (a.D <= kRnMost) return rn_##DIR<bf16, 8, 2, 8>(a, s);        \
+    } while (0)
+#define RN_F32(DIR)                                                      \
+    do {                                                                 \
+        if (a.D <= 256) return rn_##DIR<float, 4, 1, 1>(a, s);           \
+        if (a.D <= 512) return rn_##DIR<float, 4, 2, 1>(a, s);           \
+        if (a.D <= 1024) return rn_##DIR<float, 4, 1, 4>(a, s);          \
+        if (a.D <= 2048) return rn_##DIR<float, 4, 2, 4>(a, s);          \
+        if (a.D <= 4096) return rn_##DIR<float, 4, 4, 4>(a, s);          \
+        if (a.D <= kRnMost) return rn_##DIR<float, 4, 4, 8>(a, s);       \
+    } while (0)
+#define RN_ONE(DIR, T)                                                   \
+    do {                                                                 \
+        if (a.D <= 256) return rn_##DIR<T, 1, 4, 1>(a, s);               \
+        if (a.D <= 1024) return rn_##DIR<T, 1, 4, 4>(a, s);              \
+        if (a.D <= 2048) return rn_##DIR<T, 1, 8, 4>(a, s);              \
+        if (a.D <= kRnMostOne) return rn_##DIR<T, 1, 8, 8>(a, s);        \
+    } while (0)
+
+#define RN_LAUNCH(DIR)                              \
+    do {                                            \
+        const bool vec = rn_vec(a);                 \
+        if (a.dtype == 1) {                         \
+            if (vec) RN_BF16(DIR);                  \
+            RN_ONE(DIR, bf16);                      \
+            return rn_##DIR##_wide<bf16>(a, s);     \
+        }                                           \
+        if (vec) RN_F32(DIR);                       \
+        RN_ONE(DIR, float);                         \
+        return rn_##DIR##_wide<float>(a, s);        \
+    } while (0)
+
+hipError_t launch_residual_norm_fwd(const ResidualNormArgs &a, hipStream_t s) { RN_LAUNCH(fwd); }
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t s) { RN_LAUNCH(bwd); }
+
+}  // namespace ssd

@@ -19,6 +19,7 @@ SSD_FLAG_WAVEFRONT = 2
 SSD_FLAG_SCAN_FORM = 4
 SSD_FLAG_SILU = 8
 SSD_FLAG_SOFTPLUS = 16
+SSD_FLAG_GELU = 32
 
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL_ARG", 2: "SSD_ERR_BAD_SHAPE", 3: "SSD_ERR_BAD_DTYPE",
           4: "SSD_ERR_UNSUPPORTED", 5: "SSD_ERR_MISALIGNED", 6: "SSD_ERR_WORKSPACE",
@@ -32,7 +33,11 @@ EXPORTS = ["ssd_chunk_scan_workspace_bytes", "ssd_chunk_scan_fwd", "ssd_segmente
            "ssd_conv_fwd", "ssd_conv_step", "ssd_conv_bwd", "ssd_conv_bwd_workspace_bytes",
            "ssd_selective_fwd", "ssd_selective_step", "ssd_selective_bwd", "ssd_selective_kept_bytes",
            "ssd_selective_fwd_workspace_bytes", "ssd_selective_bwd_workspace_bytes",
-           "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_bytes"]
+           "ssd_norm_fwd", "ssd_norm_bwd", "ssd_norm_bwd_workspace_bytes",
+           "ssd_linear_fwd", "ssd_linear_bwd", "ssd_linear_fwd_workspace_bytes", "ssd_linear_bwd_workspace_bytes",
+           "ssd_gated_fwd", "ssd_gated_bwd", "ssd_gated_fwd_workspace_bytes", "ssd_gated_bwd_workspace_bytes",
+           "ssd_residual_norm_fwd", "ssd_residual_norm_bwd", "ssd_residual_norm_bwd_workspace_bytes",
+           "ssd_clip", "ssd_clip_workspace_bytes"]
 
 # Workspace limit of ssd_chunk_scan_fwd_noalloc (SSD_NOALLOC_SCRATCH_BYTES in the header).
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -61,6 +66,19 @@ class SelectiveDims(ctypes.Structure):
 class NormDims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("x_row_stride", ctypes.c_int64), ("dy_row_stride", ctypes.c_int64)]
+
+
+class ProductDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("inner", ctypes.c_int64), ("outer", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_row_stride", ctypes.c_int64), ("residual_row_stride", ctypes.c_int64),
+                ("dy_row_stride", ctypes.c_int64)]
+
+
+class ResidualNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("branch_row_stride", ctypes.c_int64),
+                ("residual_row_stride", ctypes.c_int64), ("gate_row_stride", ctypes.c_int64),
+                ("dy_row_stride", ctypes.c_int64), ("dtotal_row_stride", ctypes.c_int64)]
 
 
 class SSDError(RuntimeError):
@@ -103,6 +121,7 @@ def lib():
         L.ssd_shape_supported.argtypes = [i32, i32, i64, i64]
         L.ssd_shape_supported.restype = i32
         cp, sp, np_ = ctypes.POINTER(ConvDims), ctypes.POINTER(SelectiveDims), ctypes.POINTER(NormDims)
+        pp, rp = ctypes.POINTER(ProductDims), ctypes.POINTER(ResidualNormDims)
         f32 = ctypes.c_float
         for name, args in (("ssd_conv_fwd", [cp] + [vp] * 7 + [u32, vp]),
                            ("ssd_conv_step", [cp] + [vp] * 6 + [u32, vp]),
@@ -111,13 +130,25 @@ def lib():
                            ("ssd_selective_step", [sp] + [vp] * 11 + [u32, vp]),
                            ("ssd_selective_bwd", [sp] + [vp] * 21 + [u32, vp, sz, vp]),
                            ("ssd_norm_fwd", [np_, vp, vp, vp, f32, vp, vp, vp, vp]),
-                           ("ssd_norm_bwd", [np_] + [vp] * 9 + [sz, vp])):
+                           ("ssd_norm_bwd", [np_] + [vp] * 9 + [sz, vp]),
+                           ("ssd_linear_fwd", [pp] + [vp] * 6 + [u32, vp, sz, vp]),
+                           ("ssd_linear_bwd", [pp] + [vp] * 7 + [u32, vp, sz, vp]),
+                           ("ssd_gated_fwd", [pp] + [vp] * 5 + [u32, vp, sz, vp]),
+                           ("ssd_gated_bwd", [pp] + [vp] * 7 + [u32, vp, sz, vp]),
+                           ("ssd_residual_norm_fwd", [rp] + [vp] * 6 + [f32] + [vp] * 4),
+                           ("ssd_residual_norm_bwd", [rp] + [vp] * 16 + [sz, vp]),
+                           ("ssd_clip", [i32] + [vp] * 4 + [ctypes.c_double, vp, vp, sz, vp])):
             getattr(L, name).argtypes = args
             getattr(L, name).restype = ctypes.c_int
         for name, arg in (("ssd_conv_bwd_workspace_bytes", cp), ("ssd_selective_kept_bytes", sp),
                           ("ssd_selective_fwd_workspace_bytes", sp), ("ssd_selective_bwd_workspace_bytes", sp),
-                          ("ssd_norm_bwd_workspace_bytes", np_)):
+                          ("ssd_norm_bwd_workspace_bytes", np_), ("ssd_linear_fwd_workspace_bytes", pp),
+                          ("ssd_gated_fwd_workspace_bytes", pp), ("ssd_gated_bwd_workspace_bytes", pp),
+                          ("ssd_residual_norm_bwd_workspace_bytes", rp)):
             getattr(L, name).argtypes = [arg]
+            getattr(L, name).restype = sz
+        for name, args in (("ssd_linear_bwd_workspace_bytes", [pp, u32]), ("ssd_clip_workspace_bytes", [i32, vp])):
+            getattr(L, name).argtypes = args
             getattr(L, name).restype = sz
         L.ssd_status_string.argtypes = [ctypes.c_int]
         L.ssd_status_string.restype = ctypes.c_char_p
@@ -818,3 +849,288 @@ def norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
     _check(L_.ssd_norm_bwd(dims, gp, xp, wp, mp, rp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias), ws.data_ptr(),
                            ws.numel(), _current(x)))
     return g
+
+
+# ------------------------------------------- a layer's feed-forward half, and its training step
+# Conventions as above.  Weights and biases of products are of the activations' dtype, as their
+# gradients are; the norms' and the scale's parameters and gradients are float32.
+
+_ACT_FLAG = {None: 0, "silu": SSD_FLAG_SILU, "gelu": SSD_FLAG_GELU}
+
+
+def _act_flag(act):
+    try:
+        return _ACT_FLAG[act]
+    except (KeyError, TypeError):
+        raise ValueError("act must be None, 'silu' or 'gelu' (got %r)" % (act,)) from None
+
+
+def _product_inputs(x, weight, bias, gated):
+    """Checks of a product's inputs; (dtype code, rows, inner, outer, x's row stride, pointers of
+    x, weight and bias)."""
+    code = _activation("x", x, 2)
+    m, k = x.shape
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a torch.Tensor [outer, inner]")
+    n = weight.shape[0]
+    if gated and n % 2:
+        raise ValueError("weight has %d rows; a gated product has as many for g as for u" % n)
+    dev, dtype = x.device, x.dtype
+    xp, xs, _ = _rows("x", x, (m, k), dtype, dev)
+    wp = _param("weight", weight, (n, k), dev, dtype)
+    bp = _param("bias", bias, (n,), dev, dtype)
+    return code, m, k, n // 2 if gated else n, xs, (xp, wp, bp)
+
+
+def linear_fwd(x, weight, bias=None, residual=None, *, act=None, y=None, keep=False, workspace=None, stream=None):
+    """Matrix product with bias, activation and residual in its epilogue (ssd_linear_fwd):
+        pre = x weight^T + bias;  y = act(pre) + residual
+    x [M, K], weight [N, K], bias [N], residual [M, N], all of one dtype; act None, "silu" or
+    "gelu".  Returns y [M, N], or with keep=True (y, pre), where pre is what linear_bwd needs
+    (None without an activation)."""
+    L_ = lib()
+    flag = _act_flag(act)
+    code, m, k, n, xs, ptrs = _product_inputs(x, weight, bias, False)
+    dev, dtype = x.device, x.dtype
+    rp, rs, _ = _rows("residual", residual, (m, n), dtype, dev) if residual is not None else (None, 0, 0)
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return linear_fwd(x, weight, bias, residual, act=act, y=y, keep=keep, workspace=workspace)
+    dims = ProductDims(m, k, n, code, 0, xs, rs, 0)
+    ws = _workspace(workspace, L_.ssd_linear_fwd_workspace_bytes(dims), dev)
+    given = y
+    y = _out("y", y, (m, n), dtype, dev)
+    pre = torch.empty((m, n), dtype=dtype, device=dev) if keep and flag else None
+    _check(L_.ssd_linear_fwd(dims, *ptrs, rp, y.data_ptr(), _ptr(pre), flag, ws.data_ptr(), ws.numel(), _current(x)))
+    if given is not None:
+        _wrote(given)
+    return (y, pre) if keep else y
+
+
+class ProductGrads(NamedTuple):
+    dx: Optional[torch.Tensor]
+    dweight: Optional[torch.Tensor]
+    dbias: Optional[torch.Tensor]
+
+
+def _product_bwd(entry, gated, dy, x, weight, bias, pre, act, need, workspace, stream):
+    L_ = lib()
+    flag = _act_flag(act)
+    code, m, k, n, xs, (xp, wp, _) = _product_inputs(x, weight, bias, gated)
+    dev, dtype, cols = x.device, x.dtype, weight.shape[0]
+    gp, gs, _ = _rows("dh" if gated else "dy", dy, (m, n), dtype, dev)
+    if flag and pre is None:
+        raise ValueError("pre (from keep=True) is required")
+    pp = _param("pre", pre, (m, cols), dev, dtype) if flag else None
+    want_x, want_w, want_b = need
+    want_b = want_b and bias is not None
+    if not (want_x or want_w or want_b):
+        return ProductGrads(None, None, None)
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return _product_bwd(entry, gated, dy, x, weight, bias, pre, act, need, workspace, None)
+    dims = ProductDims(m, k, n, code, 0, xs, 0, gs)
+    size = L_.ssd_gated_bwd_workspace_bytes(dims) if gated else L_.ssd_linear_bwd_workspace_bytes(dims, flag)
+    ws = _workspace(workspace, size, dev)
+    g = ProductGrads(torch.empty((m, k), dtype=dtype, device=dev) if want_x else None,
+                     torch.empty((cols, k), dtype=dtype, device=dev) if want_w else None,
+                     torch.empty((cols,), dtype=dtype, device=dev) if want_b else None)
+    _check(getattr(L_, entry)(dims, gp, xp, wp, pp, _ptr(g.dx), _ptr(g.dweight), _ptr(g.dbias), flag, ws.data_ptr(),
+                              ws.numel(), _current(x)))
+    return g
+
+
+def linear_bwd(dy, x, weight, bias=None, pre=None, *, act=None, need=(True, True, True), workspace=None, stream=None):
+    """Gradients of linear_fwd (ssd_linear_bwd) from dy [M, N], with the pre of a
+    linear_fwd(keep=True) on the same arguments where there is an activation.  need: which of
+    dx, dweight and dbias are wanted (the others are None, as dbias is where the forward had
+    no bias).  The residual's gradient is dy itself."""
+    return _product_bwd("ssd_linear_bwd", False, dy, x, weight, bias, pre, act, need, workspace, stream)
+
+
+def gated_fwd(x, weight, bias=None, *, act="silu", h=None, keep=False, workspace=None, stream=None):
+    """Gated product (ssd_gated_fwd): both projections of a gated feed-forward, its activation
+    and their product in one kernel:
+        [g | u] = x weight^T + bias;  h = act(g) u
+    x [M, K], weight [2 F, K] (the rows of g, then those of u), bias [2 F], all of one dtype;
+    act "silu" or "gelu".  Returns h [M, F], or with keep=True (h, pre), where pre [M, 2 F] is
+    what gated_bwd needs."""
+    L_ = lib()
+    flag = _act_flag(act)
+    code, m, k, f, xs, ptrs = _product_inputs(x, weight, bias, True)
+    dev, dtype = x.device, x.dtype
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return gated_fwd(x, weight, bias, act=act, h=h, keep=keep, workspace=workspace)
+    dims = ProductDims(m, k, f, code, 0, xs, 0, 0)
+    ws = _workspace(workspace, L_.ssd_gated_fwd_workspace_bytes(dims), dev)
+    given = h
+    h = _out("h", h, (m, f), dtype, dev)
+    pre = torch.empty((m, 2 * f), dtype=dtype, device=dev) if keep else None
+    _check(L_.ssd_gated_fwd(dims, *ptrs, h.data_ptr(), _ptr(pre), flag, ws.data_ptr(), ws.numel(), _current(x)))
+    if given is not None:
+        _wrote(given)
+    return (h, pre) if keep else h
+
+
+def gated_bwd(dh, x, weight, bias, pre, *, act="silu", need=(True, True, True), workspace=None, stream=None):
+    """Gradients of gated_fwd (ssd_gated_bwd) from dh [M, F], with the pre of a
+    gated_fwd(keep=True) on the same arguments; need as for linear_bwd."""
+    return _product_bwd("ssd_gated_bwd", True, dh, x, weight, bias, pre, act, need, workspace, stream)
+
+
+def _residual_norm_inputs(branch, residual, gate, post_weight, scale, pre_weight, dy=None, dtotal=None):
+    """Checks of the residual norm's inputs; (dims, pointers of branch to pre_weight, of dy and
+    of dtotal)."""
+    code = _activation("branch", branch, 2)
+    rows, d = branch.shape
+    dev, dtype = branch.device, branch.dtype
+
+    def view(name, t):
+        return _rows(name, t, (rows, d), dtype, dev)[:2] if t is not None else (None, 0)
+    bp, bs = view("branch", branch)
+    rp, rs = view("residual", residual)
+    zp, zs = view("gate", gate)
+    gp, gs = view("dy", dy)
+    tp, ts = view("dtotal", dtotal)
+    ptrs = (bp, rp, zp, _param("post_weight", post_weight, (d,), dev), _param("scale", scale, (d,), dev),
+            _param("pre_weight", pre_weight, (d,), dev))
+    return ResidualNormDims(rows, d, code, 0, bs, rs, zs, gs, ts), ptrs, gp, tp
+
+
+def residual_norm_fwd(branch, residual=None, gate=None, post_weight=None, scale=None, pre_weight=None, eps=1e-5, *,
+                      y=None, total=None, want_stats=False, stream=None):
+    """The norms after and before a block with its gate, its scale and the residual
+    (ssd_residual_norm_fwd), rms(v) = v / sqrt(mean(v^2) + eps) over a row:
+        t = branch silu(gate);  total = residual + scale rms(t) post_weight;  y = rms(total) pre_weight
+    branch, residual and gate [rows, D] of one dtype; post_weight, scale and pre_weight [D]
+    float32.  What is None drops out: without post_weight there is no norm of t, without
+    pre_weight y is None.  Returns (y, total), or with want_stats=True (y, total, stats), where
+    stats [2, rows] is what residual_norm_bwd needs.  total may be residual, which is then
+    updated in place."""
+    L_ = lib()
+    dims, ptrs, _, _ = _residual_norm_inputs(branch, residual, gate, post_weight, scale, pre_weight)
+    if y is not None and pre_weight is None:
+        raise ValueError("y is given without pre_weight")
+    ctx = _elsewhere(branch, stream)
+    if ctx is not None:
+        with ctx:
+            return residual_norm_fwd(branch, residual, gate, post_weight, scale, pre_weight, eps, y=y, total=total,
+                                     want_stats=want_stats)
+    given = (y, total)
+    total = _out_like("total", total, branch)
+    if pre_weight is not None:
+        y = _out_like("y", y, branch)
+    stats = None
+    if want_stats:
+        stats = torch.empty((2, branch.shape[0]), dtype=torch.float32, device=branch.device)
+    _check(L_.ssd_residual_norm_fwd(dims, *ptrs, eps, total.data_ptr(), _ptr(y), _ptr(stats), _current(branch)))
+    if given != (None, None):
+        _wrote(*given)
+    return (y, total, stats) if want_stats else (y, total)
+
+
+class ResidualNormGrads(NamedTuple):
+    dbranch: torch.Tensor
+    dresidual: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dpre_weight: Optional[torch.Tensor]
+
+
+def residual_norm_bwd(dy, dtotal, branch, residual, gate, post_weight, scale, pre_weight, stats, *, workspace=None,
+                      stream=None):
+    """Gradients of residual_norm_fwd (ssd_residual_norm_bwd) from dy (None exactly without
+    pre_weight) and dtotal, the gradient of total (may be None beside dy), both [rows, D], with
+    the forward's inputs and stats.  Gradients of what was None are None."""
+    L_ = lib()
+    dims, ptrs, gp, tp = _residual_norm_inputs(branch, residual, gate, post_weight, scale, pre_weight, dy, dtotal)
+    rows, d = branch.shape
+    dev = branch.device
+    if (dy is None) != (pre_weight is None):
+        raise ValueError("dy has to be given exactly if pre_weight is")
+    if dy is None and dtotal is None:
+        raise ValueError("dy and dtotal are both None")
+    sp = _param("stats", stats, (2, rows), dev)
+    if sp is None:
+        raise ValueError("stats (from want_stats=True) is required")
+    ctx = _elsewhere(branch, stream)
+    if ctx is not None:
+        with ctx:
+            return residual_norm_bwd(dy, dtotal, branch, residual, gate, post_weight, scale, pre_weight, stats,
+                                     workspace=workspace)
+    ws = _workspace(workspace, L_.ssd_residual_norm_bwd_workspace_bytes(dims), dev)
+
+    def act(t):
+        return None if t is None else torch.empty((rows, d), dtype=branch.dtype, device=dev)
+
+    def f32(t):
+        return None if t is None else torch.empty((d,), dtype=torch.float32, device=dev)
+    g = ResidualNormGrads(act(branch), act(residual), act(gate), f32(post_weight), f32(scale), f32(pre_weight))
+    _check(L_.ssd_residual_norm_bwd(dims, gp, tp, *ptrs, sp, _ptr(g.dbranch), _ptr(g.dresidual), _ptr(g.dgate),
+                                    _ptr(g.dpost_weight), _ptr(g.dscale), _ptr(g.dpre_weight), ws.data_ptr(), ws.numel(),
+                                    _current(branch)))
+    return g
+
+
+def _clip(tensors, max_norm, out, scale, workspace, stream):
+    L_ = lib()
+    tensors = list(tensors)
+    n = len(tensors)
+    if n == 0:
+        raise ValueError("no tensors given")
+    first = tensors[0]
+    if not isinstance(first, torch.Tensor):
+        raise ValueError("tensor 0 must be a torch.Tensor (got %s)" % type(first).__name__)
+    dev = first.device
+    ptrs, sizes, codes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError("tensor %d must be a torch.Tensor (got %s)" % (i, type(t).__name__))
+        code = _DTYPE_CODE.get(t.dtype)
+        if code is None:
+            raise ValueError("tensor %d has dtype %s; expected torch.float32 or torch.bfloat16" % (i, t.dtype))
+        if t.device != dev:
+            raise ValueError("tensor %d is on %s; expected %s" % (i, t.device, dev))
+        if not t.is_contiguous():
+            raise ValueError("tensor %d must be contiguous" % i)
+        ptrs[i], sizes[i], codes[i] = t.data_ptr(), t.numel(), code
+    outs = ptrs if scale else None
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError("out has %d tensors; expected %d" % (len(out), n))
+        outs = (ctypes.c_void_p * n)()
+        for i, (o, t) in enumerate(zip(out, tensors)):
+            outs[i] = _param("out %d" % i, o, t.shape, dev, t.dtype)
+            if o is None:
+                raise ValueError("out %d is required" % i)
+    ctx = _elsewhere(first, stream)
+    if ctx is not None:
+        with ctx:
+            return _clip(tensors, max_norm, out, scale, workspace, None)
+    ws = _workspace(workspace, L_.ssd_clip_workspace_bytes(n, sizes), dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    _check(L_.ssd_clip(n, ptrs, outs, sizes, codes, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                       _current(first)))
+    if scale:
+        _wrote(*(tensors if out is None else out))
+    return norm
+
+
+def grad_norm(tensors, *, workspace=None, stream=None):
+    """The norm of all elements of the tensors together (ssd_clip without its scaling): any number
+    of contiguous float32 and bfloat16 tensors on one device.  Returns a float32 scalar on it."""
+    return _clip(tensors, 0.0, None, False, workspace, stream)
+
+
+def clip_grads(tensors, max_norm, *, out=None, workspace=None, stream=None):
+    """Scales the tensors by min(1, max_norm / norm), norm as grad_norm's (ssd_clip), in place or
+    into `out` (tensors of the same shapes and dtypes).  A norm that is not finite leaves the
+    values as they are.  Returns the norm (of the values before), a float32 scalar on their
+    device; nothing waits for it."""
+    return _clip(tensors, max_norm, out, True, workspace, stream)

@@ -378,6 +378,118 @@ ssd_status_t ssd_norm_bwd(const ssd_norm_dims_t *dims, const void *dy, const voi
                           const float *mean, const float *rstd, void *dx, float *dweight, float *dbias,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- a layer's feed-forward half, and its training step -------------------------- *
+ *
+ * The matrix product with bias, activation and residual; the gated product (both projections
+ * of a gated feed-forward, its activation and their product); the norms after and before a
+ * block with its gate, its scale and the residual; and the norm over many gradients with
+ * clipping by it.  Conventions as above: views at any row stride for activation inputs,
+ * contiguous outputs and parameters, everything computed in float32 and rounded once when
+ * stored, sums in a fixed order, no allocation, no synchronisation.  Weights and biases of
+ * products are in the activation dtype, as their gradients are; the norms' and the scale's
+ * parameters and gradients are float32.  A zero count of rows or channels is refused. */
+#define SSD_FLAG_GELU 32u      /* ssd_linear_*, ssd_gated_*: act(v) = v Phi(v), Phi the normal
+                                  distribution's function; SSD_FLAG_SILU: v sigmoid(v); neither:
+                                  v (linear only); not both                                   */
+
+typedef struct ssd_product_dims {
+    int64_t rows;      /* M                                                              */
+    int64_t inner;     /* K                                                              */
+    int64_t outer;     /* N: columns of the result (gated: F)                            */
+    int32_t dtype;     /* ssd_dtype_t                                                    */
+    int32_t reserved;  /* must be 0                                                      */
+    int64_t x_row_stride;
+    int64_t residual_row_stride;   /* ssd_linear_fwd with a residual                     */
+    int64_t dy_row_stride;         /* backward only                                      */
+} ssd_product_dims_t;
+
+/* y = act(pre) + residual,  pre = x weight^T + bias:
+ *   x         view [rows, inner] (act) at x_row_stride
+ *   weight    [outer, inner] (act); bias [outer] (act) or NULL
+ *   residual  view [rows, outer] (act) or NULL
+ *   y         [rows, outer] (act); pre [rows, outer] (act) or NULL (ssd_linear_bwd needs it
+ *             where there is an activation)
+ *   flags     0, SSD_FLAG_SILU or SSD_FLAG_GELU
+ *   workspace ssd_linear_fwd_workspace_bytes (0 where the product's inner dimension is not
+ *             cut: it may then be NULL) */
+size_t ssd_linear_fwd_workspace_bytes(const ssd_product_dims_t *dims);
+ssd_status_t ssd_linear_fwd(const ssd_product_dims_t *dims, const void *x, const void *weight, const void *bias,
+                            const void *residual, void *y, void *pre, uint32_t flags, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Gradients of ssd_linear_fwd from dy (view [rows, outer], act), with the forward's x, weight
+ * and, where there is an activation, pre: dx [rows, inner], dweight [outer, inner], dbias
+ * [outer] (act), each NULL where it is not wanted.  The residual's gradient is dy.  dy act'(pre)
+ * is rounded to the activation dtype before it enters dx and dweight. */
+size_t ssd_linear_bwd_workspace_bytes(const ssd_product_dims_t *dims, uint32_t flags);
+ssd_status_t ssd_linear_bwd(const ssd_product_dims_t *dims, const void *dy, const void *x, const void *weight,
+                            const void *pre, void *dx, void *dweight, void *dbias, uint32_t flags, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* h = act(g) u,  [g | u] = x weight^T + bias:
+ *   x       view [rows, inner] (act) at x_row_stride
+ *   weight  [2 outer, inner] (act): the rows of g, then those of u; bias [2 outer] or NULL
+ *   h       [rows, outer] (act); pre [rows, 2 outer] (act) or NULL: [g | u], which
+ *           ssd_gated_bwd needs
+ *   flags   SSD_FLAG_SILU or SSD_FLAG_GELU */
+size_t ssd_gated_fwd_workspace_bytes(const ssd_product_dims_t *dims);
+ssd_status_t ssd_gated_fwd(const ssd_product_dims_t *dims, const void *x, const void *weight, const void *bias, void *h,
+                           void *pre, uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of ssd_gated_fwd from dh (view [rows, outer] at dy_row_stride, act): dx [rows, inner],
+ * dweight [2 outer, inner], dbias [2 outer] (act), each NULL where it is not wanted. */
+size_t ssd_gated_bwd_workspace_bytes(const ssd_product_dims_t *dims);
+ssd_status_t ssd_gated_bwd(const ssd_product_dims_t *dims, const void *dh, const void *x, const void *weight,
+                           const void *pre, void *dx, void *dweight, void *dbias, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+typedef struct ssd_residual_norm_dims {
+    int64_t rows, channels;
+    int32_t dtype;     /* ssd_dtype_t                                                    */
+    int32_t reserved;  /* must be 0                                                      */
+    int64_t branch_row_stride, residual_row_stride, gate_row_stride;
+    int64_t dy_row_stride, dtotal_row_stride;   /* backward only                         */
+} ssd_residual_norm_dims_t;
+
+/* The norms after and before a block, rms(v) = v / sqrt(mean(v^2) + eps) over a row:
+ *     t = branch gate sigmoid(gate);  p = rms(t) post_weight;  total = residual + scale p;
+ *     y = rms(total) pre_weight                     (of total before it is rounded)
+ * branch, residual and gate are views [rows, channels] (act); residual, gate, post_weight,
+ * scale and pre_weight (the last three [channels] float32) may be NULL: what they bring drops
+ * out (no post_weight: p = t; no pre_weight: y must be NULL).  total and y [rows, channels]
+ * (act); total may be residual at a row stride of channels (updated in place).  stats
+ * [2, rows] float32 or NULL, which ssd_residual_norm_bwd needs: 1 / rms of t and of total
+ * (1 without that norm). */
+ssd_status_t ssd_residual_norm_fwd(const ssd_residual_norm_dims_t *dims, const void *branch, const void *residual,
+                                   const void *gate, const float *post_weight, const float *scale,
+                                   const float *pre_weight, float eps, void *total, void *y, float *stats,
+                                   void *stream);
+
+/* Gradients of ssd_residual_norm_fwd from dy (view, act; exactly if there is a pre_weight) and
+ * dtotal (view, act, the gradient of total; may be NULL if dy is given): dbranch, dresidual
+ * (or NULL) and dgate (exactly if gate is given) [rows, channels] (act); dpost_weight, dscale
+ * and dpre_weight [channels] float32, each NULL where it is not wanted or its parameter not
+ * given. */
+size_t ssd_residual_norm_bwd_workspace_bytes(const ssd_residual_norm_dims_t *dims);
+ssd_status_t ssd_residual_norm_bwd(const ssd_residual_norm_dims_t *dims, const void *dy, const void *dtotal,
+                                   const void *branch, const void *residual, const void *gate,
+                                   const float *post_weight, const float *scale, const float *pre_weight,
+                                   const float *stats, void *dbranch, void *dresidual, void *dgate,
+                                   float *dpost_weight, float *dscale, float *dpre_weight, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* norm = sqrt of the sum of the squares of every element of `count` tensors (host arrays of
+ * device pointers, element counts >= 0 and ssd_dtype_t), in float64 until it is stored, and
+ * out[i] = in[i] min(1, max_norm / norm).  Where norm is not finite, and where it does not exceed
+ * max_norm, values are left as they are.  in[i] and out[i] are the same pointer (clipped in
+ * place) or do not overlap; out may be NULL (the norm alone; max_norm is then not looked at).
+ * norm [1] float32 on the device.  max_norm >= 0, infinity included.  The host arrays are read
+ * before the call returns. */
+size_t ssd_clip_workspace_bytes(int32_t count, const int64_t *sizes);
+ssd_status_t ssd_clip(int32_t count, const void *const *in, void *const *out, const int64_t *sizes,
+                      const int32_t *dtypes, double max_norm, float *norm, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 /* ---- inspection (tests and tools) ------------------------------------------------ */
 
 /* Runs steps first_stage..last_stage of ssd_chunk_scan_fwd (1 = log-decay prefix sums,
