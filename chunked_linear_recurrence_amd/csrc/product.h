@@ -49,6 +49,7 @@ size_t product_workspace_bytes(const ProductArgs &a);
 hipError_t launch_product(const ProductArgs &a, hipStream_t s);
 
 // product_bf16.hip, product_f32.hip: operands copied to LDS directly; _any: from any address
+hipError_t launch_tiles_bf16_big(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_bf16(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_bf16_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_f32(const ProductArgs &a, const ProductGrid &g, hipStream_t s);

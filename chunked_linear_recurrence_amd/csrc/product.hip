@@ -15,29 +15,36 @@ static bool direct(const Operand &o, bool rows_contiguous, int64_t rows, int64_t
     return o.ld <= (int64_t)0x70000000 / e / span;
 }
 
-static ProductGrid grid_of(const ProductArgs &a, int64_t *tiles) {
-    const int64_t e = elem(a), ks = 128 / e, cols = a.kind == kGated ? 64 : 128;
-    const int64_t tm = (a.M + 127) / 128, tn = (a.N + cols - 1) / cols, steps = (a.K + ks - 1) / ks;
-    *tiles = tm <= INT32_MAX && tn <= INT32_MAX ? tm * tn : INT64_MAX;
-    int64_t splits = 1;
-    if (*tiles < 192) {
-        splits = 512 / *tiles;
-        if (splits > steps / 4) splits = steps / 4;
-        if (splits < 1) splits = 1;
-    }
+// Tiles of BM x BN and the steps of each split for a product of `splits` splits
+static ProductGrid cut(const ProductArgs &a, int64_t bm, int64_t bn, int64_t splits) {
+    const int64_t ks = 128 / elem(a), cols = a.kind == kGated ? bn / 2 : bn, steps = (a.K + ks - 1) / ks;
     const int64_t per = (steps + splits - 1) / splits;
-    return {(int)tm, (int)tn, (int)((steps + per - 1) / per), (int)per};
+    return {(int)((a.M + bm - 1) / bm), (int)((a.N + cols - 1) / cols), (int)((steps + per - 1) / per), (int)per};
+}
+static int64_t tiles_of(const ProductGrid &g) { return (int64_t)g.tiles_m * g.tiles_n; }
+
+static ProductGrid grid_of(const ProductArgs &a) {
+    const ProductGrid g = cut(a, 128, 128, 1);
+    const int64_t tiles = tiles_of(g);
+    if (tiles >= 192) return g;
+    int64_t splits = 512 / tiles;
+    if (splits > g.steps / 4) splits = g.steps / 4;
+    return cut(a, 128, 128, splits < 1 ? 1 : splits);
+}
+
+static bool big_tiles(const ProductArgs &a, ProductGrid *g) {
+    if (a.dtype != 1) return false;
+    *g = cut(a, 256, 256, 1);
+    const int64_t big = (tiles_of(*g) + 255) / 256, small = (tiles_of(cut(a, 128, 128, 1)) + 511) / 512;
+    return 8 * big <= 5 * small;
 }
 
 bool product_fits(const ProductArgs &a) {
-    int64_t tiles;
-    grid_of(a, &tiles);
-    return grid_fits(tiles, 256) && tiles <= INT32_MAX;
+    return grid_fits(tiles_of(grid_of(a)), 256);
 }
 
 size_t product_workspace_bytes(const ProductArgs &a) {
-    int64_t tiles;
-    const ProductGrid g = grid_of(a, &tiles);
+    const ProductGrid g = grid_of(a);
     return g.splits > 1 ? (size_t)g.splits * a.M * a.N * (a.kind == kGated ? 2 : 1) * 4 : 0;
 }
 
@@ -94,8 +101,9 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     const int64_t brows = a.kind == kGated ? 2 * a.N : a.N, bspan = a.kind == kGated ? a.N + 256 : 256;
     const bool dma = direct(a.a, a.a_rows, a.M, a.K, a.a_rows ? ks : 256, e) &&
                      direct(a.b, a.b_rows, brows, a.K, a.b_rows ? ks : bspan, e);
-    int64_t tiles;
-    const ProductGrid g = grid_of(a, &tiles);
+    ProductGrid g;
+    if (dma && big_tiles(a, &g)) return launch_tiles_bf16_big(a, g, s);
+    g = grid_of(a);
     hipError_t r;
     if (a.dtype == 1) r = dma ? launch_tiles_bf16(a, g, s) : launch_tiles_bf16_any(a, g, s);
     else r = dma ? launch_tiles_f32(a, g, s) : launch_tiles_f32_any(a, g, s);

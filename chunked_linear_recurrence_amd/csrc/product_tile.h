@@ -23,12 +23,29 @@
 // they meet no result that is stored.  Values past K are zeros in both operands.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "product.h"
 #include "ssd_tile.h"
 
 namespace ssd {
 
 constexpr int kStepBytes = 128;
+
+#define SSD_INLINE __attribute__((always_inline))     // of a lambda: its captures stay in registers
+
+constexpr int min_of(int a, int b) { return a < b ? a : b; }
+
+// f(0), f(1), .. f(N - 1) with constants for arguments
+template <class F, int... I>
+__device__ __forceinline__ void each_index(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each_of(F f) {
+    each_index(f, std::make_integer_sequence<int, N>{});
+}
 
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
@@ -169,27 +186,47 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
         }
     }
     u32x4 ra[C::DMA ? 1 : C::QA], rb[C::DMA ? 1 : C::QB];
-    // an operand's copies of the step at k: `rows` is where the operand's tile begins and `size`
-    // how many rows there are
-    auto copy = [&](auto layout, const Operand &o, int64_t at, int64_t size, int64_t k, int Q, const uint32_t *off,
-                    unsigned char *to) {
+    // An operand's source: where the next step to copy begins, the bytes from one step to the next,
+    // and those that a copy may read from there on, of the split's last step and of others, which
+    // reach to the end of the operand's next line.  Copies read zeros past them.
+    struct Source {
+        const unsigned char *at;
+        int64_t step;
+        uint32_t whole, last;
+    };
+    auto source = [&](auto layout, const Operand &o, int64_t row, int64_t size) SSD_INLINE {
         typedef decltype(layout) L;
-        const int64_t left = p.K - k;
-        constexpr int64_t kMost = 0x7fffffff;
-        const unsigned char *base = reinterpret_cast<const unsigned char *>(o.p) +
-                                    (L::ROWS ? k * o.ld + at : at * o.ld + k) * E;
-        const int64_t bytes = L::ROWS ? ((left - 1) * o.ld + size - at) * E : ((size - 1 - at) * o.ld + left) * E;
-        const rsrc_t rs = make_rsrc(base, (uint32_t)min(bytes, kMost));
-        for (int q = 0; q < Q; ++q) {
-            uint32_t v = off[q];
-            if (!L::ROWS && left < L::KS) {
-                const int piece = L::slot_piece((w * Q + q) * 64 + lane);
-                if (piece * V >= left) v = 0x80000000u;           // past K: zeros
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(to + (w * Q + q) * 1024), 16, v, 0, 0, 0);
+        auto bytes = [&](int64_t k) SSD_INLINE {
+            return (uint32_t)min((L::ROWS ? (k - 1) * o.ld + size - row : (size - 1 - row) * o.ld + k) * E, (int64_t)0x7fffffff);
+        };
+        return Source{reinterpret_cast<const unsigned char *>(o.p) + (L::ROWS ? k_first * o.ld + row : row * o.ld + k_first) * E,
+                      (L::ROWS ? o.ld * C::KS : C::KS) * E, bytes(C::KS + 1),
+                      bytes(min(p.K - k_first - (int64_t)(steps - 1) * C::KS, (int64_t)C::KS))};
+    };
+    // Copies `from` to `end` - 1 of step t of an operand; steps are copied in order, and the copies
+    // that end one move the source on.  Steps past the split's last read nothing and write zeros
+    // that meet no product.
+    auto copies = [&](auto layout, Source &src, int t, int from, int end, int Q, const uint32_t *off,
+                      unsigned char *to) SSD_INLINE {
+        if (from == end) return;
+        const rsrc_t rs = make_rsrc(src.at, t + 1 < steps ? src.whole : t < steps ? src.last : 0u);
+#pragma unroll
+        for (int q = from; q < end; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(to + (w * Q + q) * 1024), 16, off[q], 0, 0, 0);
+        if (end == Q) src.at += src.step;
+    };
+    // Zeros for what a copy of the step that K ends in took from behind K, where the operand's k is
+    // contiguous: the rest of its rows, or the next rows.
+    const int tail = first + steps == all && p.K % C::KS ? steps - 1 : -1;
+    auto clear_tail = [&](auto layout, unsigned char *m) SSD_INLINE {
+        typedef decltype(layout) L;
+        if constexpr (!L::ROWS) {
+            const int have = (int)(p.K % C::KS) / V;
+            for (int slot = threadIdx.x; slot < L::BYTES / 16; slot += C::THREADS)
+                if (L::slot_piece(slot) >= have) *reinterpret_cast<u32x4 *>(m + slot * 16) = u32x4{0, 0, 0, 0};
         }
     };
-    auto fetch = [&](auto layout, const Operand &o, int64_t at, int64_t size, bool is_b, int64_t k, int Q, u32x4 *reg) {
+    auto fetch = [&](auto layout, const Operand &o, int64_t at, int64_t size, bool is_b, int64_t k, int Q, u32x4 *reg) SSD_INLINE {
         typedef decltype(layout) L;
         for (int q = 0; q < Q; ++q) {
             const int slot = (w * Q + q) * 64 + lane, line = L::slot_line(slot), piece = L::slot_piece(slot);
@@ -215,24 +252,26 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
             reg[q] = v;
         }
     };
-    auto place = [&](int Q, const u32x4 *reg, unsigned char *to) {
+    auto place = [&](int Q, const u32x4 *reg, unsigned char *to) SSD_INLINE {
         for (int q = 0; q < Q; ++q) *reinterpret_cast<u32x4 *>(to + ((w * Q + q) * 64 + lane) * 16) = reg[q];
     };
     const int64_t a_size = p.M, b_size = C::KIND == kGated ? 2 * p.N : p.N;
-    // DMA: the copy of step t into (a, b).  Registers: what was fetched (step t) goes there, and
-    // the step after it is fetched.
-    auto start = [&](int t, unsigned char *a, unsigned char *b) {
-        const int64_t k = k_first + (int64_t)t * C::KS;
-        if constexpr (C::DMA) {
-            copy(LA{}, p.a, m0, a_size, k, C::QA, offa, a);
-            copy(LB{}, p.b, n0, b_size, k, C::QB, offb, b);
-        } else {
-            place(C::QA, ra, a);
-            place(C::QB, rb, b);
-            if (t + 1 < steps) {
-                fetch(LA{}, p.a, m0, a_size, false, k + C::KS, C::QA, ra);
-                fetch(LB{}, p.b, n0, b_size, true, k + C::KS, C::QB, rb);
-            }
+    Source src_a = source(LA{}, p.a, m0, a_size), src_b = source(LB{}, p.b, n0, b_size);
+    auto copies_a = [&](int t, int from, int end, unsigned char *to) SSD_INLINE {
+        copies(LA{}, src_a, t, from, end, C::QA, offa, to);
+    };
+    auto copies_b = [&](int t, int from, int end, unsigned char *to) SSD_INLINE {
+        copies(LB{}, src_b, t, from, end, C::QB, offb, to);
+    };
+    // By way of registers: what was fetched (step t) goes to (a, b), and the step after it is
+    // fetched.
+    auto store_fetch = [&](int t, unsigned char *a, unsigned char *b) SSD_INLINE {
+        place(C::QA, ra, a);
+        place(C::QB, rb, b);
+        if (t + 1 < steps) {
+            const int64_t k = k_first + (int64_t)(t + 1) * C::KS;
+            fetch(LA{}, p.a, m0, a_size, false, k, C::QA, ra);
+            fetch(LB{}, p.b, n0, b_size, true, k, C::QB, rb);
         }
     };
 
@@ -243,48 +282,91 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
 #pragma unroll
         for (int j = 0; j < C::TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     F a[2][C::TM], b[2][C::TN];
-    auto read = [&](int s, const unsigned char *ma, const unsigned char *mb) {
-#pragma unroll
-        for (int j = 0; j < C::TN; ++j)
-            b[s][j] = read_frag<LB, T>(mb, (j / C::NT) * (C::BN / 2) + wn * 16 * C::NT, j % C::NT, s, lane);
-#pragma unroll
-        for (int i = 0; i < C::TM; ++i) a[s][i] = read_frag<LA, T>(ma, wm * 16 * C::TM, i, s, lane);
+    auto read_b = [&](int s, int j, const unsigned char *m) SSD_INLINE {
+        b[s][j] = read_frag<LB, T>(m, (j / C::NT) * (C::BN / 2) + wn * 16 * C::NT, j % C::NT, s, lane);
     };
-    auto products = [&](int s) {
+    auto read_a = [&](int s, int i, const unsigned char *m) SSD_INLINE { a[s][i] = read_frag<LA, T>(m, wm * 16 * C::TM, i, s, lane); };
+    auto read = [&](int s, const unsigned char *ma, const unsigned char *mb) SSD_INLINE {
 #pragma unroll
-        for (int i = 0; i < C::TM; ++i)
+        for (int j = 0; j < C::TN; ++j) read_b(s, j, mb);
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i) read_a(s, i, ma);
+    };
+    // The products of slice s, one row of tiles after the other, in a fixed order with the reads of
+    // the other slice's fragments from (ma, mb), B's first, and the copies that `between` starts.
+    // The compiler's own order reads late and waits; a row's fragment is read no earlier than its
+    // place in the registers comes free, which keeps 256 registers enough for 8 x 4 tiles.
+    auto products = [&](int s, const unsigned char *ma, const unsigned char *mb, auto between) SSD_INLINE {
+        constexpr int R = C::TM + C::TN, GROUPS = C::TM - 1;
+        each_of<C::TM>([&](auto at) SSD_INLINE {
+            constexpr int i = decltype(at)::value;
+            between(at);
+            constexpr int first = min_of(R, (i * R + GROUPS - 1) / GROUPS), end = min_of(R, ((i + 1) * R + GROUPS - 1) / GROUPS);
+            each_of<end - first>([&](auto r) SSD_INLINE {
+                constexpr int q = first + decltype(r)::value;
+                if constexpr (q < C::TN) read_b(1 - s, q, mb);
+                else read_a(1 - s, q - C::TN, ma);
+            });
 #pragma unroll
             for (int j = 0; j < C::TN; ++j) acc[i][j] = multiply(b[s][j], a[s][i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     };
-    // this wave's copies have landed and its LDS reads are done, then every wave's; the compiler
-    // moves no access of memory across it
-    auto landed = [&] {
+    // This wave's copies have landed and its LDS reads are done, then every wave's; the compiler
+    // moves no access of memory across it.
+    auto landed = [&]() SSD_INLINE {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    auto step = [&](int t, unsigned char *a_cur, unsigned char *b_cur, unsigned char *a_next, unsigned char *b_next) {
-        read(1, a_cur, b_cur);
-        products(0);
+    auto clear = [&](unsigned char *a, unsigned char *b) SSD_INLINE {
+        clear_tail(LA{}, a);
+        clear_tail(LB{}, b);
         landed();
-        if (t + 2 < steps) start(t + 2, a_cur, b_cur);
-        if (t + 1 < steps) read(0, a_next, b_next);
-        products(1);
     };
-    if constexpr (!C::DMA) {
+    // Step t from (a0, b0); (a1, b1) are the next step's tiles.  The copies start as soon as a0 and b0
+    // are free, spread over half a slice (a copy of 64 x 16 bytes takes the memory pipe 16 cycles,
+    // and blocks the wave while the pipe is full).  After the last step the fragments read are
+    // whatever lies in LDS, and meet no product.
+    auto step = [&](int t, unsigned char *a0, unsigned char *b0, unsigned char *a1, unsigned char *b1) SSD_INLINE {
+        products(0, a0, b0, [](auto) {});
+        landed();
+        if constexpr (C::DMA) {
+            if (t + 1 == tail) clear(a1, b1);
+            products(1, a1, b1, [&](auto at) SSD_INLINE {
+                constexpr int i = decltype(at)::value, PARTS = C::TM / 4;
+                if constexpr (i < PARTS) copies_a(t + 2, i * C::QA / PARTS, (i + 1) * C::QA / PARTS, a0);
+                else if constexpr (i < 2 * PARTS)
+                    copies_b(t + 2, (i - PARTS) * C::QB / PARTS, (i - PARTS + 1) * C::QB / PARTS, b0);
+            });
+        } else {
+            if (t + 2 < steps) store_fetch(t + 2, a0, b0);
+            products(1, a1, b1, [](auto) {});
+        }
+    };
+    if constexpr (C::DMA) {
+        copies_a(0, 0, C::QA, A0);
+        copies_b(0, 0, C::QB, B0);
+        landed();
+        copies_a(1, 0, C::QA, A1);
+        copies_b(1, 0, C::QB, B1);
+        if (tail == 0) clear(A0, B0);
+    } else {
         fetch(LA{}, p.a, m0, a_size, false, k_first, C::QA, ra);
         fetch(LB{}, p.b, n0, b_size, true, k_first, C::QB, rb);
+        store_fetch(0, A0, B0);
+        if (steps > 1) store_fetch(1, A1, B1);
+        landed();
     }
-    start(0, A0, B0);
-    if constexpr (C::DMA) landed();
-    if (steps > 1) start(1, A1, B1);
-    if constexpr (!C::DMA) landed();
     read(0, A0, B0);
-    for (int t = 0; t < steps; t += 2) {
+    for (int t = 0;;) {
         step(t, A0, B0, A1, B1);
-        if (t + 1 < steps) step(t + 1, A1, B1, A0, B0);
+        if (++t >= steps) break;
+        step(t, A1, B1, A0, B0);
+        if (++t >= steps) break;
     }
+    if constexpr (C::DMA) __builtin_amdgcn_s_waitcnt(0x0f70);      // no copy is left behind
 
     // ---- results: this lane's columns are n .. n + 4 NT - 1 of each half
     const int i16 = lane & 15, g = lane >> 4;

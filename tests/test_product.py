@@ -15,6 +15,9 @@ SHAPES = [  # rows, inner, outer
     (31, 72, 200), (48, 512, 352), (64, 264, 136), (65, 72, 136), (128, 64, 128), (129, 128, 127), (130, 200, 264),
     (255, 777, 129), (300, 96, 520), (513, 640, 392), (700, 72, 1032), (1030, 136, 520),
 ]
+# enough tiles for the large ones, in each of the products: forward, by x, by the weight
+LARGE = [(2901, 200, 2840), (2901, 2840, 72), (72, 2840, 2904)]
+LARGE_GATED = [(2901, 200, 1424), (2901, 2840, 40), (72, 2840, 1456)]
 DTYPES = [torch.float32, torch.bfloat16]
 
 
@@ -43,6 +46,16 @@ def test_linear(shape, dtype, act):
     torch.cuda.synchronize()
     assert torch.equal(y, y2)
     R.check_linear(dtype, (y, pre) + g, x, w, b, r, act, dy)
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_linear_in_large_tiles(shape):
+    test_linear(shape, torch.bfloat16, "silu")
+
+
+@pytest.mark.parametrize("shape", LARGE_GATED, ids=str)
+def test_gated_in_large_tiles(shape):
+    test_gated(shape, torch.bfloat16, "silu")
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
