@@ -36,20 +36,35 @@ struct ProductArgs {
     int act;
     void *y;                      // [M, N]
     void *pre;                    // linear [M, N], gated [M, 2 F]; or null
-    float *part;                  // workspace of a product whose K is split: [splits, M, N or 2 F]
+    float *part;                  // workspace of tiles whose K is split: [rest, splits, bm, bn]
 };
 
-// How one launch cuts its product: tiles in m and n, splits of K, steps of K in each split.
+// How one launch cuts its product into tiles: `full` of them take one workgroup each, and each of
+// the `rest` behind them `splits` workgroups, of `steps` steps of K (128 bytes a row) each, whose
+// partial results a second kernel adds.
 struct ProductGrid {
-    int tiles_m, tiles_n, splits, steps;
+    int bm, bn;                   // rows and columns of B of a tile (gated: both halves')
+    int tiles_m, tiles_n;
+    int full, rest, splits, steps;
 };
+
+// Where tile `id` lies: in groups of 4 columns, row by row within a group, so that the 32 tiles that
+// an XCD (own L2) holds at a time share their operands.
+struct TileAt {
+    int m, n;
+};
+__host__ __device__ inline TileAt tile_at(int id, const ProductGrid &g) {
+    constexpr int G = 4;
+    const int group = id / (G * g.tiles_m), first = group * G, left = g.tiles_n - first, width = left < G ? left : G;
+    const int in = id - group * G * g.tiles_m;
+    return {in / width, first + in % width};
+}
 
 bool product_fits(const ProductArgs &a);                  // its work is within a launch
 size_t product_workspace_bytes(const ProductArgs &a);
 hipError_t launch_product(const ProductArgs &a, hipStream_t s);
 
-// product_bf16.hip, product_f32.hip: operands copied to LDS directly; _any: from any address
-hipError_t launch_tiles_bf16_big(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
+// One file each: operands copied to LDS directly, or (_any) from any address
 hipError_t launch_tiles_bf16(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_bf16_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_f32(const ProductArgs &a, const ProductGrid &g, hipStream_t s);

@@ -1,4 +1,6 @@
 // Which tiled kernel takes a product, and the joining of a product whose K was split.
+#include <initializer_list>
+
 #include "product.h"
 
 namespace ssd {
@@ -15,67 +17,115 @@ static bool direct(const Operand &o, bool rows_contiguous, int64_t rows, int64_t
     return o.ld <= (int64_t)0x70000000 / e / span;
 }
 
-// Tiles of BM x BN and the steps of each split for a product of `splits` splits
-static ProductGrid cut(const ProductArgs &a, int64_t bm, int64_t bn, int64_t splits) {
-    const int64_t ks = 128 / elem(a), cols = a.kind == kGated ? bn / 2 : bn, steps = (a.K + ks - 1) / ks;
+// A shape of tile: its size, the workgroups that a CU holds, and what they take (us): a step of K of
+// one alone on its CU, of each of several that share it, and the rest of a workgroup.
+struct Shape {
+    int size, each_cu;
+    float alone, step, fixed;
+    int slots() const { return 256 * each_cu; }
+};
+
+constexpr int kMostSplits = 16, kSplitSteps = 4;        // of a tile; steps of a split at least
+
+// Tiles of a shape for this product; those that fill the last round of workgroups only in part are
+// split so that they fill it.
+static ProductGrid cut(const ProductArgs &a, const Shape &sh, int64_t splits) {
+    const int64_t ks = 128 / elem(a), cols = a.kind == kGated ? sh.size / 2 : sh.size, steps = (a.K + ks - 1) / ks;
+    ProductGrid g;
+    g.bm = g.bn = sh.size;
+    g.tiles_m = (int)((a.M + sh.size - 1) / sh.size);
+    g.tiles_n = (int)((a.N + cols - 1) / cols);
+    const int64_t tiles = (int64_t)g.tiles_m * g.tiles_n;
     const int64_t per = (steps + splits - 1) / splits;
-    return {(int)((a.M + bm - 1) / bm), (int)((a.N + cols - 1) / cols), (int)((steps + per - 1) / per), (int)per};
-}
-static int64_t tiles_of(const ProductGrid &g) { return (int64_t)g.tiles_m * g.tiles_n; }
-
-static ProductGrid grid_of(const ProductArgs &a) {
-    const ProductGrid g = cut(a, 128, 128, 1);
-    const int64_t tiles = tiles_of(g);
-    if (tiles >= 192) return g;
-    int64_t splits = 512 / tiles;
-    if (splits > g.steps / 4) splits = g.steps / 4;
-    return cut(a, 128, 128, splits < 1 ? 1 : splits);
+    g.splits = (int)((steps + per - 1) / per);
+    g.steps = (int)per;
+    g.rest = g.splits > 1 ? (int)(tiles % sh.slots()) : 0;
+    g.full = (int)(tiles - g.rest);
+    if (g.rest == 0) g.splits = 1;
+    return g;
 }
 
-static bool big_tiles(const ProductArgs &a, ProductGrid *g) {
-    if (a.dtype != 1) return false;
-    *g = cut(a, 256, 256, 1);
-    const int64_t big = (tiles_of(*g) + 255) / 256, small = (tiles_of(cut(a, 128, 128, 1)) + 511) / 512;
-    return 8 * big <= 5 * small;
+static int64_t part_floats(const ProductGrid &g) { return (int64_t)g.rest * g.splits * g.bm * g.bn; }
+
+static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g) {
+    const int64_t ks = 128 / elem(a), steps = (a.K + ks - 1) / ks;
+    auto time = [&](int64_t n, int64_t steps) {
+        const int64_t rounds = n / sh.slots(), last = (n % sh.slots() + 255) / 256;      // workgroups a CU in the last
+        float t = rounds * (steps * sh.each_cu * sh.step + sh.fixed);
+        if (last) t += steps * (last * sh.step > sh.alone ? last * sh.step : sh.alone) + sh.fixed;
+        return t;
+    };
+    float t = time(g.full, steps);
+    if (g.rest) t += time((int64_t)g.rest * g.splits, g.steps) + 4.f + part_floats(g) * 2e-6f;
+    return t;
+}
+
+// The cheapest way to cut a product, by its sizes and type alone.
+static ProductGrid grid_of(const ProductArgs &a, bool dma) {
+    static const Shape bf16_shapes[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
+    static const Shape f32_shapes[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 4.f}};
+    const Shape *shapes = a.dtype == 1 ? bf16_shapes : f32_shapes;
+    const int n = a.dtype == 1 ? (dma ? 3 : 2) : 2;
+    const int64_t ks = 128 / elem(a), steps = (a.K + ks - 1) / ks;
+    ProductGrid best = cut(a, shapes[n - 1], 1);
+    float least = cost_of(a, shapes[n - 1], best);
+    for (int i = 0; i < n; ++i) {
+        // whole, split until the last round is full, and half as far
+        const ProductGrid whole = cut(a, shapes[i], 1);
+        const int rest = (whole.full + whole.rest) % shapes[i].slots();
+        int64_t most = rest ? shapes[i].slots() / rest : 1;
+        if (most > kMostSplits) most = kMostSplits;
+        if (most > steps / kSplitSteps) most = steps / kSplitSteps;
+        for (int64_t splits : {(int64_t)1, (most + 1) / 2, most}) {
+            if (splits < 1) continue;
+            const ProductGrid g = cut(a, shapes[i], splits);
+            const float t = cost_of(a, shapes[i], g);
+            if (t < least) {
+                least = t;
+                best = g;
+            }
+        }
+    }
+    return best;
 }
 
 bool product_fits(const ProductArgs &a) {
-    return grid_fits(tiles_of(grid_of(a)), 256);
+    const int64_t cols = a.kind == kGated ? 32 : 64;
+    return (a.M + 63) / 64 <= INT32_MAX / 256 / ((a.N + cols - 1) / cols);
 }
 
 size_t product_workspace_bytes(const ProductArgs &a) {
-    const ProductGrid g = grid_of(a);
-    return g.splits > 1 ? (size_t)g.splits * a.M * a.N * (a.kind == kGated ? 2 : 1) * 4 : 0;
+    const int64_t x = part_floats(grid_of(a, true)), y = part_floats(grid_of(a, false));
+    return (size_t)(x > y ? x : y) * 4;
 }
 
-// Adds the splits' sums in their order and finishes the results, V columns a thread.
+// Adds the partial results of shared tiles in their order and finishes them, V columns a thread.
 template <typename T, ProductKind KIND>
-__global__ __launch_bounds__(256) void product_join_kernel(const float *part, int splits, Epilogue ep) {
+__global__ __launch_bounds__(256) void product_join_kernel(const float *part, ProductGrid g, Epilogue ep) {
     constexpr int V = product_vec<T>();
-    const int64_t chunks = (ep.N + V - 1) / V, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= ep.M * chunks) return;
-    const int64_t m = id / chunks, n = id % chunks * V, cols = KIND == kGated ? 2 * ep.N : ep.N;
-    const int left = (int)min(ep.N - n, (int64_t)V);
-    const bool whole = left == V && ep.N % 4 == 0;
+    const int bm = g.bm, bn = g.bn, cols = KIND == kGated ? bn / 2 : bn;
+    const int in = blockIdx.x * 256 + threadIdx.x, row = in / (cols / V), col = in % (cols / V) * V;
+    const int id = g.full + blockIdx.y;
+    const TileAt tile = tile_at(id, g);
+    const int64_t m = (int64_t)tile.m * bm + row, n = (int64_t)tile.n * cols + col;
+    if (row >= bm || m >= ep.M || n >= ep.N) return;
     auto sum = [&](const float *p, float (&v)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = 0.f;
-        for (int s = 0; s < splits; ++s, p += ep.M * cols) {
+        for (int s = 0; s < g.splits; ++s, p += bm * bn)
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
-                float q[4];
-                load_some<float, 4>(p + i, left - i, whole, q);
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(p + i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[i + j] += q[j];
             }
-        }
     };
-    const float *p = part + m * cols + n;
+    const float *p = part + (int64_t)blockIdx.y * g.splits * bm * bn + row * bn + col;
     float v[V];
     sum(p, v);
     if constexpr (KIND == kGated) {
         float u[V];
-        sum(p + ep.N, u);
+        sum(p + bn / 2, u);
         finish_gated<T, V>(ep, m, n, v, u);
     } else {
         finish_linear<T, V>(ep, m, n, v);
@@ -83,11 +133,12 @@ __global__ __launch_bounds__(256) void product_join_kernel(const float *part, in
 }
 
 template <typename T>
-static hipError_t join(const ProductArgs &a, int splits, hipStream_t s) {
+static hipError_t join(const ProductArgs &a, const ProductGrid &g, hipStream_t s) {
     constexpr int V = product_vec<T>();
-    const uint32_t blocks = (uint32_t)((a.M * ((a.N + V - 1) / V) + 255) / 256);
-    if (a.kind == kGated) product_join_kernel<T, kGated><<<blocks, 256, 0, s>>>(a.part, splits, epilogue_of(a));
-    else product_join_kernel<T, kLinear><<<blocks, 256, 0, s>>>(a.part, splits, epilogue_of(a));
+    const int chunks = g.bm * (a.kind == kGated ? g.bn / 2 : g.bn) / V;
+    const dim3 grid((uint32_t)((chunks + 255) / 256), (uint32_t)g.rest);
+    if (a.kind == kGated) product_join_kernel<T, kGated><<<grid, 256, 0, s>>>(a.part, g, epilogue_of(a));
+    else product_join_kernel<T, kLinear><<<grid, 256, 0, s>>>(a.part, g, epilogue_of(a));
     return hipGetLastError();
 }
 
@@ -101,14 +152,12 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     const int64_t brows = a.kind == kGated ? 2 * a.N : a.N, bspan = a.kind == kGated ? a.N + 256 : 256;
     const bool dma = direct(a.a, a.a_rows, a.M, a.K, a.a_rows ? ks : 256, e) &&
                      direct(a.b, a.b_rows, brows, a.K, a.b_rows ? ks : bspan, e);
-    ProductGrid g;
-    if (dma && big_tiles(a, &g)) return launch_tiles_bf16_big(a, g, s);
-    g = grid_of(a);
+    const ProductGrid g = grid_of(a, dma);
     hipError_t r;
     if (a.dtype == 1) r = dma ? launch_tiles_bf16(a, g, s) : launch_tiles_bf16_any(a, g, s);
     else r = dma ? launch_tiles_f32(a, g, s) : launch_tiles_f32_any(a, g, s);
-    if (r != hipSuccess || g.splits == 1) return r;
-    return a.dtype == 1 ? join<bf16>(a, g.splits, s) : join<float>(a, g.splits, s);
+    if (r != hipSuccess || g.rest == 0) return r;
+    return a.dtype == 1 ? join<bf16>(a, g, s) : join<float>(a, g, s);
 }
 
 }  // namespace ssd

@@ -60,9 +60,11 @@ struct TileLayout {
     static constexpr int PITCH = PIECES * 16;
     // what the places of a line's pieces are XORed with
     __host__ __device__ static constexpr int key(int line) {
-        if (!ROWS) return INTER ? (line & 3) | ((((line >> 3) ^ (line >> 4)) & 1) << 2) : line & 7;
-        if (E == 2) return INTER ? (line & 1) | (((line >> 1) & 1) << 3) : (line & 3) << 1;
-        return INTER ? (line >> 2) & 3 : ((line >> 2) & 3) << 2;
+        if (!ROWS) return INTER ? (line & 3) | ((line / (4 * NT)) & 1) << 2 : line & 7;
+        if (E == 2 && PIECES == 8) return (line >> 1 & 1) << (INTER ? 2 : 1);          // lines of 128 bytes
+        if (E == 2) return INTER ? (line & 1) | (line >> 1 & 1) << 3 : (line & 3) << 1;
+        if (!INTER) return (line >> 2 & 3) << 2;
+        return NT == 4 ? line >> 2 & 3 : (line >> 2 & 1) | (line >> 3 & 1) << 3;
     }
     __host__ __device__ static constexpr int row_of(int j, int i) {
         return INTER ? 4 * NT * (i >> 2) + 4 * j + (i & 3) : 16 * j + i;
@@ -123,6 +125,7 @@ struct ProductCfg {
     static constexpr int KS = kStepBytes / (int)sizeof(T);
     static constexpr int QA = LA::BYTES / 1024 / NW, QB = LB::BYTES / 1024 / NW;   // copies per wave and step
     static_assert(QA * 1024 * NW == LA::BYTES && QB * 1024 * NW == LB::BYTES, "whole waves of 16-byte pieces");
+    static constexpr int WAVES = BM >= 128 ? 2 : 4;               // of a SIMD at least: registers for its tiles
     static_assert(KIND != kGated || (TN % 2 == 0 && !B_ROWS), "gate and up rows side by side");
 };
 
@@ -135,23 +138,44 @@ __device__ __forceinline__ int64_t b_row(const ProductArgs &p, int64_t n0, int r
     return min(n0 + r, p.N - 1);
 }
 
-// Tile of a workgroup.  Consecutive workgroups go to the 8 XCDs in turn; each XCD (own L2) takes
-// a contiguous range of the order below: columns of tiles in groups of 4, and within a group
-// row by row, so that the 32 tiles an XCD holds at a time share their operands.
-struct TileAt {
+// What a workgroup does: its tile, its steps of K from `first` on, and, where its tile is shared,
+// which of the partial results it leaves (-1: none).
+struct Work {
     int m, n;
+    int64_t first;
+    int steps, part;
 };
-__device__ __forceinline__ TileAt tile_at(int bid, const ProductGrid &g) {
-    const int n = g.tiles_m * g.tiles_n, per = n / 8, more = n % 8, x = bid % 8;
-    const int id = x * per + min(x, more) + bid / 8;
-    constexpr int G = 4;
-    const int group = id / (G * g.tiles_m), first = group * G, width = min(G, g.tiles_n - first);
-    const int in = id - group * G * g.tiles_m;
-    return {in / width, first + in % width};
+
+// Consecutive workgroups go to the 8 XCDs in turn: the i-th of n workgroups in an order in which
+// each XCD takes a contiguous range.
+__device__ __forceinline__ int xcd_order(int i, int n) {
+    const int per = n / 8, more = n % 8, x = i % 8;
+    return x * per + min(x, more) + i / 8;
+}
+
+__device__ __forceinline__ Work work_of(const ProductGrid &g, int64_t steps) {
+    Work w;
+    int id = blockIdx.x;
+    if (id < g.full) {
+        id = xcd_order(id, g.full);
+        w.first = 0;
+        w.steps = (int)steps;
+        w.part = -1;
+    } else {
+        const int i = xcd_order(id - g.full, g.rest * g.splits), split = i / g.rest, tile = i % g.rest;
+        id = g.full + tile;
+        w.first = (int64_t)split * g.steps;
+        w.steps = (int)min((int64_t)g.steps, steps - w.first);
+        w.part = tile * g.splits + split;
+    }
+    const TileAt at = tile_at(id, g);
+    w.m = at.m;
+    w.n = at.n;
+    return w;
 }
 
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, Epilogue ep, ProductGrid grid) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductArgs p, Epilogue ep, ProductGrid grid) {
     typedef typename C::T T;
     typedef typename Frag<T>::type F;
     typedef typename C::LA LA;
@@ -161,30 +185,36 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
 
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
-    const TileAt tile = tile_at(blockIdx.x, grid);
-    const int64_t m0 = (int64_t)tile.m * C::BM, n0 = (int64_t)tile.n * C::BCOLS;
-    const int64_t first = (int64_t)blockIdx.y * grid.steps;       // this split's steps
     const int64_t all = (p.K + C::KS - 1) / C::KS;
-    const int steps = (int)min((int64_t)grid.steps, all - first);
-    const int64_t k_first = first * C::KS;
+    const Work work = work_of(grid, all);
+    const int64_t m0 = (int64_t)work.m * C::BM, n0 = (int64_t)work.n * C::BCOLS;
+    const int steps = work.steps;
+    const int64_t k_first = work.first * C::KS;
+    const int tail = work.first + steps == all && p.K % C::KS ? steps - 1 : -1;      // the step that K ends in
 
     // ---- copies
-    // DMA: 32-bit offsets from a scalar base that moves with k
+    const int64_t a_size = p.M, b_size = C::KIND == kGated ? 2 * p.N : p.N;
+    // 32-bit offsets of this lane's pieces from a scalar base that moves with k.  Copies by way of
+    // registers read whole pieces where the operand's rows are contiguous too: one that reaches
+    // past the rows reads the next line's first values, and one behind them the tile's first,
+    // which meet no result that is stored.
     uint32_t offa[C::QA], offb[C::QB];
-    if constexpr (C::DMA) {
+    auto offsets = [&](auto layout, const Operand &o, int64_t at, int64_t size, bool is_b, int Q, uint32_t *off) SSD_INLINE {
+        typedef decltype(layout) L;
 #pragma unroll
-        for (int q = 0; q < C::QA; ++q) {
-            const int slot = (w * C::QA + q) * 64 + lane, line = LA::slot_line(slot), piece = LA::slot_piece(slot);
-            const int64_t r = LA::ROWS ? line : min(m0 + line, p.M - 1) - m0;
-            offa[q] = (uint32_t)(r * p.a.ld * E) + piece * 16;
+        for (int q = 0; q < Q; ++q) {
+            const int slot = (w * Q + q) * 64 + lane, line = L::slot_line(slot), piece = L::slot_piece(slot);
+            if (L::ROWS) {
+                const int64_t n = C::DMA || at + piece * V < size ? at + piece * V : max(min(at, size - V), (int64_t)0);
+                off[q] = (uint32_t)((line * o.ld + n - (C::DMA ? at : max(min(at, size - V), (int64_t)0))) * E);
+            } else {
+                const int64_t r = is_b ? b_row<C>(p, at, line) : min(at + line, size - 1);
+                off[q] = (uint32_t)((r - at) * o.ld * E) + piece * 16;
+            }
         }
-#pragma unroll
-        for (int q = 0; q < C::QB; ++q) {
-            const int slot = (w * C::QB + q) * 64 + lane, line = LB::slot_line(slot), piece = LB::slot_piece(slot);
-            const int64_t r = LB::ROWS ? line : b_row<C>(p, n0, line) - n0;
-            offb[q] = (uint32_t)(r * p.b.ld * E) + piece * 16;
-        }
-    }
+    };
+    offsets(LA{}, p.a, m0, a_size, false, C::QA, offa);
+    offsets(LB{}, p.b, n0, b_size, true, C::QB, offb);
     u32x4 ra[C::DMA ? 1 : C::QA], rb[C::DMA ? 1 : C::QB];
     // An operand's source: where the next step to copy begins, the bytes from one step to the next,
     // and those that a copy may read from there on, of the split's last step and of others, which
@@ -217,7 +247,6 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
     };
     // Zeros for what a copy of the step that K ends in took from behind K, where the operand's k is
     // contiguous: the rest of its rows, or the next rows.
-    const int tail = first + steps == all && p.K % C::KS ? steps - 1 : -1;
     auto clear_tail = [&](auto layout, unsigned char *m) SSD_INLINE {
         typedef decltype(layout) L;
         if constexpr (!L::ROWS) {
@@ -226,36 +255,50 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
                 if (L::slot_piece(slot) >= have) *reinterpret_cast<u32x4 *>(m + slot * 16) = u32x4{0, 0, 0, 0};
         }
     };
-    auto fetch = [&](auto layout, const Operand &o, int64_t at, int64_t size, bool is_b, int64_t k, int Q, u32x4 *reg) SSD_INLINE {
+    // By way of registers.  Steps of which every piece lies in the operand (to the end of its next
+    // line, where its rows are contiguous) are fetched whole from any address; the others value by
+    // value.
+    auto quick = [&](auto layout, const Operand &o, int64_t size) SSD_INLINE {
         typedef decltype(layout) L;
+        if (L::ROWS) return size >= V && o.ld >= V && o.ld <= (int64_t)0x70000000 / E / L::KS;
+        return o.ld <= (int64_t)0x70000000 / E / (C::KIND == kGated ? p.N + L::SIZE : L::SIZE);
+    };
+    const bool quick_a = !C::DMA && quick(LA{}, p.a, a_size), quick_b = !C::DMA && quick(LB{}, p.b, b_size);
+    auto fetch = [&](auto layout, const Operand &o, int64_t at, int64_t size, bool is_b, bool quickly, int t, int Q,
+                     const uint32_t *off, u32x4 *reg) SSD_INLINE {
+        typedef decltype(layout) L;
+        const int64_t k = k_first + (int64_t)t * C::KS;
+        const T *const src = reinterpret_cast<const T *>(o.p);
+        if (quickly && (L::ROWS ? work.first + t + 1 < all : t != tail)) {
+            const unsigned char *base = reinterpret_cast<const unsigned char *>(
+                L::ROWS ? src + k * o.ld + min(at, size - V) : src + at * o.ld + k);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) __builtin_memcpy(&reg[q], base + off[q], 16);
+            return;
+        }
+#pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int slot = (w * Q + q) * 64 + lane, line = L::slot_line(slot), piece = L::slot_piece(slot);
-            const T *src;
+            const T *from;
             int64_t have;
             if (L::ROWS) {
                 have = k + line < p.K ? size - (at + piece * V) : 0;
-                src = reinterpret_cast<const T *>(o.p) + (k + line) * o.ld + at + piece * V;
+                from = src + (k + line) * o.ld + at + piece * V;
             } else {
                 const int64_t r = is_b ? b_row<C>(p, at, line) : min(at + line, size - 1);
                 have = p.K - (k + piece * V);
-                src = reinterpret_cast<const T *>(o.p) + r * o.ld + k + piece * V;
+                from = src + r * o.ld + k + piece * V;
             }
-            u32x4 v = {0, 0, 0, 0};
-            if (have >= V) {
-                __builtin_memcpy(&v, src, 16);
-            } else if (have > 0) {
-                T t[V];
+            T v[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) t[i] = i < have ? src[i] : from_f32<T>(0.f);
-                __builtin_memcpy(&v, t, 16);
-            }
-            reg[q] = v;
+            for (int i = 0; i < V; ++i) v[i] = i < have ? from[i] : from_f32<T>(0.f);
+            __builtin_memcpy(&reg[q], v, 16);
         }
     };
     auto place = [&](int Q, const u32x4 *reg, unsigned char *to) SSD_INLINE {
+#pragma unroll
         for (int q = 0; q < Q; ++q) *reinterpret_cast<u32x4 *>(to + ((w * Q + q) * 64 + lane) * 16) = reg[q];
     };
-    const int64_t a_size = p.M, b_size = C::KIND == kGated ? 2 * p.N : p.N;
     Source src_a = source(LA{}, p.a, m0, a_size), src_b = source(LB{}, p.b, n0, b_size);
     auto copies_a = [&](int t, int from, int end, unsigned char *to) SSD_INLINE {
         copies(LA{}, src_a, t, from, end, C::QA, offa, to);
@@ -263,16 +306,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
     auto copies_b = [&](int t, int from, int end, unsigned char *to) SSD_INLINE {
         copies(LB{}, src_b, t, from, end, C::QB, offb, to);
     };
+    auto fetch_both = [&](int t) SSD_INLINE {
+        fetch(LA{}, p.a, m0, a_size, false, quick_a, t, C::QA, offa, ra);
+        fetch(LB{}, p.b, n0, b_size, true, quick_b, t, C::QB, offb, rb);
+    };
     // By way of registers: what was fetched (step t) goes to (a, b), and the step after it is
     // fetched.
     auto store_fetch = [&](int t, unsigned char *a, unsigned char *b) SSD_INLINE {
         place(C::QA, ra, a);
         place(C::QB, rb, b);
-        if (t + 1 < steps) {
-            const int64_t k = k_first + (int64_t)(t + 1) * C::KS;
-            fetch(LA{}, p.a, m0, a_size, false, k, C::QA, ra);
-            fetch(LB{}, p.b, n0, b_size, true, k, C::QB, rb);
-        }
+        if (t + 1 < steps) fetch_both(t + 1);
     };
 
     // ---- products
@@ -297,7 +340,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
     // The compiler's own order reads late and waits; a row's fragment is read no earlier than its
     // place in the registers comes free, which keeps 256 registers enough for 8 x 4 tiles.
     auto products = [&](int s, const unsigned char *ma, const unsigned char *mb, auto between) SSD_INLINE {
-        constexpr int R = C::TM + C::TN, GROUPS = C::TM - 1;
+        constexpr int R = C::TM + C::TN, GROUPS = C::TM > 2 ? C::TM - 1 : C::TM;
         each_of<C::TM>([&](auto at) SSD_INLINE {
             constexpr int i = decltype(at)::value;
             between(at);
@@ -335,7 +378,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
         if constexpr (C::DMA) {
             if (t + 1 == tail) clear(a1, b1);
             products(1, a1, b1, [&](auto at) SSD_INLINE {
-                constexpr int i = decltype(at)::value, PARTS = C::TM / 4;
+                constexpr int i = decltype(at)::value, PARTS = C::TM > 4 ? C::TM / 4 : 1;
                 if constexpr (i < PARTS) copies_a(t + 2, i * C::QA / PARTS, (i + 1) * C::QA / PARTS, a0);
                 else if constexpr (i < 2 * PARTS)
                     copies_b(t + 2, (i - PARTS) * C::QB / PARTS, (i - PARTS + 1) * C::QB / PARTS, b0);
@@ -353,8 +396,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
         copies_b(1, 0, C::QB, B1);
         if (tail == 0) clear(A0, B0);
     } else {
-        fetch(LA{}, p.a, m0, a_size, false, k_first, C::QA, ra);
-        fetch(LB{}, p.b, n0, b_size, true, k_first, C::QB, rb);
+        fetch_both(0);
         store_fetch(0, A0, B0);
         if (steps > 1) store_fetch(1, A1, B1);
         landed();
@@ -369,36 +411,36 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
     if constexpr (C::DMA) __builtin_amdgcn_s_waitcnt(0x0f70);      // no copy is left behind
 
     // ---- results: this lane's columns are n .. n + 4 NT - 1 of each half
-    const int i16 = lane & 15, g = lane >> 4;
-    const int64_t n = n0 + wn * 16 * C::NT + 4 * C::NT * g;
+    const int i16 = lane & 15, g = lane >> 4, col = wn * 16 * C::NT + 4 * C::NT * g;
+    if (work.part >= 0) {
+        float *part = p.part + (int64_t)work.part * C::BM * C::BN;
+#pragma unroll
+        for (int i = 0; i < C::TM; ++i) {
+            float *row = part + (wm * 16 * C::TM + 16 * i + i16) * C::BN + col;
+#pragma unroll
+            for (int j = 0; j < C::TN; ++j)
+                *reinterpret_cast<f32x4 *>(row + (j / C::NT) * (C::BN / 2) + 4 * (j % C::NT)) = acc[i][j];
+        }
+        return;
+    }
+    constexpr int W = V < 4 * C::NT ? V : 4 * C::NT;
+    const int64_t n = n0 + col;
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
         const int64_t m = m0 + wm * 16 * C::TM + 16 * i + i16;
         if (m >= p.M) continue;
-        if (grid.splits > 1) {
-            const int64_t cols = b_size;
-            float *part = p.part + ((int64_t)blockIdx.y * p.M + m) * cols;
 #pragma unroll
-            for (int j = 0; j < C::TN; ++j) {
-                const int64_t c = n + 4 * (j % C::NT);
-                const int left = (int)min(p.N - c, (int64_t)4);
-                float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                if (left > 0) store_some<float, 4>(part + c + (j / C::NT) * p.N, left, left == 4 && p.N % 4 == 0, v);
-            }
-            continue;
-        }
+        for (int c = 0; c < 4 * C::NT; c += W) {
+            float v[W];
 #pragma unroll
-        for (int c = 0; c < 4 * C::NT; c += V) {
-            float v[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = acc[i][(c + e) / 4][e % 4];
+            for (int e = 0; e < W; ++e) v[e] = acc[i][(c + e) / 4][e % 4];
             if constexpr (C::KIND == kGated) {
-                float u[V];
+                float u[W];
 #pragma unroll
-                for (int e = 0; e < V; ++e) u[e] = acc[i][C::NT + (c + e) / 4][e % 4];
-                finish_gated<T, V>(ep, m, n + c, v, u);
+                for (int e = 0; e < W; ++e) u[e] = acc[i][C::NT + (c + e) / 4][e % 4];
+                finish_gated<T, W>(ep, m, n + c, v, u);
             } else {
-                finish_linear<T, V>(ep, m, n + c, v);
+                finish_linear<T, W>(ep, m, n + c, v);
             }
         }
     }
@@ -406,8 +448,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void product_kernel(ProductArgs p, E
 
 template <class C>
 hipError_t launch_tiles(const ProductArgs &a, const ProductGrid &g, hipStream_t s) {
-    product_kernel<C><<<dim3((uint32_t)(g.tiles_m * g.tiles_n), (uint32_t)g.splits), C::THREADS, 0, s>>>(
-        a, epilogue_of(a), g);
+    product_kernel<C><<<(uint32_t)(g.full + g.rest * g.splits), C::THREADS, 0, s>>>(a, epilogue_of(a), g);
     return hipGetLastError();
 }
 
