@@ -70,6 +70,10 @@ hipError_t launch_tiles_bf16_any(const ProductArgs &a, const ProductGrid &g, hip
 hipError_t launch_tiles_f32(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_f32_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 
+// Few rows: product_rows.hip, without a workspace
+bool product_few_rows(const ProductArgs &a);
+hipError_t launch_product_rows(const ProductArgs &a, hipStream_t s);
+
 // The elementwise part of a backward and the sums over its rows
 struct ProductActArgs {
     int64_t M, N;

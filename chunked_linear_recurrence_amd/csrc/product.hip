@@ -95,6 +95,7 @@ bool product_fits(const ProductArgs &a) {
 }
 
 size_t product_workspace_bytes(const ProductArgs &a) {
+    if (product_few_rows(a)) return 0;
     const int64_t x = part_floats(grid_of(a, true)), y = part_floats(grid_of(a, false));
     return (size_t)(x > y ? x : y) * 4;
 }
@@ -143,6 +144,7 @@ static hipError_t join(const ProductArgs &a, const ProductGrid &g, hipStream_t s
 }
 
 hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
+    if (product_few_rows(a0)) return launch_product_rows(a0, s);
     ProductArgs a = a0;
     if (a.K == 1) {
         if (a.a_rows) a.a.ld = a.M;

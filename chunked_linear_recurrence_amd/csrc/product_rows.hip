@@ -1,0 +1,152 @@
+// The products of product.h for few rows (single tokens of a batch): a stream of the weight's rows,
+// each read once, with nothing staged in LDS.
+//
+// A workgroup takes 16 rows of the weight (gated: 16 of g and the 16 of u beside them), or 32, and
+// its waves a contiguous share of k each, so that even a weight of a few megabytes is on its way
+// in a thousand waves at once.  A lane's 16 bytes are its fragment of the matrix units as they
+// come from memory (row lane % 16, 8 or 4 values of k); x's fragments, 16 rows of x each, come
+// from the caches the same way.  The waves' sums are added in wave order through LDS.
+#include "product_tile.h"
+
+namespace ssd {
+
+template <typename T, ProductKind KIND, int MT, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p, Epilogue ep) {
+    typedef typename Frag<T>::type F;
+    constexpr int V = 16 / (int)sizeof(T), KS = kStepBytes / (int)sizeof(T), TILES = KIND == kGated ? 2 * NT : NT;
+    constexpr int U = MT * TILES > 4 ? 1 : MT > 1 ? 2 : 4;       // steps whose loads are started together
+    __shared__ f32x4 sums[WAVES][MT][TILES][64];
+    const int lane = threadIdx.x % 64, i16 = lane % 16, g = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t n0 = (int64_t)blockIdx.x * 16 * NT;
+    const int64_t steps = (p.K + KS - 1) / KS, whole = p.K / KS;
+    const int64_t first = steps * wave / WAVES, end = steps * (wave + 1) / WAVES;
+    const T *x[MT], *b[TILES];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        x[i] = reinterpret_cast<const T *>(p.a.p) + min((int64_t)(16 * i + i16), p.M - 1) * p.a.ld + g * V;
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+        const int64_t row = min(n0 + 16 * (j % NT) + i16, p.N - 1) + (j / NT) * p.N;
+        b[j] = reinterpret_cast<const T *>(p.b.p) + row * p.b.ld + g * V;
+    }
+    f32x4 acc[MT][TILES];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto load = [](const T *q) SSD_INLINE {
+        F f;
+        __builtin_memcpy(&f, q, 16);
+        return f;
+    };
+    auto take = [&](int64_t s, auto count) SSD_INLINE {
+        constexpr int N = decltype(count)::value;
+        F fb[N][2][TILES], fx[N][2][MT];
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = (s + q) * KS + h * (KS / 2);
+#pragma unroll
+                for (int j = 0; j < TILES; ++j) fb[q][h][j] = load(b[j] + k);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) fx[q][h][i] = load(x[i] + k);
+            }
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < TILES; ++j) acc[i][j] = multiply(fb[q][h][j], fx[q][h][i], acc[i][j]);
+    };
+    int64_t s = first;
+    const int64_t full = min(end, whole);
+    for (; s + U <= full; s += U) take(s, std::integral_constant<int, U>{});
+    for (; s < full; ++s) take(s, std::integral_constant<int, 1>{});
+    if (s < end) {                                               // the step that K ends in
+        auto some = [&](const T *q, int64_t k) SSD_INLINE {
+            const int64_t have = p.K - k - g * V;
+            T v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = e < have ? q[k + e] : from_f32<T>(0.f);
+            F f;
+            __builtin_memcpy(&f, v, 16);
+            return f;
+        };
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = s * KS + h * (KS / 2);
+            F fb[TILES];
+#pragma unroll
+            for (int j = 0; j < TILES; ++j) fb[j] = some(b[j], k);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const F fx = some(x[i], k);
+#pragma unroll
+                for (int j = 0; j < TILES; ++j) acc[i][j] = multiply(fb[j], fx, acc[i][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) sums[wave][i][j][lane] = acc[i][j];
+    __syncthreads();
+    // results of (16 rows of x, 16 columns) by one wave each: lane (i16, g) has row i16, columns 4 g ..
+    for (int t = wave; t < MT * NT; t += WAVES) {
+        const int i = t / NT, j = t % NT;
+        auto total = [&](int tile, float (&v)[4]) SSD_INLINE {
+            f32x4 r = sums[0][i][tile][lane];
+            for (int w = 1; w < WAVES; ++w) r += sums[w][i][tile][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = r[e];
+        };
+        const int64_t m = 16 * i + i16, n = n0 + 16 * j + 4 * g;
+        if (m >= p.M) continue;
+        float v[4];
+        total(j, v);
+        if constexpr (KIND == kGated) {
+            float u[4];
+            total(NT + j, u);
+            finish_gated<T, 4>(ep, m, n, v, u);
+        } else {
+            finish_linear<T, 4>(ep, m, n, v);
+        }
+    }
+}
+
+// Up to 32 rows, and up to 64 of a small weight: there the tiles' second launch costs more than x's
+// fragments, which every workgroup reads for itself.  32 rows of 4096 x 4096 in bfloat16: 12.9 us
+// here, 13.8 in tiles; 64 rows 21.6 and 13.9; 64 rows of 1536 x 768 8.9 and 11.3.
+bool product_few_rows(const ProductArgs &a) {
+    if (a.a_rows || a.b_rows) return false;
+    return a.M <= 32 || (a.M <= 64 && a.N * a.K <= (INT64_C(1) << 22));
+}
+
+// 16 rows of the weight a workgroup and up to 16 waves for them while that leaves CUs idle, else 32
+// rows and 4 waves, which halves the reads of x: 32 rows of 2048 x (2 x 5632) 16.8 us with 16 and
+// 13.5 with 32, one row 10.6 and 10.4.
+template <typename T, ProductKind KIND, int MT>
+static hipError_t rows_launch(const ProductArgs &a, hipStream_t s) {
+    const Epilogue ep = epilogue_of(a);
+    if (a.N <= 4096) product_rows_kernel<T, KIND, MT, 1, 16 / MT><<<(uint32_t)((a.N + 15) / 16), 64 * (16 / MT), 0, s>>>(a, ep);
+    else product_rows_kernel<T, KIND, MT, 2, 4><<<(uint32_t)((a.N + 31) / 32), 256, 0, s>>>(a, ep);
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t rows_by_m(const ProductArgs &a, hipStream_t s) {
+    const bool gated = a.kind == kGated;
+    if (a.M <= 16) return gated ? rows_launch<T, kGated, 1>(a, s) : rows_launch<T, kLinear, 1>(a, s);
+    if (a.M <= 32) return gated ? rows_launch<T, kGated, 2>(a, s) : rows_launch<T, kLinear, 2>(a, s);
+    return gated ? rows_launch<T, kGated, 4>(a, s) : rows_launch<T, kLinear, 4>(a, s);
+}
+
+hipError_t launch_product_rows(const ProductArgs &a, hipStream_t s) {
+    return a.dtype == 1 ? rows_by_m<bf16>(a, s) : rows_by_m<float>(a, s);
+}
+
+}  // namespace ssd
