@@ -75,8 +75,8 @@ ssd::ProductArgs grad_x_args(const ssd_product_dims_t &d, int64_t cols, const vo
     a.dtype = d.dtype;
     a.kind = ssd::kPlain;
     a.b_rows = true;
-    a.a = {dpre, ld};
-    a.b = {weight, d.inner};
+    a.a = {dpre, ld, 0};
+    a.b = {weight, d.inner, 0};
     return a;
 }
 ssd::ProductArgs grad_w_args(const ssd_product_dims_t &d, int64_t cols, const void *dpre, int64_t ld, const void *x) {
@@ -88,13 +88,13 @@ ssd::ProductArgs grad_w_args(const ssd_product_dims_t &d, int64_t cols, const vo
     a.dtype = d.dtype;
     a.kind = ssd::kPlain;
     a.a_rows = a.b_rows = true;
-    a.a = {dpre, ld};
-    a.b = {x, d.x_row_stride};
+    a.a = {dpre, ld, 0};
+    a.b = {x, d.x_row_stride, 0};
     return a;
 }
 
-// A backward's workspace: dpre where it is formed, the bias' partial sums, and the partial
-// results of the two products, which run one after the other.
+// A backward's workspace: dpre where it is formed, the bias' partial sums, and what the two
+// products need, which run one after the other.
 struct GradLayout {
     size_t dpre, sums, part, total;
 };
@@ -107,8 +107,9 @@ GradLayout grad_layout(const ssd_product_dims_t &d, bool gated, bool forms) {
     lo.sums = off;
     off += align_up((size_t)(ssd::product_act_rows(d.rows, d.outer, d.dtype) * cols * 4));
     lo.part = off;
-    off += align_up(std::max(ssd::product_workspace_bytes(grad_x_args(d, cols, nullptr, 0, nullptr)),
-                             ssd::product_workspace_bytes(grad_w_args(d, cols, nullptr, 0, nullptr))));
+    const int64_t ld = forms ? cols : d.dy_row_stride;
+    off += align_up(std::max(ssd::product_workspace_bytes(grad_x_args(d, cols, nullptr, ld, nullptr)),
+                             ssd::product_workspace_bytes(grad_w_args(d, cols, nullptr, ld, nullptr))));
     lo.total = off;
     return lo;
 }

@@ -13,6 +13,8 @@
 
 namespace ssd {
 
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
 enum Act { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 
 // An operand [rows, K] of a product: element (r, k) at p + r * ld + k, or, where the rows are
@@ -20,6 +22,7 @@ enum Act { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 struct Operand {
     const void *p;
     int64_t ld;
+    int64_t size;                 // values that may be read of a line, where the rows are contiguous
 };
 
 enum ProductKind { kLinear, kGated, kPlain };
@@ -145,20 +148,26 @@ __device__ __forceinline__ float act_d_f32(float v, int act, float *d) {
 // ---------------------------------------------------------------------------------
 template <typename T> constexpr int product_vec() { return 16 / (int)sizeof(T); }
 
-// Loads of V values at p that may not lie on 16 bytes or reach past the row's end
+// V values at p, or the first n of them (the rest 0), wherever p lies: global memory takes 16 bytes at
+// any element's address
 template <typename T, int V>
-__device__ __forceinline__ void load_some(const T *p, int n, bool whole, float (&v)[V]) {
-    if (whole) {
-        unpack<T, V>(load_pack<T, V>(p), v);
+__device__ __forceinline__ void load_some(const T *p, int n, float (&v)[V]) {
+    if (n >= V) {
+        typename Pack<T, V>::type q;
+        __builtin_memcpy(&q, p, sizeof(q));
+        unpack<T, V>(q, v);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
     }
 }
 template <typename T, int V>
-__device__ __forceinline__ void store_some(T *p, int n, bool whole, const float (&v)[V]) {
-    if (whole) {
-        store_f32<T, V>(p, v);
+__device__ __forceinline__ void store_some(T *p, int n, const float (&v)[V]) {
+    if (n >= V) {
+        typename Pack<T, V>::type q;
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = from_f32<T>(v[i]);
+        __builtin_memcpy(p, &q, sizeof(q));
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -166,50 +175,38 @@ __device__ __forceinline__ void store_some(T *p, int n, bool whole, const float 
     }
 }
 
-// The epilogue's flags that are the same for all of a launch: rows and pointers on 16 bytes.
-inline bool rows_at16(const void *p, int64_t ld, int64_t e) { return ((uintptr_t)p & 15u) == 0 && ld * e % 16 == 0; }
-
 struct Epilogue {
     int64_t M, N;
     const void *bias, *residual;
     int64_t residual_ld;
     int act;
     void *y, *pre;
-    bool vec;                     // every row of the tensors above starts on 16 bytes
 };
 
-inline Epilogue epilogue_of(const ProductArgs &a) {
-    const int64_t e = a.dtype == 1 ? 2 : 4;
-    Epilogue r = {a.M, a.N, a.bias, a.residual, a.residual_ld, a.act, a.y, a.pre, false};
-    r.vec = rows_at16(a.y, a.N, e) && (!a.bias || rows_at16(a.bias, a.N, e)) &&
-            (!a.residual || rows_at16(a.residual, a.M > 1 ? a.residual_ld : 0, e)) &&
-            (!a.pre || rows_at16(a.pre, a.N, e));
-    return r;
-}
+inline Epilogue epilogue_of(const ProductArgs &a) { return {a.M, a.N, a.bias, a.residual, a.residual_ld, a.act, a.y, a.pre}; }
 
 // v: the product's values at row m, columns n .. n + V - 1
 template <typename T, int V>
 __device__ __forceinline__ void finish_linear(const Epilogue &p, int64_t m, int64_t n, float (&v)[V]) {
     const int left = (int)min(p.N - n, (int64_t)V);
     if (left <= 0) return;
-    const bool whole = p.vec && left == V;
     float b[V];
     if (p.bias) {
-        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + n, left, whole, b);
+        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + n, left, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += b[i];
     }
-    if (p.pre) store_some<T, V>(reinterpret_cast<T *>(p.pre) + m * p.N + n, left, whole, v);
+    if (p.pre) store_some<T, V>(reinterpret_cast<T *>(p.pre) + m * p.N + n, left, v);
     if (p.act != kActNone) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = act_f32(v[i], p.act);
     }
     if (p.residual) {
-        load_some<T, V>(reinterpret_cast<const T *>(p.residual) + m * p.residual_ld + n, left, whole, b);
+        load_some<T, V>(reinterpret_cast<const T *>(p.residual) + m * p.residual_ld + n, left, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += b[i];
     }
-    store_some<T, V>(reinterpret_cast<T *>(p.y) + m * p.N + n, left, whole, v);
+    store_some<T, V>(reinterpret_cast<T *>(p.y) + m * p.N + n, left, v);
 }
 
 // g and u: both products' values at row m, columns n .. n + V - 1 of each half
@@ -217,24 +214,23 @@ template <typename T, int V>
 __device__ __forceinline__ void finish_gated(const Epilogue &p, int64_t m, int64_t n, float (&g)[V], float (&u)[V]) {
     const int left = (int)min(p.N - n, (int64_t)V);
     if (left <= 0) return;
-    const bool whole = p.vec && left == V;
     float b[V];
     if (p.bias) {
-        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + n, left, whole, b);
+        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + n, left, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) g[i] += b[i];
-        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + p.N + n, left, whole, b);
+        load_some<T, V>(reinterpret_cast<const T *>(p.bias) + p.N + n, left, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) u[i] += b[i];
     }
     if (p.pre) {
         T *pre = reinterpret_cast<T *>(p.pre) + 2 * m * p.N + n;
-        store_some<T, V>(pre, left, whole, g);
-        store_some<T, V>(pre + p.N, left, whole, u);
+        store_some<T, V>(pre, left, g);
+        store_some<T, V>(pre + p.N, left, u);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] = act_f32(g[i], p.act) * u[i];
-    store_some<T, V>(reinterpret_cast<T *>(p.y) + m * p.N + n, left, whole, g);
+    store_some<T, V>(reinterpret_cast<T *>(p.y) + m * p.N + n, left, g);
 }
 
 }  // namespace ssd

@@ -7,15 +7,32 @@ namespace ssd {
 
 static int64_t elem(const ProductArgs &a) { return a.dtype == 1 ? 2 : 4; }
 
-// Whether an operand's 16-byte pieces all lie on 16 bytes and inside a row, with the tile's
-// offsets below 2^31: `span` rows of a tile where k is contiguous, of k otherwise.
-static bool direct(const Operand &o, bool rows_contiguous, int64_t rows, int64_t k, int64_t span, int64_t e) {
-    const int64_t along = rows_contiguous ? rows : k, across = rows_contiguous ? k : rows;
-    if ((uintptr_t)o.p & 15u || along * e % 16 != 0) return false;
-    if (across > 1 && o.ld * e % 16 != 0) return false;
-    if (rows_contiguous && o.ld < rows) return false;     // lines past K have to lie past the last one
-    return o.ld <= (int64_t)0x70000000 / e / span;
+// An operand as lines of contiguous values.
+struct Lines {
+    int64_t count, length, ld;
+    int64_t span;                 // lines a tile's offsets reach over
+    bool rows;                    // a line is one k, its values rows
+};
+static Lines lines_of(const ProductArgs &a, bool of_b) {
+    const int64_t ks = 128 / elem(a), rows = !of_b ? a.M : a.kind == kGated ? 2 * a.N : a.N;
+    const bool contiguous = of_b ? a.b_rows : a.a_rows;
+    const int64_t ld = of_b ? a.b.ld : a.a.ld;
+    if (contiguous) return {a.K, rows, ld, ks, true};
+    return {rows, a.K, ld, of_b && a.kind == kGated ? a.N + 256 : 256, false};
 }
+
+// Whether 16-byte pieces from the lines' starts on cover them without reaching into what lies
+// behind, with a tile's offsets below 2^31, if the first line starts on 16 bytes.
+static bool direct(const Lines &o, int64_t e) {
+    if (o.length * e % 16 != 0) return false;
+    if (o.count > 1 && o.ld * e % 16 != 0) return false;
+    if (o.rows && o.count > 1 && o.ld < o.length) return false;     // lines past K have to lie past the last one
+    return o.ld <= (int64_t)0x70000000 / e / o.span;
+}
+
+static int64_t packed_ld(const Lines &o, int64_t e) { return (o.length * e + 15) / 16 * (16 / e); }
+static size_t packed_bytes(const Lines &o, int64_t e) { return (size_t)(o.count * packed_ld(o, e) * e + 255) / 256 * 256; }
+static bool can_pack(const Lines &o, int64_t e) { return packed_ld(o, e) <= (int64_t)0x70000000 / e / o.span; }
 
 // A shape of tile: its size, the workgroups that a CU holds, and what they take (us): a step of K of
 // one alone on its CU, of each of several that share it, and the rest of a workgroup.
@@ -27,8 +44,7 @@ struct Shape {
 
 constexpr int kMostSplits = 16, kSplitSteps = 4;        // of a tile; steps of a split at least
 
-// Tiles of a shape for this product; those that fill the last round of workgroups only in part are
-// split so that they fill it.
+// Tiles of a shape for this product; those beyond a whole number for each CU are split.
 static ProductGrid cut(const ProductArgs &a, const Shape &sh, int64_t splits) {
     const int64_t ks = 128 / elem(a), cols = a.kind == kGated ? sh.size / 2 : sh.size, steps = (a.K + ks - 1) / ks;
     ProductGrid g;
@@ -39,7 +55,7 @@ static ProductGrid cut(const ProductArgs &a, const Shape &sh, int64_t splits) {
     const int64_t per = (steps + splits - 1) / splits;
     g.splits = (int)((steps + per - 1) / per);
     g.steps = (int)per;
-    g.rest = g.splits > 1 ? (int)(tiles % sh.slots()) : 0;
+    g.rest = g.splits > 1 ? (int)(tiles % 256) : 0;
     g.full = (int)(tiles - g.rest);
     if (g.rest == 0) g.splits = 1;
     return g;
@@ -61,22 +77,25 @@ static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g
 }
 
 // The cheapest way to cut a product, by its sizes and type alone.
-static ProductGrid grid_of(const ProductArgs &a, bool dma) {
-    static const Shape bf16_shapes[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
-    static const Shape f32_shapes[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 4.f}};
-    const Shape *shapes = a.dtype == 1 ? bf16_shapes : f32_shapes;
-    const int n = a.dtype == 1 ? (dma ? 3 : 2) : 2;
+static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
+    static const Shape bf16_dma[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
+    static const Shape bf16_any[] = {{64, 4, 0.30f, 0.32f, 3.f}, {128, 2, 0.9f, 0.9f, 4.f}};
+    static const Shape f32_dma[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 4.f}};
+    static const Shape f32_any[] = {{64, 4, 0.7f, 0.8f, 3.f}, {128, 2, 2.5f, 2.4f, 4.f}};
+    const Shape *shapes = a.dtype == 1 ? (dma ? bf16_dma : bf16_any) : dma ? f32_dma : f32_any;
+    const int n = a.dtype == 1 && dma ? 3 : 2;
     const int64_t ks = 128 / elem(a), steps = (a.K + ks - 1) / ks;
     ProductGrid best = cut(a, shapes[n - 1], 1);
     float least = cost_of(a, shapes[n - 1], best);
     for (int i = 0; i < n; ++i) {
-        // whole, split until the last round is full, and half as far
+        // whole, or the tiles that do not make a whole number for each CU split until they give each one
+        // workgroup, as many as it holds, or half of that
         const ProductGrid whole = cut(a, shapes[i], 1);
-        const int rest = (whole.full + whole.rest) % shapes[i].slots();
-        int64_t most = rest ? shapes[i].slots() / rest : 1;
-        if (most > kMostSplits) most = kMostSplits;
-        if (most > steps / kSplitSteps) most = steps / kSplitSteps;
-        for (int64_t splits : {(int64_t)1, (most + 1) / 2, most}) {
+        const int rest = (whole.full + whole.rest) % 256;
+        int64_t most = steps / kSplitSteps < kMostSplits ? steps / kSplitSteps : kMostSplits;
+        const int64_t one = rest ? 256 / rest : 1, all = rest ? shapes[i].slots() / rest : 1;
+        for (int64_t want : {(int64_t)1, one, (all + 1) / 2, all}) {
+            const int64_t splits = want < most ? want : most;
             if (splits < 1) continue;
             const ProductGrid g = cut(a, shapes[i], splits);
             const float t = cost_of(a, shapes[i], g);
@@ -86,7 +105,39 @@ static ProductGrid grid_of(const ProductArgs &a, bool dma) {
             }
         }
     }
+    *cost = least;
     return best;
+}
+
+// How a product runs, by its sizes, strides and type alone.  Operands whose lines are not whole
+// pieces of 16 bytes are read from any address by way of registers, or, where the product is long
+// enough to win that back, laid out anew in the workspace first.
+struct Plan {
+    bool dma, pack_a, pack_b;
+    ProductGrid g;
+    size_t part, total;           // the partial results' place in the workspace (packed operands first), its bytes
+};
+static size_t part_bytes(const ProductGrid &g) { return (size_t)part_floats(g) * 4; }
+
+static Plan plan_of(const ProductArgs &a) {
+    const int64_t e = elem(a);
+    const Lines la = lines_of(a, false), lb = lines_of(a, true);
+    Plan p = {true, !direct(la, e), !direct(lb, e), {}, 0, 0};
+    float fast, any;
+    p.g = grid_of(a, true, &fast);
+    if (p.pack_a || p.pack_b) {
+        const ProductGrid g = grid_of(a, false, &any);
+        const size_t bytes = (p.pack_a ? packed_bytes(la, e) : 0) + (p.pack_b ? packed_bytes(lb, e) : 0);
+        const bool can = (!p.pack_a || can_pack(la, e)) && (!p.pack_b || can_pack(lb, e));
+        if (can && fast + 6.f + bytes * 6e-7f < any) {
+            p.part = bytes;
+        } else {
+            p.dma = p.pack_a = p.pack_b = false;
+            p.g = g;
+        }
+    }
+    p.total = p.part + part_bytes(p.g);
+    return p;
 }
 
 bool product_fits(const ProductArgs &a) {
@@ -94,10 +145,73 @@ bool product_fits(const ProductArgs &a) {
     return (a.M + 63) / 64 <= INT32_MAX / 256 / ((a.N + cols - 1) / cols);
 }
 
+// Tensors may start off 16 bytes, which their sizes do not tell: the product then runs from any
+// address.
 size_t product_workspace_bytes(const ProductArgs &a) {
     if (product_few_rows(a)) return 0;
-    const int64_t x = part_floats(grid_of(a, true)), y = part_floats(grid_of(a, false));
-    return (size_t)(x > y ? x : y) * 4;
+    const Plan p = plan_of(a);
+    if (!p.dma) return p.total;
+    float cost;
+    const size_t any = part_bytes(grid_of(a, false, &cost));
+    return p.total > any ? p.total : any;
+}
+
+// Lines of `length` values at ld to lines of whole pieces, the rest of the last piece zeros: both
+// operands (blockIdx.y) in one launch, a wave for each line, four pieces of a lane on their way.
+struct Packing {
+    const void *src;
+    int64_t ld, lines, length;
+    void *dst;
+};
+template <typename T>
+__global__ __launch_bounds__(256) void product_pack_kernel(Packing a, Packing b) {
+    constexpr int V = product_vec<T>(), U = 4;
+    const Packing p = blockIdx.y ? b : a;
+    const int lane = threadIdx.x % 64;
+    const int64_t whole = p.length / V, pieces = (p.length + V - 1) / V;
+    for (int64_t line = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; line < p.lines; line += (int64_t)gridDim.x * 4) {
+        const T *from = reinterpret_cast<const T *>(p.src) + line * p.ld;
+        u32x4 *to = reinterpret_cast<u32x4 *>(p.dst) + line * pieces;
+        for (int64_t at = lane; at < whole; at += 64 * U) {
+            u32x4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) __builtin_memcpy(&v[u], from + min(at + 64 * u, whole - 1) * V, 16);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (at + 64 * u < whole) to[at + 64 * u] = v[u];
+        }
+        if (lane == 0 && whole < pieces) {
+            T v[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = whole * V + k < p.length ? from[whole * V + k] : from_f32<T>(0.f);
+            __builtin_memcpy(&to[whole], v, 16);
+        }
+    }
+}
+
+// Lays operands anew at `to`, one behind the other.
+static hipError_t pack(const Plan &p, const Lines &la, const Lines &lb, ProductArgs *a, char *to, hipStream_t s) {
+    const int64_t e = elem(*a);
+    Packing job[2];
+    int n = 0;
+    int64_t lines = 0;
+    auto add = [&](const Lines &o, Operand *op) {
+        job[n++] = {op->p, o.ld, o.count, o.length, to};
+        op->p = to;
+        op->ld = packed_ld(o, e);
+        if (o.rows) op->size = op->ld;
+        to += packed_bytes(o, e);
+        if (o.count > lines) lines = o.count;
+    };
+    if (p.pack_a) add(la, &a->a);
+    if (p.pack_b) add(lb, &a->b);
+    if (n == 0) return hipSuccess;
+    if (n == 1) job[1] = job[0];
+    const int64_t blocks = (lines + 3) / 4;
+    const dim3 grid((uint32_t)(blocks < 2048 ? blocks : 2048), (uint32_t)n);
+    if (e == 2) product_pack_kernel<bf16><<<grid, 256, 0, s>>>(job[0], job[1]);
+    else product_pack_kernel<float><<<grid, 256, 0, s>>>(job[0], job[1]);
+    return hipGetLastError();
 }
 
 // Adds the partial results of shared tiles in their order and finishes them, V columns a thread.
@@ -146,20 +260,26 @@ static hipError_t join(const ProductArgs &a, const ProductGrid &g, hipStream_t s
 hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     if (product_few_rows(a0)) return launch_product_rows(a0, s);
     ProductArgs a = a0;
-    if (a.K == 1) {
-        if (a.a_rows) a.a.ld = a.M;
-        if (a.b_rows) a.b.ld = a.N;
+    const Lines la = lines_of(a, false), lb = lines_of(a, true);
+    a.a.size = la.length;
+    a.b.size = lb.length;
+    Plan p = plan_of(a);
+    auto at16 = [](const void *q) { return ((uintptr_t)q & 15u) == 0; };
+    if (p.dma && ((!p.pack_a && !at16(a.a.p)) || (!p.pack_b && !at16(a.b.p)))) {
+        float cost;
+        p = {false, false, false, grid_of(a, false, &cost), 0, 0};
     }
-    const int64_t e = elem(a), ks = 128 / e;
-    const int64_t brows = a.kind == kGated ? 2 * a.N : a.N, bspan = a.kind == kGated ? a.N + 256 : 256;
-    const bool dma = direct(a.a, a.a_rows, a.M, a.K, a.a_rows ? ks : 256, e) &&
-                     direct(a.b, a.b_rows, brows, a.K, a.b_rows ? ks : bspan, e);
-    const ProductGrid g = grid_of(a, dma);
-    hipError_t r;
-    if (a.dtype == 1) r = dma ? launch_tiles_bf16(a, g, s) : launch_tiles_bf16_any(a, g, s);
-    else r = dma ? launch_tiles_f32(a, g, s) : launch_tiles_f32_any(a, g, s);
-    if (r != hipSuccess || g.rest == 0) return r;
-    return a.dtype == 1 ? join<bf16>(a, g, s) : join<float>(a, g, s);
+    char *ws = reinterpret_cast<char *>(a.part);
+    hipError_t r = pack(p, la, lb, &a, ws, s);
+    if (r != hipSuccess) return r;
+    a.part = reinterpret_cast<float *>(ws + p.part);
+    // one line of k has no stride of its own; lines past K lie past it
+    if (la.rows && la.count == 1 && a.a.ld < a.a.size) a.a.ld = a.a.size;
+    if (lb.rows && lb.count == 1 && a.b.ld < a.b.size) a.b.ld = a.b.size;
+    if (a.dtype == 1) r = p.dma ? launch_tiles_bf16(a, p.g, s) : launch_tiles_bf16_any(a, p.g, s);
+    else r = p.dma ? launch_tiles_f32(a, p.g, s) : launch_tiles_f32_any(a, p.g, s);
+    if (r != hipSuccess || p.g.rest == 0) return r;
+    return a.dtype == 1 ? join<bf16>(a, p.g, s) : join<float>(a, p.g, s);
 }
 
 }  // namespace ssd

@@ -7,37 +7,37 @@
 //
 // dpre is rounded to the activations' type, in which the matrix units take it: one rounding of
 // each term of dx and dweight, whose sums are float32.  A stream of 3 (linear) or 5 (gated)
-// elements per result column; a wave takes 64 V neighbouring columns and every 4th row of its
+// elements per result column; a wave takes 64 x 16 bytes of neighbouring columns and every 4th row of its
 // workgroup's share, with one running sum a column, and a second kernel adds the workgroups'
 // rows of sums in order, so results do not depend on scheduling.
 #include "product.h"
 
 namespace ssd {
 
-template <typename T, int V, bool GATED>
+template <typename T, bool GATED>
 __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int64_t rows_each) {
-    __shared__ float red[GATED ? 2 : 1][V][64];
+    constexpr int V = product_vec<T>(), H = GATED ? 2 : 1;
+    __shared__ float red[H][V][64];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int64_t n = ((int64_t)blockIdx.x * 64 + lane) * V, cols = GATED ? 2 * p.N : p.N;
-    const bool on = n < p.N;
+    const int left = (int)min(p.N - n, (int64_t)V);
     const int64_t first = (int64_t)blockIdx.y * rows_each, end = min(first + rows_each, p.M);
-    float sum[GATED ? 2 : 1][V];
+    float sum[H][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        sum[0][i] = 0.f;
-        if constexpr (GATED) sum[1][i] = 0.f;
-    }
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[h][i] = 0.f;
     const T *dy = reinterpret_cast<const T *>(p.dy) + n, *pre = reinterpret_cast<const T *>(p.pre) + n;
     T *dpre = reinterpret_cast<T *>(p.dpre) + n;
-    if (on)
+    if (left > 0)
 #pragma unroll 2
         for (int64_t m = first + wave; m < end; m += 4) {
             float d[V];
-            unpack<T, V>(load_pack<T, V>(dy + m * p.dy_ld), d);
+            load_some<T, V>(dy + m * p.dy_ld, left, d);
             if constexpr (GATED) {
                 float g[V], u[V];
-                unpack<T, V>(load_pack<T, V>(pre + m * cols), g);
-                unpack<T, V>(load_pack<T, V>(pre + m * cols + p.N), u);
+                load_some<T, V>(pre + m * cols, left, g);
+                load_some<T, V>(pre + m * cols + p.N, left, u);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float s;
@@ -47,19 +47,19 @@ __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int6
                     sum[0][i] += g[i];
                     sum[1][i] += u[i];
                 }
-                store_f32<T, V>(dpre + m * cols, g);
-                store_f32<T, V>(dpre + m * cols + p.N, u);
+                store_some<T, V>(dpre + m * cols, left, g);
+                store_some<T, V>(dpre + m * cols + p.N, left, u);
             } else {
                 if (p.act != kActNone) {
                     float v[V];
-                    unpack<T, V>(load_pack<T, V>(pre + m * cols), v);
+                    load_some<T, V>(pre + m * cols, left, v);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         float s;
                         act_d_f32(v[i], p.act, &s);
                         d[i] *= s;
                     }
-                    if (p.dpre) store_f32<T, V>(dpre + m * cols, d);
+                    store_some<T, V>(dpre + m * cols, left, d);
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) sum[0][i] += d[i];
@@ -67,16 +67,17 @@ __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int6
         }
     if (!p.part) return;
 #pragma unroll
-    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+    for (int h = 0; h < H; ++h) {
         for (int w = 0; w < 4; ++w) {
             if (wave == w)
 #pragma unroll
                 for (int i = 0; i < V; ++i) red[h][i][lane] = (w ? red[h][i][lane] : 0.f) + sum[h][i];
             __syncthreads();
         }
-        if (wave == 0 && on)
+        if (wave == 0)
 #pragma unroll
-            for (int i = 0; i < V; ++i) p.part[blockIdx.y * cols + h * p.N + n + i] = red[h][i][lane];
+            for (int i = 0; i < V; ++i)
+                if (i < left) p.part[blockIdx.y * cols + h * p.N + n + i] = red[h][i][lane];
     }
 }
 
@@ -88,45 +89,34 @@ __global__ __launch_bounds__(1024) void product_bias_kernel(const float *part, i
     if (threadIdx.x < 64 && col < cols) out[col] = from_f32<T>(s);
 }
 
-static bool act_vec(const ProductActArgs &a) {
-    const int64_t e = a.dtype == 1 ? 2 : 4;
-    return rows_at16(a.dy, a.M > 1 ? a.dy_ld : 0, e) && rows_at16(a.pre, a.N, e) && rows_at16(a.dpre, a.N, e) && a.N * e % 16 == 0;
-}
-
 // Workgroups over the rows: about 2048 of 4 waves in all, 16 rows for each at least.
 int64_t product_act_rows(int64_t M, int64_t N, int32_t dtype) {
-    const int64_t v = dtype == 1 ? 8 : 4, across = (N + 64 * v - 1) / (64 * v);
+    const int64_t w = dtype == 1 ? 512 : 256, across = (N + w - 1) / w;
     int64_t n = (2048 + across - 1) / across;
     if (n > (M + 15) / 16) n = (M + 15) / 16;
     return n;
 }
 
-static int64_t act_across(const ProductActArgs &a, bool vec) {
-    const int64_t w = 64 * (vec ? (a.dtype == 1 ? 8 : 4) : 1);
+static int64_t act_across(const ProductActArgs &a) {
+    const int64_t w = a.dtype == 1 ? 512 : 256;
     return (a.N + w - 1) / w;
 }
 
 bool product_act_fits(const ProductActArgs &a) {
-    return grid_fits(act_across(a, act_vec(a)), 256) && grid_fits((a.N * (a.gated ? 2 : 1) + 63) / 64, 1024);
+    return grid_fits(act_across(a), 256) && grid_fits((a.N * (a.gated ? 2 : 1) + 63) / 64, 1024);
 }
 
-template <typename T, int V>
+template <typename T>
 static void act_launch(const ProductActArgs &a, dim3 grid, int64_t rows_each, hipStream_t s) {
-    if (a.gated) product_act_kernel<T, V, true><<<grid, 256, 0, s>>>(a, rows_each);
-    else product_act_kernel<T, V, false><<<grid, 256, 0, s>>>(a, rows_each);
+    if (a.gated) product_act_kernel<T, true><<<grid, 256, 0, s>>>(a, rows_each);
+    else product_act_kernel<T, false><<<grid, 256, 0, s>>>(a, rows_each);
 }
 
 hipError_t launch_product_act(const ProductActArgs &a, hipStream_t s) {
-    const bool vec = act_vec(a);
     const int64_t blocks = product_act_rows(a.M, a.N, a.dtype), each = (a.M + blocks - 1) / blocks;
-    const dim3 grid((uint32_t)act_across(a, vec), (uint32_t)((a.M + each - 1) / each));
-    if (a.dtype == 1) {
-        if (vec) act_launch<bf16, 8>(a, grid, each, s);
-        else act_launch<bf16, 1>(a, grid, each, s);
-    } else {
-        if (vec) act_launch<float, 4>(a, grid, each, s);
-        else act_launch<float, 1>(a, grid, each, s);
-    }
+    const dim3 grid((uint32_t)act_across(a), (uint32_t)((a.M + each - 1) / each));
+    if (a.dtype == 1) act_launch<bf16>(a, grid, each, s);
+    else act_launch<float>(a, grid, each, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dbias) return e;
     const int64_t cols = a.gated ? 2 * a.N : a.N;

@@ -47,7 +47,6 @@ __device__ __forceinline__ void each_of(F f) {
     each_index(f, std::make_integer_sequence<int, N>{});
 }
 
-typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 // One operand's tile of R rows in LDS, and how a wave's fragments take its rows: row i of
 // fragment j is 4 NT (i / 4) + 4 j + i % 4 (INTER, NT fragments) or 16 j + i.
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     const int tail = work.first + steps == all && p.K % C::KS ? steps - 1 : -1;      // the step that K ends in
 
     // ---- copies
-    const int64_t a_size = p.M, b_size = C::KIND == kGated ? 2 * p.N : p.N;
+    const int64_t a_size = LA::ROWS ? p.a.size : p.M, b_size = LB::ROWS ? p.b.size : C::KIND == kGated ? 2 * p.N : p.N;
     // 32-bit offsets of this lane's pieces from a scalar base that moves with k.  Copies by way of
     // registers read whole pieces where the operand's rows are contiguous too: one that reaches
     // past the rows reads the next line's first values, and one behind them the tile's first,
@@ -250,7 +249,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     auto clear_tail = [&](auto layout, unsigned char *m) SSD_INLINE {
         typedef decltype(layout) L;
         if constexpr (!L::ROWS) {
-            const int have = (int)(p.K % C::KS) / V;
+            const int have = ((int)(p.K % C::KS) + V - 1) / V;
             for (int slot = threadIdx.x; slot < L::BYTES / 16; slot += C::THREADS)
                 if (L::slot_piece(slot) >= have) *reinterpret_cast<u32x4 *>(m + slot * 16) = u32x4{0, 0, 0, 0};
         }

@@ -17,6 +17,8 @@ SHAPES = [  # rows, inner, outer
 ]
 # enough tiles for the large ones, in each of the products: forward, by x, by the weight
 LARGE = [(2901, 200, 2840), (2901, 2840, 72), (72, 2840, 2904)]
+# large enough to have unaligned operands laid out anew first
+UNALIGNED = [(1500, 1001, 1203), (1203, 777, 2050), (900, 2001, 1600)]
 LARGE_GATED = [(2901, 200, 1424), (2901, 2840, 40), (72, 2840, 1456)]
 DTYPES = [torch.float32, torch.bfloat16]
 
@@ -51,6 +53,14 @@ def test_linear(shape, dtype, act):
 @pytest.mark.parametrize("shape", LARGE, ids=str)
 def test_linear_in_large_tiles(shape):
     test_linear(shape, torch.bfloat16, "silu")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", UNALIGNED, ids=str)
+def test_unaligned_and_long(shape, dtype):
+    test_linear(shape, dtype, "silu")
+    test_linear(shape, dtype, None)
+    test_gated(shape, dtype, "gelu")
 
 
 @pytest.mark.parametrize("shape", LARGE_GATED, ids=str)
