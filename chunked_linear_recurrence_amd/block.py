@@ -7,8 +7,14 @@ and the residual.
     y_t = block.step(x_t, state)         # the next token [b, 768], the state moved on in place
 
 The projections are plain matrix products (torch); everything between them runs in the
-library's kernels, forwards and backwards.  `python -m chunked_linear_recurrence_amd.block`
-trains a small block, runs a prompt and continues it token by token.
+library's kernels, forwards and backwards.
+
+    layer = SelectiveLayer(768, device="cuda")
+
+is such a block and a gated feed-forward behind it, called in the same way: the sum with the
+residual and the norm between the two halves are one kernel, the gated product one, and the
+product back with its residual one.  `python -m chunked_linear_recurrence_amd.block` trains a
+small block and a small layer, runs a prompt of each and continues it token by token.
 """
 import math
 
@@ -24,6 +30,10 @@ def _rows(g, like):
     if g is None:
         return torch.zeros_like(like)
     return g if g.stride(-1) == 1 else g.contiguous()
+
+
+def _last_contiguous(g):
+    return g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous()
 
 
 class _Norm(torch.autograd.Function):
@@ -77,6 +87,57 @@ class _Selective(torch.autograd.Function):
         return (g.du, g.ddelta, g.dA, g.dB, g.dC, g.dD, g.dz, g.ddelta_bias, g.dinit if ctx.has_init else None, None)
 
 
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, act):
+        y, pre = ssd.linear_fwd(x, weight, bias, residual, act=act, keep=True)
+        ctx.save_for_backward(x, weight, bias, pre)
+        ctx.act = act
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias, pre = ctx.saved_tensors
+        g = ssd.linear_bwd(_last_contiguous(dy), x, weight, bias, pre, act=ctx.act, need=ctx.needs_input_grad[:3])
+        return g.dx, g.dweight, g.dbias, dy if ctx.needs_input_grad[3] else None, None
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, act):
+        h, pre = ssd.gated_fwd(x, weight, bias, act=act, keep=True)
+        ctx.save_for_backward(x, weight, bias, pre)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x, weight, bias, pre = ctx.saved_tensors
+        g = ssd.gated_bwd(_last_contiguous(dh), x, weight, bias, pre, act=ctx.act, need=ctx.needs_input_grad[:3])
+        return g.dx, g.dweight, g.dbias, None
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, branch, residual, gate, post_weight, scale, pre_weight, eps):
+        ctx.set_materialize_grads(False)
+        y, total, stats = ssd.residual_norm_fwd(branch, residual, gate, post_weight, scale, pre_weight, eps, want_stats=True)
+        ctx.save_for_backward(branch, residual, gate, post_weight, scale, pre_weight, stats)
+        return y, total
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dtotal):
+        branch, residual, gate, post_weight, scale, pre_weight, stats = ctx.saved_tensors
+        dy = None if pre_weight is None else _rows(dy, branch)
+        if dtotal is not None or dy is None:
+            dtotal = _rows(dtotal, branch)
+        g = ssd.residual_norm_bwd(dy, dtotal, branch, residual, gate, post_weight, scale, pre_weight, stats)
+        return g.dbranch, g.dresidual, g.dgate, g.dpost_weight, g.dscale, g.dpre_weight, None
+
+
 def norm(x, weight=None, bias=None, eps=1e-5):
     """ssd.norm_fwd with gradients: x [rows, channels]."""
     return _Norm.apply(x, weight, bias, eps)
@@ -92,6 +153,22 @@ def selective(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state=Non
     kept by every call (dstate / 2 bytes a token and channel), with gradients switched off too;
     ssd.selective_fwd by itself keeps none."""
     return _Selective.apply(u, delta, A, B, C, D, z, delta_bias, init_state, lengths)
+
+
+def linear(x, weight, bias=None, residual=None, act=None):
+    """ssd.linear_fwd with gradients: x [rows, inner], weight [outer, inner]."""
+    return _Linear.apply(x, weight, bias, residual, act)
+
+
+def gated(x, weight, bias=None, act="silu"):
+    """ssd.gated_fwd with gradients: x [rows, inner], weight [2 hidden, inner].  What the backward
+    needs (2 hidden values a row) is kept by every call; ssd.gated_fwd by itself keeps nothing."""
+    return _Gated.apply(x, weight, bias, act)
+
+
+def residual_norm(branch, residual=None, gate=None, post_weight=None, scale=None, pre_weight=None, eps=1e-5):
+    """ssd.residual_norm_fwd with gradients; (y, total), y None without pre_weight."""
+    return _ResidualNorm.apply(branch, residual, gate, post_weight, scale, pre_weight, eps)
 
 
 class SelectiveBlock(torch.nn.Module):
@@ -124,16 +201,14 @@ class SelectiveBlock(torch.nn.Module):
         self.D = f32(torch.ones(d))
         self.out_proj = matrix(width, d)
 
-    def forward(self, x, state=None, lengths=None):
-        """x [b, L, width]; state as returned (None: zeros); lengths [b] int32: each row's own
-        tokens.  What x holds past them reaches no result and no gradient but the residual's own.
-        Returns (y [b, L, width], state)."""
+    def branch(self, x, state=None, lengths=None):
+        """What forward adds to x, [b * L, width], and the state."""
         b, L, _ = x.shape
         d, n, r = self.channels, self.dstate, self.rank
         conv_state, scan_state = state if state is not None else (None, None)
         own = x
         if lengths is not None:      # the norm and the projections take every row; 0 x NaN would reach their weights
-            own = x.masked_fill((torch.arange(L, device=x.device) >= lengths[:, None])[..., None], 0)
+            own = x.masked_fill(_behind(x, lengths), 0)
         h = norm(own.reshape(b * L, self.width), self.norm_weight, self.norm_bias)
         xz = F.linear(h, self.in_proj).view(b, L, 2 * d)
         u, conv_state = conv(xz[..., :d], self.conv_weight, self.conv_bias, conv_state, lengths)
@@ -143,11 +218,18 @@ class SelectiveBlock(torch.nn.Module):
         C = p[:, r + n:].view(b, L, 1, n)
         y, scan_state = selective(u, delta, -torch.exp(self.A_log), B, C, self.D, xz[..., d:], self.dt_bias, scan_state,
                                   lengths)
-        return x + F.linear(y.view(b * L, d), self.out_proj).view(b, L, self.width), (conv_state, scan_state)
+        return F.linear(y.view(b * L, d), self.out_proj), (conv_state, scan_state)
+
+    def forward(self, x, state=None, lengths=None):
+        """x [b, L, width]; state as returned (None: zeros); lengths [b] int32: each row's own
+        tokens.  What x holds past them reaches no result and no gradient but the residual's own.
+        Returns (y [b, L, width], state)."""
+        y, state = self.branch(x, state, lengths)
+        return x + y.view(x.shape), state
 
     @torch.no_grad()
-    def step(self, x, state):
-        """One token x [b, width]; state is moved on in place.  Returns y [b, width]."""
+    def step_branch(self, x, state):
+        """What step adds to x."""
         d, n, r = self.channels, self.dstate, self.rank
         h = ssd.norm_fwd(x, self.norm_weight, self.norm_bias)
         xz = F.linear(h, self.in_proj)
@@ -156,31 +238,84 @@ class SelectiveBlock(torch.nn.Module):
         delta = F.linear(p[:, :r], self.dt_proj)
         y = ssd.selective_step(u, delta, -torch.exp(self.A_log), p[:, None, r:r + n], p[:, None, r + n:], self.D, xz[:, d:],
                                self.dt_bias, state[1])
-        return x + F.linear(y, self.out_proj)
+        return F.linear(y, self.out_proj)
+
+    @torch.no_grad()
+    def step(self, x, state):
+        """One token x [b, width]; state is moved on in place.  Returns y [b, width]."""
+        return x + self.step_branch(x, state)
+
+
+def _behind(x, lengths):
+    """[b, L, 1]: the tokens behind each row's own."""
+    return (torch.arange(x.shape[1], device=x.device) >= lengths[:, None])[..., None]
+
+
+class SelectiveLayer(torch.nn.Module):
+    """A SelectiveBlock and a gated feed-forward of `hidden` channels (8/3 of the width, a whole
+    number of 64, by default) behind it:
+        total = x + scale * branch(x);  y = total + out(act(g) * u),  [g | u] = rms(total) w_in^T
+    scale [width] and the norm's weight are float32, the projections `dtype`.  Arguments beside
+    these are the block's."""
+
+    def __init__(self, width, hidden=None, *, act="silu", dtype=torch.bfloat16, device="cuda", **block):
+        super().__init__()
+        self.block = SelectiveBlock(width, dtype=dtype, device=device, **block)
+        self.width, self.hidden, self.act = width, hidden or 64 * math.ceil(width / 24), act
+        self.scale = torch.nn.Parameter(torch.ones(width, device=device))
+        self.norm_weight = torch.nn.Parameter(torch.ones(width, device=device))
+
+        def matrix(rows, cols):
+            return torch.nn.Parameter((torch.randn(rows, cols, device=device) / math.sqrt(cols)).to(dtype))
+        self.in_proj, self.out_proj = matrix(2 * self.hidden, width), matrix(width, self.hidden)
+
+    def forward(self, x, state=None, lengths=None):
+        """As SelectiveBlock's, but the outputs behind a row's own tokens are 0 and what x holds
+        there reaches no gradient at all."""
+        b, L, _ = x.shape
+        if lengths is not None:
+            x = x.masked_fill(_behind(x, lengths), 0)
+        branch, state = self.block.branch(x, state, lengths)
+        n, total = residual_norm(branch, x.reshape(b * L, self.width), scale=self.scale, pre_weight=self.norm_weight)
+        y = linear(gated(n, self.in_proj, act=self.act), self.out_proj, residual=total)
+        return y.view(b, L, self.width), state
+
+    @torch.no_grad()
+    def step(self, x, state):
+        """One token x [b, width]; state is moved on in place.  Returns y [b, width]."""
+        n, total = ssd.residual_norm_fwd(self.block.step_branch(x, state), x, scale=self.scale, pre_weight=self.norm_weight)
+        return ssd.linear_fwd(ssd.gated_fwd(n, self.in_proj, act=self.act), self.out_proj, None, total)
+
+
+def _train(name, model, max_norm=None):
+    """Trains on a small task, then runs a prompt and continues it token by token."""
+    b, L, width, T = 4, 512, model.width, 32
+    opt = torch.optim.Adam(model.parameters(), lr=2e-3)
+    x = torch.randn(b, L, width, device="cuda").bfloat16()
+    target = torch.roll(x, 3, 1)                       # each token answers with the one three before it
+    for k in range(20):
+        y, _ = model(x)
+        loss = (y.float() - target.float())[:, 3:].square().mean()
+        opt.zero_grad()
+        loss.backward()
+        norm = None if max_norm is None else ssd.clip_grads([p.grad for p in model.parameters()], max_norm)
+        opt.step()
+        if k % 5 == 0 or k == 19:
+            print("%s, training step %2d: loss %.4f%s" % (
+                name, k, loss.item(), "" if norm is None else ", gradients' norm %.4f" % norm.item()), flush=True)
+    with torch.no_grad():
+        whole, _ = model(x)
+        y, state = model(x[:, :L - T].contiguous())
+        steps = [model.step(x[:, t], state) for t in range(L - T, L)]
+        err = (torch.stack(steps, 1).float() - whole[:, L - T:].float()).abs().max().item()
+    print("%s, prompt of %d tokens, then %d single tokens: largest difference from one prompt %.3g (largest value %.3g)" % (
+        name, L - T, T, err, whole.float().abs().max().item()), flush=True)
 
 
 def main():
     torch.manual_seed(0)
-    b, L, width, T = 4, 512, 256, 32
-    block = SelectiveBlock(width)
-    opt = torch.optim.Adam(block.parameters(), lr=2e-3)
-    x = torch.randn(b, L, width, device="cuda").bfloat16()
-    target = torch.roll(x, 3, 1)                       # each token answers with the one three before it
-    for k in range(20):
-        y, _ = block(x)
-        loss = (y.float() - target.float())[:, 3:].square().mean()
-        opt.zero_grad()
-        loss.backward()
-        opt.step()
-        if k % 5 == 0 or k == 19:
-            print("training step %2d: loss %.4f" % (k, loss.item()), flush=True)
-    with torch.no_grad():
-        whole, _ = block(x)
-        y, state = block(x[:, :L - T].contiguous())
-        steps = [block.step(x[:, t], state) for t in range(L - T, L)]
-        err = (torch.stack(steps, 1).float() - whole[:, L - T:].float()).abs().max().item()
-    print("prompt of %d tokens, then %d single tokens: largest difference from one prompt %.3g (largest value %.3g)" % (
-        L - T, T, err, whole.float().abs().max().item()), flush=True)
+    _train("block", SelectiveBlock(256))
+    _train("layer", SelectiveLayer(256), max_norm=1.0)
 
 
 if __name__ == "__main__":

@@ -136,6 +136,7 @@ ssd_status_t product_fwd(const char *what, bool gated, const ssd_product_dims_t 
     TRY(act_of(flags, gated, &act));
     if (!x || !weight || !y) return fail(SSD_ERR_NULL_ARG, "x, weight and %s must be non-NULL", gated ? "h" : "y");
     ssd::ProductArgs a = product_args(d, gated);
+    if (!ssd::product_fits(a)) return beyond(what);
     const size_t need = align_up(ssd::product_workspace_bytes(a));
     TRY(check_workspace(workspace, workspace_bytes, need));
     const size_t e = (size_t)act_bytes(d.dtype), n = (size_t)d.outer * (gated ? 2 : 1), m = (size_t)d.rows;
@@ -148,7 +149,6 @@ ssd_status_t product_fwd(const char *what, bool gated, const ssd_product_dims_t 
     const Tensor out[] = {{gated ? "h" : "y", y, m * (size_t)d.outer * e, e}, {"pre", pre, m * n * e, e},
                           {"workspace", need ? workspace : nullptr, need, 16}};
     TRY(check_tensors(in, 4, out, 3));
-    if (!ssd::product_fits(a)) return beyond(what);
     a.a.p = x;
     a.b.p = weight;
     a.bias = bias;

@@ -142,7 +142,15 @@ static Plan plan_of(const ProductArgs &a) {
 
 bool product_fits(const ProductArgs &a) {
     const int64_t cols = a.kind == kGated ? 32 : 64;
-    return (a.M + 63) / 64 <= INT32_MAX / 256 / ((a.N + cols - 1) / cols);
+    const int64_t down = (a.M + 63) / 64, across = (a.N + cols - 1) / cols;
+    if (down > (INT64_C(1) << 30) / across) return false;       // tiles are counted in int
+    if (down * across <= 1 << 22) return true;                   // whatever their shape
+    float cost;
+    for (bool dma : {false, true}) {
+        const ProductGrid g = grid_of(a, dma, &cost);
+        if (!grid_fits(g.full + (int64_t)g.rest * g.splits, g.bm == 256 ? 512 : 256)) return false;
+    }
+    return true;
 }
 
 // Tensors may start off 16 bytes, which their sizes do not tell: the product then runs from any

@@ -123,7 +123,7 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
 // here, 13.8 in tiles; 64 rows 21.6 and 13.9; 64 rows of 1536 x 768 8.9 and 11.3.
 bool product_few_rows(const ProductArgs &a) {
     if (a.a_rows || a.b_rows) return false;
-    return a.M <= 32 || (a.M <= 64 && a.N * a.K <= (INT64_C(1) << 22));
+    return a.M <= SSD_PRODUCT_FEW_ROWS || (a.M <= 64 && a.N * a.K <= (INT64_C(1) << 22));
 }
 
 // 16 rows of the weight a workgroup and up to 16 waves for them while that leaves CUs idle, else 32

@@ -4,6 +4,7 @@ Every step of the computation runs in the library's HIP kernels.  torch is used 
 device memory (output and workspace tensors) and for the current HIP stream.  If the
 built library is missing the first call raises; there is no fallback path.
 """
+import array
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -855,6 +856,8 @@ def norm_bwd(dy, x, weight, mean, rstd, *, workspace=None, stream=None):
 # Conventions as above.  Weights and biases of products are of the activations' dtype, as their
 # gradients are; the norms' and the scale's parameters and gradients are float32.
 
+_FEW_ROWS = 32       # forward products of up to so many rows need no workspace (SSD_PRODUCT_FEW_ROWS)
+
 _ACT_FLAG = {None: 0, "silu": SSD_FLAG_SILU, "gelu": SSD_FLAG_GELU}
 
 
@@ -898,10 +901,10 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=None, y=None, keep=Fa
         with ctx:
             return linear_fwd(x, weight, bias, residual, act=act, y=y, keep=keep, workspace=workspace)
     dims = ProductDims(m, k, n, code, 0, xs, rs, 0)
-    ws = _workspace(workspace, L_.ssd_linear_fwd_workspace_bytes(dims), dev)
+    ws = _workspace(workspace, L_.ssd_linear_fwd_workspace_bytes(dims) if m > _FEW_ROWS else 0, dev)
     given = y
-    y = _out("y", y, (m, n), dtype, dev)
-    pre = torch.empty((m, n), dtype=dtype, device=dev) if keep and flag else None
+    y = x.new_empty((m, n)) if y is None else _out("y", y, (m, n), dtype, dev)
+    pre = x.new_empty((m, n)) if keep and flag else None
     _check(L_.ssd_linear_fwd(dims, *ptrs, rp, y.data_ptr(), _ptr(pre), flag, ws.data_ptr(), ws.numel(), _current(x)))
     if given is not None:
         _wrote(given)
@@ -966,10 +969,10 @@ def gated_fwd(x, weight, bias=None, *, act="silu", h=None, keep=False, workspace
         with ctx:
             return gated_fwd(x, weight, bias, act=act, h=h, keep=keep, workspace=workspace)
     dims = ProductDims(m, k, f, code, 0, xs, 0, 0)
-    ws = _workspace(workspace, L_.ssd_gated_fwd_workspace_bytes(dims), dev)
+    ws = _workspace(workspace, L_.ssd_gated_fwd_workspace_bytes(dims) if m > _FEW_ROWS else 0, dev)
     given = h
-    h = _out("h", h, (m, f), dtype, dev)
-    pre = torch.empty((m, 2 * f), dtype=dtype, device=dev) if keep else None
+    h = x.new_empty((m, f)) if h is None else _out("h", h, (m, f), dtype, dev)
+    pre = x.new_empty((m, 2 * f)) if keep else None
     _check(L_.ssd_gated_fwd(dims, *ptrs, h.data_ptr(), _ptr(pre), flag, ws.data_ptr(), ws.numel(), _current(x)))
     if given is not None:
         _wrote(given)
@@ -1087,7 +1090,7 @@ def _clip(tensors, max_norm, out, scale, workspace, stream):
     if not isinstance(first, torch.Tensor):
         raise ValueError("tensor 0 must be a torch.Tensor (got %s)" % type(first).__name__)
     dev = first.device
-    ptrs, sizes, codes = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    codes = []
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise ValueError("tensor %d must be a torch.Tensor (got %s)" % (i, type(t).__name__))
@@ -1098,24 +1101,30 @@ def _clip(tensors, max_norm, out, scale, workspace, stream):
             raise ValueError("tensor %d is on %s; expected %s" % (i, t.device, dev))
         if not t.is_contiguous():
             raise ValueError("tensor %d must be contiguous" % i)
-        ptrs[i], sizes[i], codes[i] = t.data_ptr(), t.numel(), code
+        codes.append(code)
+    # arrays of machine integers, whose addresses the call takes
+    ptrs = array.array("Q", [t.data_ptr() for t in tensors])
+    sizes, codes = array.array("q", [t.numel() for t in tensors]), array.array("i", codes)
     outs = ptrs if scale else None
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError("out has %d tensors; expected %d" % (len(out), n))
-        outs = (ctypes.c_void_p * n)()
         for i, (o, t) in enumerate(zip(out, tensors)):
-            outs[i] = _param("out %d" % i, o, t.shape, dev, t.dtype)
-            if o is None:
-                raise ValueError("out %d is required" % i)
+            if not isinstance(o, torch.Tensor):
+                raise ValueError("out %d must be a torch.Tensor (got %s)" % (i, type(o).__name__))
+            if o.shape != t.shape or o.dtype != t.dtype or o.device != dev or not o.is_contiguous():
+                raise ValueError("out %d must be a contiguous tensor of shape %s, dtype %s on %s" % (
+                    i, tuple(t.shape), t.dtype, dev))
+        outs = array.array("Q", [o.data_ptr() for o in out])
     ctx = _elsewhere(first, stream)
     if ctx is not None:
         with ctx:
             return _clip(tensors, max_norm, out, scale, workspace, None)
-    ws = _workspace(workspace, L_.ssd_clip_workspace_bytes(n, sizes), dev)
+    at = lambda a: None if a is None else a.buffer_info()[0]
+    ws = _workspace(workspace, L_.ssd_clip_workspace_bytes(n, at(sizes)), dev)
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    _check(L_.ssd_clip(n, ptrs, outs, sizes, codes, max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+    _check(L_.ssd_clip(n, at(ptrs), at(outs), at(sizes), at(codes), max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
                        _current(first)))
     if scale:
         _wrote(*(tensors if out is None else out))

@@ -410,8 +410,9 @@ typedef struct ssd_product_dims {
  *   y         [rows, outer] (act); pre [rows, outer] (act) or NULL (ssd_linear_bwd needs it
  *             where there is an activation)
  *   flags     0, SSD_FLAG_SILU or SSD_FLAG_GELU
- *   workspace ssd_linear_fwd_workspace_bytes (0 where the product's inner dimension is not
- *             cut: it may then be NULL) */
+ *   workspace ssd_linear_fwd_workspace_bytes (0 for up to SSD_PRODUCT_FEW_ROWS rows and
+ *             wherever none is needed: it may then be NULL) */
+#define SSD_PRODUCT_FEW_ROWS 32
 size_t ssd_linear_fwd_workspace_bytes(const ssd_product_dims_t *dims);
 ssd_status_t ssd_linear_fwd(const ssd_product_dims_t *dims, const void *x, const void *weight, const void *bias,
                             const void *residual, void *y, void *pre, uint32_t flags, void *workspace,
