@@ -315,7 +315,7 @@ def _train(name, model, max_norm=None):
 def main():
     torch.manual_seed(0)
     _train("block", SelectiveBlock(256))
-    _train("layer", SelectiveLayer(256), max_norm=1.0)
+    _train("layer", SelectiveLayer(256), max_norm=0.1)
 
 
 if __name__ == "__main__":

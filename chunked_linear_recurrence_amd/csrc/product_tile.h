@@ -35,6 +35,8 @@ constexpr int kStepBytes = 128;
 
 #define SSD_INLINE __attribute__((always_inline))     // of a lambda: its captures stay in registers
 
+constexpr int kAhead = 3;         // the step whose lines are touched, after the one multiplied
+
 constexpr int min_of(int a, int b) { return a < b ? a : b; }
 
 // f(0), f(1), .. f(N - 1) with constants for arguments
@@ -124,6 +126,7 @@ struct ProductCfg {
     static constexpr int KS = kStepBytes / (int)sizeof(T);
     static constexpr int QA = LA::BYTES / 1024 / NW, QB = LB::BYTES / 1024 / NW;   // copies per wave and step
     static_assert(QA * 1024 * NW == LA::BYTES && QB * 1024 * NW == LB::BYTES, "whole waves of 16-byte pieces");
+    static constexpr bool TOUCH = DMA && BM == 256;
     static constexpr int WAVES = BM >= 128 ? 2 : 4;               // of a SIMD at least: registers for its tiles
     static_assert(KIND != kGated || (TN % 2 == 0 && !B_ROWS), "gate and up rows side by side");
 };
@@ -181,6 +184,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     typedef typename C::LB LB;
     constexpr int E = (int)sizeof(T), V = 16 / E;
     __shared__ __align__(16) unsigned char A0[LA::BYTES], B0[LB::BYTES], A1[LA::BYTES], B1[LB::BYTES];
+    __shared__ __align__(16) unsigned char unread[C::TOUCH ? C::NW * 256 : 16];      // what touched lines leave
 
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
@@ -305,6 +309,35 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     auto copies_b = [&](int t, int from, int end, unsigned char *to) SSD_INLINE {
         copies(LB{}, src_b, t, from, end, C::QB, offb, to);
     };
+    // A line of memory that no workgroup of the XCD has read yet comes from behind its L2, later than a
+    // step takes: with every line already there the copies alone of 8192^3 take 0.85 million
+    // cycles, as they are 1.67 (the products 1.05).  So the lines of a later step are touched
+    // ahead, one access of 4 bytes each, by one of the workgroups that share them: of the 4 tiles of
+    // a row each takes a quarter of A's lines, of the 8 of a column an eighth of B's; even waves
+    // A's, odd waves B's.  (8192^3: 840 -> 824 us, 783 -> 775 by x, 807 -> 782 by the weight; in
+    // the smaller tiles, whose workgroups share a CU, it was not tried.)
+    const bool of_b = w & 1;
+    Source src_ahead = of_b ? src_b : src_a;
+    uint32_t off_ahead = 0x80000000u;                            // none: past every source
+    if constexpr (C::TOUCH) {
+        static_assert(LA::BYTES == 256 * 128 && LB::BYTES == 256 * 128, "256 lines of 128 bytes a step");
+        constexpr int NA = 256 / 4 / (C::NW / 2), NB = 256 / 8 / (C::NW / 2);            // of them a wave's
+        const int n = of_b ? NB : NA, line = ((of_b ? work.m % 8 : work.n % 4) * (C::NW / 2) + w / 2) * n + lane;
+        if (lane < n) {
+            if (of_b ? LB::ROWS : LA::ROWS) {
+                off_ahead = (uint32_t)(line / 4 * (of_b ? p.b.ld : p.a.ld) * E) + line % 4 * 128;
+            } else {
+                const int64_t r = of_b ? b_row<C>(p, n0, line) - n0 : min(m0 + line, p.M - 1) - m0;
+                off_ahead = (uint32_t)(r * (of_b ? p.b.ld : p.a.ld) * E);
+            }
+        }
+        src_ahead.at += (kAhead - 1) * src_ahead.step;
+    }
+    auto touch = [&](int t) SSD_INLINE {
+        const rsrc_t rs = make_rsrc(src_ahead.at, t + 1 < steps ? src_ahead.whole : 0u);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)(unread + w * 256), 4, off_ahead, 0, 0, 0);
+        src_ahead.at += src_ahead.step;
+    };
     auto fetch_both = [&](int t) SSD_INLINE {
         fetch(LA{}, p.a, m0, a_size, false, quick_a, t, C::QA, offa, ra);
         fetch(LB{}, p.b, n0, b_size, true, quick_b, t, C::QB, offb, rb);
@@ -358,7 +391,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     // moves no access of memory across it.
     auto landed = [&]() SSD_INLINE {
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0);
+        __builtin_amdgcn_s_waitcnt(C::TOUCH ? 0x0071 : 0);        // the last touch, behind the copies, may be on its way
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
@@ -381,6 +414,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
                 if constexpr (i < PARTS) copies_a(t + 2, i * C::QA / PARTS, (i + 1) * C::QA / PARTS, a0);
                 else if constexpr (i < 2 * PARTS)
                     copies_b(t + 2, (i - PARTS) * C::QB / PARTS, (i - PARTS + 1) * C::QB / PARTS, b0);
+                else if constexpr (C::TOUCH && i == 2 * PARTS) touch(t + kAhead);
             });
         } else {
             if (t + 2 < steps) store_fetch(t + 2, a0, b0);
@@ -390,9 +424,14 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     if constexpr (C::DMA) {
         copies_a(0, 0, C::QA, A0);
         copies_b(0, 0, C::QB, B0);
+        __builtin_amdgcn_s_waitcnt(0);
         landed();
         copies_a(1, 0, C::QA, A1);
         copies_b(1, 0, C::QB, B1);
+        if constexpr (C::TOUCH) {
+            __builtin_amdgcn_sched_barrier(0);                   // behind the copies, which the waits count on
+            touch(kAhead - 1);
+        }
         if (tail == 0) clear(A0, B0);
     } else {
         fetch_both(0);
