@@ -118,12 +118,14 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
     }
 }
 
-// Up to 32 rows, and up to 64 of a small weight: there the tiles' second launch costs more than x's
-// fragments, which every workgroup reads for itself.  32 rows of 4096 x 4096 in bfloat16: 12.9 us
-// here, 13.8 in tiles; 64 rows 21.6 and 13.9; 64 rows of 1536 x 768 8.9 and 11.3.
+// Up to 32 rows; up to 48 of a weight of many rows, which workgroups take 32 at a time; up to 64 of a
+// small weight: beyond, tiles share x's reads, which here every workgroup makes for itself.  In
+// bfloat16, here and in tiles: 32 rows of 4096 x 4096 12.8 us and 13.8, 64 rows 21.7 and 13.9; 48
+// rows of 2048 x (2 x 5632) 16.8 and 19.6, 64 rows 19.3 and 19.9; 64 rows of 1536 x 768 8.9 and 11.3.
 bool product_few_rows(const ProductArgs &a) {
     if (a.a_rows || a.b_rows) return false;
-    return a.M <= SSD_PRODUCT_FEW_ROWS || (a.M <= 64 && a.N * a.K <= (INT64_C(1) << 22));
+    return a.M <= SSD_PRODUCT_FEW_ROWS || (a.M <= 48 && a.N > 4096) ||
+           (a.M <= 64 && a.N * a.K <= (INT64_C(1) << 22));
 }
 
 // 16 rows of the weight a workgroup and up to 16 waves for them while that leaves CUs idle, else 32
@@ -132,7 +134,8 @@ bool product_few_rows(const ProductArgs &a) {
 template <typename T, ProductKind KIND, int MT>
 static hipError_t rows_launch(const ProductArgs &a, hipStream_t s) {
     const Epilogue ep = epilogue_of(a);
-    if (a.N <= 4096) product_rows_kernel<T, KIND, MT, 1, 16 / MT><<<(uint32_t)((a.N + 15) / 16), 64 * (16 / MT), 0, s>>>(a, ep);
+    constexpr int WAVES = MT == 1 ? 16 : MT == 2 ? 8 : 4;
+    if (a.N <= 4096) product_rows_kernel<T, KIND, MT, 1, WAVES><<<(uint32_t)((a.N + 15) / 16), 64 * WAVES, 0, s>>>(a, ep);
     else product_rows_kernel<T, KIND, MT, 2, 4><<<(uint32_t)((a.N + 31) / 32), 256, 0, s>>>(a, ep);
     return hipGetLastError();
 }
@@ -142,6 +145,7 @@ static hipError_t rows_by_m(const ProductArgs &a, hipStream_t s) {
     const bool gated = a.kind == kGated;
     if (a.M <= 16) return gated ? rows_launch<T, kGated, 1>(a, s) : rows_launch<T, kLinear, 1>(a, s);
     if (a.M <= 32) return gated ? rows_launch<T, kGated, 2>(a, s) : rows_launch<T, kLinear, 2>(a, s);
+    if (a.M <= 48) return gated ? rows_launch<T, kGated, 3>(a, s) : rows_launch<T, kLinear, 3>(a, s);
     return gated ? rows_launch<T, kGated, 4>(a, s) : rows_launch<T, kLinear, 4>(a, s);
 }
 

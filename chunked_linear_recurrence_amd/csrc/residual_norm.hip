@@ -10,7 +10,8 @@
 //
 // What is not given drops out.  A stream of up to 5 elements in the forward and 8 in the
 // backward per channel; a row is read once and held in registers between its sums (1, 4 or 8
-// waves, the fewest that hold it; rows wider than that are read again for each sum).  s is
+// waves, the fewest that hold it; rows wider than that, or narrower than 16 bytes and off them,
+// are read again for each sum).  s is
 // formed again in the backward in float32, from the same reads that its rounded copy would
 // cost, so no rounding of s enters a gradient.  The three column sums are kept in registers
 // over a workgroup's rows, leave it as one row of partial sums, and a second kernel adds those
@@ -23,10 +24,43 @@ constexpr int kRnFwdBlocks = 1024, kRnBwdBlocks = 512;   // workgroups at most
 
 template <int WPR> constexpr int rn_threads() { return WPR == 8 ? 512 : 256; }
 // Whether registers hold the next row beside the backward's current one
-template <typename T, int V, int K> constexpr bool rn_ahead() { return K * (V == 1 ? 1 : V * (int)sizeof(T) / 4) <= 8; }
+template <typename T, int V, int K> constexpr bool rn_ahead() { return K * V * (int)sizeof(T) / 4 <= 8; }
 template <int WPR> constexpr int rn_rows() { return WPR == 1 ? 4 : 1; }       // rows a workgroup holds at a time
 
-template <typename T, int V, int K, int WPR>
+// Where a thread's k-th access of V values to a row of D begins.  ANY: rows may start anywhere and end
+// inside an access, which then begins V values before the row's end; the first `over` of its
+// values are another thread's, read as zeros and not stored.  (Loads of single values for the
+// row's end made the workgroup wait for one wave: 16000 rows of 2047 channels in bfloat16, 255 us
+// backward.)
+template <int V, int WPR, bool ANY>
+struct Place {
+    int c, over;
+    bool on;
+    __device__ __forceinline__ Place(int k, int tid, int D) {
+        const int at = (k * 64 * WPR + tid) * V;
+        on = at < D;
+        c = ANY ? min(at, D - V) : at;
+        over = ANY ? at - c : 0;
+    }
+};
+template <typename T, int V, int WPR, bool ANY>
+__device__ __forceinline__ void store_at(void *p, int64_t row, int D, const Place<V, WPR, ANY> &at, const float (&v)[V]) {
+    T *y = reinterpret_cast<T *>(p) + row * D + at.c;
+    if constexpr (!ANY) {
+        store_f32<T, V>(y, v);
+    } else if (at.over == 0) {
+        typename Pack<T, V>::type q;
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = from_f32<T>(v[i]);
+        __builtin_memcpy(y, &q, sizeof(q));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i >= at.over) y[i] = from_f32<T>(v[i]);
+    }
+}
+
+template <typename T, int V, int K, int WPR, bool ANY>
 struct RowRegs {
     typename Pack<T, V>::type v[K];
     // this thread's accesses of a row (null: none); those past the row are left alone
@@ -34,8 +68,22 @@ struct RowRegs {
         if (!x) return;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * 64 * WPR + tid) * V;
-            if (c < D) v[k] = load_pack<T, V>(x + c);
+            const Place<V, WPR, ANY> at(k, tid, D);
+            if (at.on) __builtin_memcpy(&v[k], x + at.c, sizeof(v[k]));
+        }
+    }
+    // of what was loaded, another thread's values to zeros (apart, so that loads may be on their way)
+    __device__ __forceinline__ void own(int D, int tid) {
+        if constexpr (ANY) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const Place<V, WPR, ANY> at(k, tid, D);
+                if (at.on && at.over > 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (i < at.over) v[k][i] = from_f32<T>(0.f);
+                }
+            }
         }
     }
 };
@@ -45,28 +93,27 @@ __device__ __forceinline__ const T *row_at(const void *p, int64_t row, int64_t s
     return p ? reinterpret_cast<const T *>(p) + row * stride : nullptr;
 }
 
-template <int V, int K, int WPR>
+template <int V, int K, int WPR, bool ANY>
 __device__ __forceinline__ void load_params(const float *p, int D, int tid, float (&v)[K][V]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+        const Place<V, WPR, ANY> at(k, tid, D);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (k * 64 * WPR + tid) * V;
-            v[k][i] = p && c < D ? p[c + i] : 1.f;
-        }
+        for (int i = 0; i < V; ++i) v[k][i] = p && at.on ? p[at.c + i] : 1.f;
+    }
 }
 
-template <typename T, int V, int K, int WPR>
+template <typename T, int V, int K, int WPR, bool ANY>
 __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(ResidualNormArgs a) {
     __shared__ float red[16];
     constexpr int R = rn_rows<WPR>();
     const int tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
     const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? threadIdx.x / 64 : 0), by = (int64_t)gridDim.x * R;
     float post[K][V], scale[K][V], pre[K][V];
-    load_params<V, K, WPR>(a.post, a.D, tid, post);
-    load_params<V, K, WPR>(a.scale, a.D, tid, scale);
-    load_params<V, K, WPR>(a.pre, a.D, tid, pre);
-    RowRegs<T, V, K, WPR> bn = {}, zn = {}, rn = {};
+    load_params<V, K, WPR, ANY>(a.post, a.D, tid, post);
+    load_params<V, K, WPR, ANY>(a.scale, a.D, tid, scale);
+    load_params<V, K, WPR, ANY>(a.pre, a.D, tid, pre);
+    RowRegs<T, V, K, WPR, ANY> bn = {}, zn = {}, rn = {};
     auto fetch = [&](int64_t row) {
         bn.load(row_at<T>(a.branch, row, a.branch_stride), a.D, tid);
         zn.load(row_at<T>(a.gate, row, a.gate_stride), a.D, tid);
@@ -74,8 +121,10 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
     };
     if (first < a.rows) fetch(first);
     for (int64_t row = first; row < a.rows; row += by) {
-        const RowRegs<T, V, K, WPR> b = bn, z = zn, r = rn;
+        RowRegs<T, V, K, WPR, ANY> b = bn, z = zn, r = rn;
         if (row + by < a.rows) fetch(row + by);
+        b.own(a.D, tid);
+        if (a.residual) r.own(a.D, tid);
         float v[K][V];
         float sq = 0.f;
 #pragma unroll
@@ -87,7 +136,7 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
 #pragma unroll
                 for (int i = 0; i < V; ++i) v[k][i] *= silu_f32(g[i]);
             }
-            if ((k * 64 * WPR + tid) * V < a.D)
+            if (Place<V, WPR, ANY>(k, tid, a.D).on)
 #pragma unroll
                 for (int i = 0; i < V; ++i) sq = fmaf(v[k][i], v[k][i], sq);
         }
@@ -100,9 +149,9 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
             unpack<T, V>(r.v[k], res);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[k][i] = fmaf(v[k][i] * rt * post[k][i], scale[k][i], a.residual ? res[i] : 0.f);
-            const int c = (k * 64 * WPR + tid) * V;
-            if (c < a.D) {
-                store_f32<T, V>(reinterpret_cast<T *>(a.total) + row * a.D + c, v[k]);
+            const Place<V, WPR, ANY> at(k, tid, a.D);
+            if (at.on) {
+                store_at<T, V, WPR, ANY>(a.total, row, a.D, at, v[k]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) sq = fmaf(v[k][i], v[k][i], sq);
             }
@@ -112,11 +161,11 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
             rs = 1.f / sqrtf(row_sum<WPR>(sq, red) / a.D + a.eps);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int c = (k * 64 * WPR + tid) * V;
-                if (c < a.D) {
+                const Place<V, WPR, ANY> at(k, tid, a.D);
+                if (at.on) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * rs * pre[k][i];
-                    store_f32<T, V>(reinterpret_cast<T *>(a.y) + row * a.D + c, v[k]);
+                    store_at<T, V, WPR, ANY>(a.y, row, a.D, at, v[k]);
                 }
             }
         }
@@ -127,7 +176,7 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
     }
 }
 
-// Rows wider than registers: one workgroup a row, a pass over it for each sum and one to store.
+// Rows that registers do not hold: one workgroup a row, a pass over it for each sum and one to store.
 template <typename T>
 struct WideRow {
     const T *b, *z, *r;
@@ -174,7 +223,7 @@ __global__ __launch_bounds__(1024) void residual_norm_fwd_wide_kernel(ResidualNo
     }
 }
 
-template <typename T, int V, int K, int WPR>
+template <typename T, int V, int K, int WPR, bool ANY>
 __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(ResidualNormArgs a) {
     __shared__ float red[16];
     __shared__ float cols[WPR == 1 ? 3 * 64 * V * K : 1];
@@ -182,16 +231,16 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
     const int wave = threadIdx.x / 64, tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
     const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0), by = (int64_t)gridDim.x * R;
     float post[K][V], scale[K][V], pre[K][V], sums[3][K][V];
-    load_params<V, K, WPR>(a.post, a.D, tid, post);
-    load_params<V, K, WPR>(a.scale, a.D, tid, scale);
-    load_params<V, K, WPR>(a.pre, a.D, tid, pre);
+    load_params<V, K, WPR, ANY>(a.post, a.D, tid, post);
+    load_params<V, K, WPR, ANY>(a.scale, a.D, tid, scale);
+    load_params<V, K, WPR, ANY>(a.pre, a.D, tid, pre);
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) sums[q][k][i] = 0.f;
-    RowRegs<T, V, K, WPR> bn = {}, zn = {}, rn = {}, yn = {}, tn = {};
+    RowRegs<T, V, K, WPR, ANY> bn = {}, zn = {}, rn = {}, yn = {}, tn = {};
     float rt_n = 1.f, rs_n = 1.f;
     auto fetch = [&](int64_t row) {
         bn.load(row_at<T>(a.branch, row, a.branch_stride), a.D, tid);
@@ -204,9 +253,12 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
     };
     if (first < a.rows) fetch(first);
     for (int64_t row = first; row < a.rows; row += by) {
-        const RowRegs<T, V, K, WPR> bq = bn, zq = zn, rq = rn, yq = yn, tq = tn;
+        RowRegs<T, V, K, WPR, ANY> bq = bn, zq = zn, rq = rn, yq = yn, tq = tn;
         const float rt = rt_n, rs = rs_n;
         if (rn_ahead<T, V, K>() && row + by < a.rows) fetch(row + by);
+        bq.own(a.D, tid);
+        if (a.dy) yq.own(a.D, tid);
+        if (a.dtotal) tq.own(a.D, tid);
         float that[K][V], d[K][V], s[K][V];
         float dot = 0.f;
 #pragma unroll
@@ -225,7 +277,7 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
                 float r[V], dy[V];
                 unpack<T, V>(rq.v[k], r);
                 unpack<T, V>(yq.v[k], dy);
-                const bool on = (k * 64 * WPR + tid) * V < a.D;
+                const bool on = Place<V, WPR, ANY>(k, tid, a.D).on;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     s[k][i] = fmaf(that[k][i] * post[k][i], scale[k][i], r[i]) * rs;      // shat
@@ -249,9 +301,9 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
         dot = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * 64 * WPR + tid) * V;
-            if (c < a.D) {
-                if (a.dresidual) store_f32<T, V>(reinterpret_cast<T *>(a.dresidual) + row * a.D + c, d[k]);
+            const Place<V, WPR, ANY> at(k, tid, a.D);
+            if (at.on) {
+                if (a.dresidual) store_at<T, V, WPR, ANY>(a.dresidual, row, a.D, at, d[k]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     sums[1][k][i] = fmaf(d[k][i], that[k][i] * post[k][i], sums[1][k][i]);
@@ -271,8 +323,8 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * 64 * WPR + tid) * V;
-            if (c >= a.D) continue;
+            const Place<V, WPR, ANY> at(k, tid, a.D);
+            if (!at.on) continue;
             if (a.gate) {
                 float z[V], b[V], dz[V];
                 unpack<T, V>(zq.v[k], z);
@@ -283,9 +335,9 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
                     dz[i] = d[k][i] * b[i] * sg * fmaf(z[i], 1.f - sg, 1.f);
                     d[k][i] *= z[i] * sg;
                 }
-                store_f32<T, V>(reinterpret_cast<T *>(a.dgate) + row * a.D + c, dz);
+                store_at<T, V, WPR, ANY>(a.dgate, row, a.D, at, dz);
             }
-            store_f32<T, V>(reinterpret_cast<T *>(a.dbranch) + row * a.D + c, d[k]);
+            store_at<T, V, WPR, ANY>(a.dbranch, row, a.D, at, d[k]);
         }
         if (!rn_ahead<T, V, K>() && row + by < a.rows) fetch(row + by);
     }
@@ -309,24 +361,25 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
             __syncthreads();
         }
         for (int m = threadIdx.x; m < 3 * M; m += 256) {
-            const int q = m / M, l = m % 64, ki = m % M / 64;
-            const int c = ((ki / V) * 64 + l) * V + ki % V;
-            if (c < a.D) part[(int64_t)q * a.D + c] = cols[m];
+            const int q = m / M, l = m % 64, k = m % M / 64 / V, i = m / 64 % V;
+            const Place<V, WPR, ANY> at(k, l, a.D);
+            if (at.on && i >= at.over) part[(int64_t)q * a.D + at.c + i] = cols[m];
         }
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * 64 * WPR + tid) * V;
-            if (c < a.D)
+            const Place<V, WPR, ANY> at(k, tid, a.D);
+            if (at.on)
 #pragma unroll
                 for (int q = 0; q < 3; ++q)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) part[(int64_t)q * a.D + c + i] = sums[q][k][i];
+                    for (int i = 0; i < V; ++i)
+                        if (i >= at.over) part[(int64_t)q * a.D + at.c + i] = sums[q][k][i];
         }
     }
 }
 
-// Rows wider than registers: the same sums by passes over the row; the terms of the three
+// Rows that registers do not hold: the same sums by passes over the row; the terms of the three
 // column sums are left to the kernel below, which needs each row's two means (rows of `mean`).
 template <typename T>
 __device__ __forceinline__ void wide_terms(const ResidualNormArgs &a, const WideRow<T> &w, int64_t row, int c, float rt,
@@ -406,11 +459,11 @@ __global__ __launch_bounds__(1024) void residual_norm_sum_kernel(ResidualNormArg
     if (out) out[col % a.D] = s;
 }
 
-// Rows that registers hold: 8192 channels, 4096 where accesses take one value.
-constexpr int kRnMost = 8192, kRnMostOne = 4096;
+// Channels that registers hold at most
+constexpr int kRnMost = 8192;
 
 int64_t residual_norm_bwd_blocks(int64_t rows) { return rows < kRnBwdBlocks ? rows : kRnBwdBlocks; }
-size_t residual_norm_mean_rows(int64_t rows, int64_t D) { return D > kRnMostOne ? (size_t)rows : 0; }
+size_t residual_norm_mean_rows(int64_t rows, int64_t D) { return D > kRnMost || D < 8 ? (size_t)rows : 0; }
 
 static bool rn_sums(const ResidualNormArgs &a) { return a.dpre || a.dscale || a.dpost; }
 
@@ -424,14 +477,14 @@ static bool rn_vec(const ResidualNormArgs &a) {
 }
 
 bool residual_norm_fits(const ResidualNormArgs &a) {
-    return a.D <= (rn_vec(a) ? kRnMost : kRnMostOne) || (grid_fits(a.rows, 1024) && grid_fits((3 * (int64_t)a.D + 63) / 64, 1024));
+    return (a.D >= 8 && a.D <= kRnMost) || (grid_fits(a.rows, 1024) && grid_fits((3 * (int64_t)a.D + 63) / 64, 1024));
 }
 
-template <typename T, int V, int K, int WPR>
+template <typename T, int V, int K, int WPR, bool ANY>
 static hipError_t rn_fwd(const ResidualNormArgs &a, hipStream_t s) {
     constexpr int R = rn_rows<WPR>();
     const int64_t n = min((a.rows + R - 1) / R, (int64_t)kRnFwdBlocks);
-    residual_norm_fwd_kernel<T, V, K, WPR><<<(uint32_t)n, rn_threads<WPR>(), 0, s>>>(a);
+    residual_norm_fwd_kernel<T, V, K, WPR, ANY><<<(uint32_t)n, rn_threads<WPR>(), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -441,13 +494,13 @@ static hipError_t rn_sum(const ResidualNormArgs &a, int64_t blocks, hipStream_t 
     return hipGetLastError();
 }
 
-template <typename T, int V, int K, int WPR>
+template <typename T, int V, int K, int WPR, bool ANY>
 static hipError_t rn_bwd(const ResidualNormArgs &a0, hipStream_t s) {
     constexpr int R = rn_rows<WPR>();
     ResidualNormArgs a = a0;
     if (!rn_sums(a)) a.part = nullptr;
     const int64_t n = min((a.rows + R - 1) / R, residual_norm_bwd_blocks(a.rows));
-    residual_norm_bwd_kernel<T, V, K, WPR><<<(uint32_t)n, rn_threads<WPR>(), 0, s>>>(a);
+    residual_norm_bwd_kernel<T, V, K, WPR, ANY><<<(uint32_t)n, rn_threads<WPR>(), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : rn_sum(a, n, s);
 }
@@ -469,43 +522,35 @@ static hipError_t rn_bwd_wide(const ResidualNormArgs &a, hipStream_t s) {
     return e != hipSuccess ? e : rn_sum(a, n, s);
 }
 
-// The fewest waves that hold a row of D channels at 16 bytes (16 values at most) or one value
-// an access.
-#define RN_BF16(DIR)                                                     \
+// The fewest waves that hold a row of D channels, 16 bytes an access and 16 values a thread at most.
+#define RN_BF16(DIR, ANY)                                                \
     do {                                                                 \
-        if (a.D <= 512) return rn_##DIR<bf16, 8, 1, 1>(a, s);            \
-        if (a.D <= 1024) return rn_##DIR<bf16, 8, 2, 1>(a, s);           \
-        if (a.D <= 2048) return rn_##DIR<bf16, 8, 1, 4>(a, s);           \
-        if (a.D <= 4096) return rn_##DIR<bf16, 8, 2, 4>(a, s);           \
-        if (a.D <= kRnMost) return rn_##DIR<bf16, 8, 2, 8>(a, s);        \
+        if (a.D <= 512) return rn_##DIR<bf16, 8, 1, 1, ANY>(a, s);       \
+        if (a.D <= 1024) return rn_##DIR<bf16, 8, 2, 1, ANY>(a, s);      \
+        if (a.D <= 2048) return rn_##DIR<bf16, 8, 1, 4, ANY>(a, s);      \
+        if (a.D <= 4096) return rn_##DIR<bf16, 8, 2, 4, ANY>(a, s);      \
+        if (a.D <= kRnMost) return rn_##DIR<bf16, 8, 2, 8, ANY>(a, s);   \
     } while (0)
-#define RN_F32(DIR)                                                      \
+#define RN_F32(DIR, ANY)                                                 \
     do {                                                                 \
-        if (a.D <= 256) return rn_##DIR<float, 4, 1, 1>(a, s);           \
-        if (a.D <= 512) return rn_##DIR<float, 4, 2, 1>(a, s);           \
-        if (a.D <= 1024) return rn_##DIR<float, 4, 1, 4>(a, s);          \
-        if (a.D <= 2048) return rn_##DIR<float, 4, 2, 4>(a, s);          \
-        if (a.D <= 4096) return rn_##DIR<float, 4, 4, 4>(a, s);          \
-        if (a.D <= kRnMost) return rn_##DIR<float, 4, 4, 8>(a, s);       \
-    } while (0)
-#define RN_ONE(DIR, T)                                                   \
-    do {                                                                 \
-        if (a.D <= 256) return rn_##DIR<T, 1, 4, 1>(a, s);               \
-        if (a.D <= 1024) return rn_##DIR<T, 1, 4, 4>(a, s);              \
-        if (a.D <= 2048) return rn_##DIR<T, 1, 8, 4>(a, s);              \
-        if (a.D <= kRnMostOne) return rn_##DIR<T, 1, 8, 8>(a, s);        \
+        if (a.D <= 256) return rn_##DIR<float, 4, 1, 1, ANY>(a, s);      \
+        if (a.D <= 512) return rn_##DIR<float, 4, 2, 1, ANY>(a, s);      \
+        if (a.D <= 1024) return rn_##DIR<float, 4, 1, 4, ANY>(a, s);     \
+        if (a.D <= 2048) return rn_##DIR<float, 4, 2, 4, ANY>(a, s);     \
+        if (a.D <= 4096) return rn_##DIR<float, 4, 4, 4, ANY>(a, s);     \
+        if (a.D <= kRnMost) return rn_##DIR<float, 4, 4, 8, ANY>(a, s);  \
     } while (0)
 
 #define RN_LAUNCH(DIR)                              \
     do {                                            \
         const bool vec = rn_vec(a);                 \
         if (a.dtype == 1) {                         \
-            if (vec) RN_BF16(DIR);                  \
-            RN_ONE(DIR, bf16);                      \
+            if (vec) RN_BF16(DIR, false);           \
+            if (a.D >= 8) RN_BF16(DIR, true);       \
             return rn_##DIR##_wide<bf16>(a, s);     \
         }                                           \
-        if (vec) RN_F32(DIR);                       \
-        RN_ONE(DIR, float);                         \
+        if (vec) RN_F32(DIR, false);                \
+        if (a.D >= 4) RN_F32(DIR, true);            \
         return rn_##DIR##_wide<float>(a, s);        \
     } while (0)
 

@@ -12,7 +12,7 @@ DEV = "cuda:0"
 
 SHAPES = [  # rows, inner, outer
     (1, 1, 1), (1, 8, 16), (2, 7, 3), (1, 2048, 520), (3, 1000, 264), (5, 64, 64), (16, 256, 96), (17, 129, 33),
-    (31, 72, 200), (32, 300, 4300), (9, 136, 4104), (48, 512, 352), (40, 1100, 4000), (64, 264, 136), (65, 72, 136), (128, 64, 128), (129, 128, 127), (130, 200, 264),
+    (31, 72, 200), (32, 300, 4300), (9, 136, 4104), (45, 200, 4100), (64, 72, 4200), (48, 512, 352), (40, 1100, 4000), (64, 264, 136), (65, 72, 136), (128, 64, 128), (129, 128, 127), (130, 200, 264),
     (255, 777, 129), (300, 96, 520), (513, 640, 392), (700, 72, 1032), (1030, 136, 520),
 ]
 # enough tiles for the large ones, in each of the products: forward, by x, by the weight

@@ -113,7 +113,7 @@ def run(t):
 SHAPES = [  # rows, D, elements between rows beyond D
     (1, 1, 0), (1, 768, 0), (3, 2, 0), (2, 63, 1), (5, 64, 0), (4, 65, 3), (7, 255, 0), (6, 257, 0), (9, 512, 8),
     (3, 520, 0), (700, 1024, 0), (11, 1025, 0), (5, 2048, 2048), (3, 2056, 0), (2, 4095, 0), (4, 4096, 0), (3, 4104, 8),
-    (3, 8192, 0), (2, 8199, 0), (3, 16384, 0), (1500, 40, 0),
+    (3, 8192, 0), (3, 5001, 1), (2, 8190, 3), (600, 1001, 0), (2, 8199, 0), (3, 16384, 0), (1500, 40, 0),
 ]
 
 
