@@ -461,24 +461,37 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
         }
         return;
     }
-    constexpr int W = V < 4 * C::NT ? V : 4 * C::NT;
-    const int64_t n = n0 + col;
+    // what the epilogue reads, all of it before the first store, which the compiler would not pass
+    constexpr int W = V < 4 * C::NT ? V : 4 * C::NT, PARTS = 4 * C::NT / W;
+    const int64_t n = n0 + col, m = m0 + wm * 16 * C::TM + i16;
+    float bias[C::KIND == kGated ? 2 : 1][PARTS][W];
+    typename Pack<T, W>::type residual[C::TM][PARTS];
+#pragma unroll
+    for (int c = 0; c < PARTS; ++c) {
+        if constexpr (C::KIND != kPlain) load_bias<T, W>(ep, n + c * W, false, bias[0][c]);
+        if constexpr (C::KIND == kGated) load_bias<T, W>(ep, n + c * W, true, bias[1][c]);
+        if constexpr (C::KIND == kLinear)
+#pragma unroll
+            for (int i = 0; i < C::TM; ++i) residual[i][c] = load_residual<T, W>(ep, m + 16 * i, n + c * W);
+    }
 #pragma unroll
     for (int i = 0; i < C::TM; ++i) {
-        const int64_t m = m0 + wm * 16 * C::TM + 16 * i + i16;
-        if (m >= p.M) continue;
+        if (m + 16 * i >= p.M) break;
 #pragma unroll
-        for (int c = 0; c < 4 * C::NT; c += W) {
+        for (int c = 0; c < PARTS; ++c) {
             float v[W];
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[e] = acc[i][(c + e) / 4][e % 4];
+            for (int e = 0; e < W; ++e) v[e] = acc[i][(c * W + e) / 4][e % 4];
             if constexpr (C::KIND == kGated) {
                 float u[W];
 #pragma unroll
-                for (int e = 0; e < W; ++e) u[e] = acc[i][C::NT + (c + e) / 4][e % 4];
-                finish_gated<T, W>(ep, m, n + c, v, u);
+                for (int e = 0; e < W; ++e) u[e] = acc[i][C::NT + (c * W + e) / 4][e % 4];
+                finish_gated<T, W>(ep, m + 16 * i, n + c * W, bias[0][c], bias[1][c], v, u);
+            } else if constexpr (C::KIND == kLinear) {
+                finish_linear<T, W>(ep, m + 16 * i, n + c * W, bias[0][c], residual[i][c], v);
             } else {
-                finish_linear<T, W>(ep, m, n + c, v);
+                const int left = (int)min(p.N - (n + c * W), (int64_t)W);
+                store_some<T, W>(reinterpret_cast<T *>(ep.y) + (m + 16 * i) * ep.N + n + c * W, left, v);
             }
         }
     }
