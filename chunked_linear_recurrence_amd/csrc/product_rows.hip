@@ -15,6 +15,10 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
     typedef typename Frag<T>::type F;
     constexpr int V = 16 / (int)sizeof(T), KS = kStepBytes / (int)sizeof(T), TILES = KIND == kGated ? 2 * NT : NT;
     constexpr int U = MT * TILES > 4 ? 1 : MT > 1 ? 2 : 4;       // steps whose loads are started together
+    // Whether the next ones are on their way while these are multiplied, where few waves share a CU and
+    // registers hold both: 48 rows of 6216 x (2 x 4200) 44.2 -> 38.1 us, 33 of 2048 x (2 x 5632) 17.4 ->
+    // 14.9; one row of 4096 x (2 x 8192) 22.1 -> 24.1, so not for it.
+    constexpr bool AHEAD = NT == 2 && (MT == 2 || MT == 3);
     __shared__ f32x4 sums[WAVES][MT][TILES][64];
     const int lane = threadIdx.x % 64, i16 = lane % 16, g = lane / 16;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -40,9 +44,9 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
         __builtin_memcpy(&f, q, 16);
         return f;
     };
-    auto take = [&](int64_t s, auto count) SSD_INLINE {
-        constexpr int N = decltype(count)::value;
-        F fb[N][2][TILES], fx[N][2][MT];
+    // the fragments of N steps
+    auto fetch = [&](int64_t s, auto &fb, auto &fx) SSD_INLINE {
+        constexpr int N = (int)(sizeof(fb) / sizeof(fb[0]));
 #pragma unroll
         for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -53,6 +57,9 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
 #pragma unroll
                 for (int i = 0; i < MT; ++i) fx[q][h][i] = load(x[i] + k);
             }
+    };
+    auto products = [&](const auto &fb, const auto &fx) SSD_INLINE {
+        constexpr int N = (int)(sizeof(fb) / sizeof(fb[0]));
 #pragma unroll
         for (int q = 0; q < N; ++q)
 #pragma unroll
@@ -64,8 +71,33 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
     };
     int64_t s = first;
     const int64_t full = min(end, whole);
-    for (; s + U <= full; s += U) take(s, std::integral_constant<int, U>{});
-    for (; s < full; ++s) take(s, std::integral_constant<int, 1>{});
+    if constexpr (AHEAD) {
+        F fb[2][U][2][TILES], fx[2][U][2][MT];
+        if (s + U <= full) {
+            fetch(s, fb[0], fx[0]);
+            s += U;
+            while (s + 2 * U <= full) {
+                fetch(s, fb[1], fx[1]);
+                __builtin_amdgcn_sched_barrier(0);
+                products(fb[0], fx[0]);
+                fetch(s + U, fb[0], fx[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                products(fb[1], fx[1]);
+                s += 2 * U;
+            }
+            products(fb[0], fx[0]);
+        }
+    }
+    for (; s + U <= full; s += U) {
+        F fb[U][2][TILES], fx[U][2][MT];
+        fetch(s, fb, fx);
+        products(fb, fx);
+    }
+    for (; U > 1 && s < full; ++s) {
+        F fb[1][2][TILES], fx[1][2][MT];
+        fetch(s, fb, fx);
+        products(fb, fx);
+    }
     if (s < end) {                                               // the step that K ends in
         auto some = [&](const T *q, int64_t k) SSD_INLINE {
             const int64_t have = p.K - k - g * V;
@@ -121,7 +153,7 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
 // Up to 32 rows; up to 48 of a weight of many rows, which workgroups take 32 at a time; up to 64 of a
 // small weight: beyond, tiles share x's reads, which here every workgroup makes for itself.  In
 // bfloat16, here and in tiles: 32 rows of 4096 x 4096 12.8 us and 13.8, 64 rows 21.7 and 13.9; 48
-// rows of 2048 x (2 x 5632) 16.8 and 19.6, 64 rows 19.3 and 19.9; 64 rows of 1536 x 768 8.9 and 11.3.
+// rows of 2048 x (2 x 5632) 16.2 and 19.6, 64 rows 19.6 and 19.9; 64 rows of 1536 x 768 8.9 and 11.3.
 bool product_few_rows(const ProductArgs &a) {
     if (a.a_rows || a.b_rows) return false;
     return a.M <= SSD_PRODUCT_FEW_ROWS || (a.M <= 48 && a.N > 4096) ||
