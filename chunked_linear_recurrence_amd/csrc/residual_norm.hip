@@ -124,6 +124,7 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
         RowRegs<T, V, K, WPR, ANY> b = bn, z = zn, r = rn;
         if (row + by < a.rows) fetch(row + by);
         b.own(a.D, tid);
+        if (a.gate) z.own(a.D, tid);                             // 0 x infinity
         if (a.residual) r.own(a.D, tid);
         float v[K][V];
         float sq = 0.f;

@@ -194,3 +194,25 @@ def test_many_rows_are_summed_in_a_fixed_order():
     _, _, stats = ssd.residual_norm_fwd(*t[:6], EPS, want_stats=True)
     a, b = (ssd.residual_norm_bwd(t[6], t[7], *t[:6], stats) for _ in range(2))
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("d", [1024, 1025, 1029, 333])
+def test_an_infinite_gate_stays_in_its_channel(d, dtype):
+    """Channels that a row's last access shares with the one before it are read twice and count
+    once, whatever they hold: the sum of squares is infinite and not NaN, so the normed row is
+    0 and the total the residual, but for the infinite channel itself."""
+    rows = 5
+    gen = torch.Generator().manual_seed(d)
+    branch, residual, gate = (torch.randn(rows, d, generator=gen).to(dtype) for _ in range(3))
+    at = d - 3
+    branch[:, at] = 1.
+    gate[:, at] = float("inf")
+    ones = torch.ones(d, device=DEV)
+    y, total = ssd.residual_norm_fwd(branch.to(DEV), residual.to(DEV), gate.to(DEV), ones)
+    assert y is None
+    others = [c for c in range(d) if c != at]
+    assert torch.equal(total.cpu()[:, others], residual[:, others]) and total[:, at].isnan().all()
+    y, total = ssd.residual_norm_fwd(branch.to(DEV), residual.to(DEV), gate.to(DEV), None, None, ones)
+    assert total[:, at].isinf().all() and total[:, others].isfinite().all()
+    assert (y[:, others] == 0).all() and y[:, at].isnan().all()
