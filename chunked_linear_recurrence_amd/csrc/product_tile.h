@@ -230,7 +230,8 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
     auto source = [&](auto layout, const Operand &o, int64_t row, int64_t size) SSD_INLINE {
         typedef decltype(layout) L;
         auto bytes = [&](int64_t k) SSD_INLINE {
-            return (uint32_t)min((L::ROWS ? (k - 1) * o.ld + size - row : (size - 1 - row) * o.ld + k) * E, (int64_t)0x7fffffff);
+            const int64_t in = (k + V - 1) / V * V;               // lines are whole pieces, zeros past K
+            return (uint32_t)min((L::ROWS ? (k - 1) * o.ld + size - row : (size - 1 - row) * o.ld + in) * E, (int64_t)0x7fffffff);
         };
         return Source{reinterpret_cast<const unsigned char *>(o.p) + (L::ROWS ? k_first * o.ld + row : row * o.ld + k_first) * E,
                       (L::ROWS ? o.ld * C::KS : C::KS) * E, bytes(C::KS + 1),

@@ -63,6 +63,16 @@ def test_unaligned_and_long(shape, dtype):
     test_gated(shape, dtype, "gelu")
 
 
+@pytest.mark.parametrize("shape", [(4095, 777, 2051), (2561, 2047, 2051)], ids=str)
+def test_laid_out_with_an_odd_last_value(shape):
+    """bfloat16 operands that are laid out anew (in a workspace that holds both) and whose lines end
+    with half of 4 bytes."""
+    m, k, n = shape
+    dims = ssd.ProductDims(m, k, n, ssd._DTYPE_CODE[torch.bfloat16], 0, k, n, n)
+    assert ssd.lib().ssd_linear_fwd_workspace_bytes(dims) >= 2 * (m + n) * k
+    test_linear(shape, torch.bfloat16, "silu")
+
+
 @pytest.mark.parametrize("shape", LARGE_GATED, ids=str)
 def test_gated_in_large_tiles(shape):
     test_gated(shape, torch.bfloat16, "silu")
