@@ -42,6 +42,8 @@ struct Shape {
     int slots() const { return 256 * each_cu; }
 };
 
+// A split's partial results (64 KB of a tile of 128, written and read again) have to be fewer than what
+// it reads for them: at least 4 steps of 32 KB.
 constexpr int kMostSplits = 16, kSplitSteps = 4;        // of a tile; steps of a split at least
 
 // Tiles of a shape for this product; those beyond a whole number for each CU are split.
@@ -76,7 +78,10 @@ static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g
     return t;
 }
 
-// The cheapest way to cut a product, by its sizes and type alone.
+// The cheapest way to cut a product, by its sizes and type alone.  Small tiles give every CU work,
+// large ones read less from LDS and the caches for each product: us in tiles of 64, 128 and 256,
+// bfloat16, 512 x 2048 x 2048 13.5, 23.3, 32.9; 2048 x 2048 x 4096 55.9, 40.0, 49.3; 4096^3 189, 134,
+// 109; float32 512 x 1024 x 1024 16.8, 29.2 (whole tiles of 64: 21.6).
 static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
     static const Shape bf16_dma[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
     static const Shape bf16_any[] = {{64, 4, 0.30f, 0.32f, 3.f}, {128, 2, 0.9f, 0.9f, 4.f}};
@@ -111,7 +116,8 @@ static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
 
 // How a product runs, by its sizes, strides and type alone.  Operands whose lines are not whole
 // pieces of 16 bytes are read from any address by way of registers, or, where the product is long
-// enough to win that back, laid out anew in the workspace first.
+// enough to win that back (6 us and 0.6 for each MB), laid out anew in the workspace first:
+// 4095^3 in bfloat16 217 us by way of registers and 134 so, 1999 x 777 x 1025 in float32 63 and 45.
 struct Plan {
     bool dma, pack_a, pack_b;
     ProductGrid g;
