@@ -94,7 +94,7 @@ ssd::ProductArgs grad_w_args(const ssd_product_dims_t &d, int64_t cols, const vo
 }
 
 // A backward's workspace: dpre where it is formed, the bias' partial sums, and what the two
-// products need, which run one after the other.
+// products need.
 struct GradLayout {
     size_t dpre, sums, part, total;
 };
@@ -108,8 +108,8 @@ GradLayout grad_layout(const ssd_product_dims_t &d, bool gated, bool forms) {
     off += align_up((size_t)(ssd::product_act_rows(d.rows, d.outer, d.dtype) * cols * 4));
     lo.part = off;
     const int64_t ld = forms ? cols : d.dy_row_stride;
-    off += align_up(std::max(ssd::product_workspace_bytes(grad_x_args(d, cols, nullptr, ld, nullptr)),
-                             ssd::product_workspace_bytes(grad_w_args(d, cols, nullptr, ld, nullptr))));
+    off += align_up(ssd::product_grads_workspace_bytes(grad_x_args(d, cols, nullptr, ld, nullptr),
+                                                       grad_w_args(d, cols, nullptr, ld, nullptr)));
     lo.total = off;
     return lo;
 }
@@ -211,8 +211,7 @@ ssd_status_t product_bwd(const char *what, bool gated, const ssd_product_dims_t 
     gx.y = dx;
     gw.y = dweight;
     gx.part = gw.part = reinterpret_cast<float *>(ws + lo.part);
-    if (r == hipSuccess && dx) r = ssd::launch_product(gx, s);
-    if (r == hipSuccess && dweight) r = ssd::launch_product(gw, s);
+    if (r == hipSuccess) r = ssd::launch_product_grads(gx, gw, s);
     return launched(what, r);
 }
 

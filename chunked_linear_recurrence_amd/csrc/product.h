@@ -66,12 +66,21 @@ __host__ __device__ inline TileAt tile_at(int id, const ProductGrid &g) {
 bool product_fits(const ProductArgs &a);                  // its work is within a launch
 size_t product_workspace_bytes(const ProductArgs &a);
 hipError_t launch_product(const ProductArgs &a, hipStream_t s);
+// A gradient's products by x (dpre [M, K] x weight) and by the weight (dpre^T x x); the results that are
+// null are left out
+size_t product_grads_workspace_bytes(const ProductArgs &x, const ProductArgs &w);
+hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipStream_t s);
 
 // One file each: operands copied to LDS directly, or (_any) from any address
 hipError_t launch_tiles_bf16(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_bf16_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_f32(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
 hipError_t launch_tiles_f32_any(const ProductArgs &a, const ProductGrid &g, hipStream_t s);
+// Both products of a gradient in one launch (operands copied directly, tiles of 64)
+hipError_t launch_pair_bf16(const ProductArgs &x, const ProductGrid &gx, const ProductArgs &w, const ProductGrid &gw,
+                            bool x_first, hipStream_t s);
+hipError_t launch_pair_f32(const ProductArgs &x, const ProductGrid &gx, const ProductArgs &w, const ProductGrid &gw,
+                           bool x_first, hipStream_t s);
 
 // Few rows: product_rows.hip, without a workspace
 bool product_few_rows(const ProductArgs &a);

@@ -42,6 +42,13 @@ struct Shape {
     int slots() const { return 256 * each_cu; }
 };
 
+// For operands copied to LDS directly and for those from any address
+constexpr Shape bf16_dma[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
+constexpr Shape bf16_any[] = {{64, 4, 0.30f, 0.32f, 3.f}, {128, 2, 0.9f, 0.9f, 4.f}};
+constexpr Shape f32_dma[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 4.f}};
+constexpr Shape f32_any[] = {{64, 4, 0.7f, 0.8f, 3.f}, {128, 2, 2.5f, 2.4f, 4.f}};
+constexpr int kPairTiles = 1 << 20;                     // of two products in one launch, well within a grid's range
+
 // A split's partial results (64 KB of a tile of 128, written and read again) have to be fewer than what
 // it reads for them: at least 4 steps of 32 KB.
 constexpr int kMostSplits = 16, kSplitSteps = 4;        // of a tile; steps of a split at least
@@ -83,10 +90,6 @@ static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g
 // bfloat16, 512 x 2048 x 2048 13.5, 23.3, 32.9; 2048 x 2048 x 4096 55.9, 40.0, 49.3; 4096^3 189, 134,
 // 109; float32 512 x 1024 x 1024 16.8, 29.2 (whole tiles of 64: 21.6).
 static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
-    static const Shape bf16_dma[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
-    static const Shape bf16_any[] = {{64, 4, 0.30f, 0.32f, 3.f}, {128, 2, 0.9f, 0.9f, 4.f}};
-    static const Shape f32_dma[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 4.f}};
-    static const Shape f32_any[] = {{64, 4, 0.7f, 0.8f, 3.f}, {128, 2, 2.5f, 2.4f, 4.f}};
     const Shape *shapes = a.dtype == 1 ? (dma ? bf16_dma : bf16_any) : dma ? f32_dma : f32_any;
     const int n = a.dtype == 1 && dma ? 3 : 2;
     const int64_t ks = 128 / elem(a), steps = (a.K + ks - 1) / ks;
@@ -170,17 +173,17 @@ size_t product_workspace_bytes(const ProductArgs &a) {
     return p.total > any ? p.total : any;
 }
 
-// Lines of `length` values at ld to lines of whole pieces, the rest of the last piece zeros: both
-// operands (blockIdx.y) in one launch, a wave for each line, four pieces of a lane on their way.
+// Lines of `length` values at ld to lines of whole pieces, the rest of the last piece zeros: up to
+// three operands (blockIdx.y) in one launch, a wave for each line, four pieces of a lane on their way.
 struct Packing {
     const void *src;
     int64_t ld, lines, length;
     void *dst;
 };
 template <typename T>
-__global__ __launch_bounds__(256) void product_pack_kernel(Packing a, Packing b) {
+__global__ __launch_bounds__(256) void product_pack_kernel(Packing a, Packing b, Packing c) {
     constexpr int V = product_vec<T>(), U = 4;
-    const Packing p = blockIdx.y ? b : a;
+    const Packing p = blockIdx.y == 0 ? a : blockIdx.y == 1 ? b : c;
     const int lane = threadIdx.x % 64;
     const int64_t whole = p.length / V, pieces = (p.length + V - 1) / V;
     for (int64_t line = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; line < p.lines; line += (int64_t)gridDim.x * 4) {
@@ -203,29 +206,33 @@ __global__ __launch_bounds__(256) void product_pack_kernel(Packing a, Packing b)
     }
 }
 
+static hipError_t pack_launch(const Packing *job, int n, int64_t e, hipStream_t s) {
+    int64_t lines = 0;
+    for (int i = 0; i < n; ++i)
+        if (job[i].lines > lines) lines = job[i].lines;
+    const int64_t blocks = (lines + 3) / 4;
+    const dim3 grid((uint32_t)(blocks < 2048 ? blocks : 2048), (uint32_t)n);
+    const Packing &b = job[n > 1 ? 1 : 0], &c = job[n > 2 ? 2 : 0];
+    if (e == 2) product_pack_kernel<bf16><<<grid, 256, 0, s>>>(job[0], b, c);
+    else product_pack_kernel<float><<<grid, 256, 0, s>>>(job[0], b, c);
+    return hipGetLastError();
+}
+
 // Lays operands anew at `to`, one behind the other.
 static hipError_t pack(const Plan &p, const Lines &la, const Lines &lb, ProductArgs *a, char *to, hipStream_t s) {
     const int64_t e = elem(*a);
     Packing job[2];
     int n = 0;
-    int64_t lines = 0;
     auto add = [&](const Lines &o, Operand *op) {
         job[n++] = {op->p, o.ld, o.count, o.length, to};
         op->p = to;
         op->ld = packed_ld(o, e);
         if (o.rows) op->size = op->ld;
         to += packed_bytes(o, e);
-        if (o.count > lines) lines = o.count;
     };
     if (p.pack_a) add(la, &a->a);
     if (p.pack_b) add(lb, &a->b);
-    if (n == 0) return hipSuccess;
-    if (n == 1) job[1] = job[0];
-    const int64_t blocks = (lines + 3) / 4;
-    const dim3 grid((uint32_t)(blocks < 2048 ? blocks : 2048), (uint32_t)n);
-    if (e == 2) product_pack_kernel<bf16><<<grid, 256, 0, s>>>(job[0], job[1]);
-    else product_pack_kernel<float><<<grid, 256, 0, s>>>(job[0], job[1]);
-    return hipGetLastError();
+    return n ? pack_launch(job, n, e, s) : hipSuccess;
 }
 
 // Adds the partial results of shared tiles in their order and finishes them, V columns a thread.
@@ -294,6 +301,87 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     else r = p.dma ? launch_tiles_f32(a, p.g, s) : launch_tiles_f32_any(a, p.g, s);
     if (r != hipSuccess || p.g.rest == 0) return r;
     return a.dtype == 1 ? join<bf16>(a, p.g, s) : join<float>(a, p.g, s);
+}
+
+// A gradient's two products in one launch, where tiles of 64 are the cheapest for each and their work
+// together loads the CUs more evenly than in turn: dpre, x and the weight laid out anew once, tiles
+// whole.  Both gradients, us in turn and together: float32 1999 x 777 x 1025 98 and 80, 1024^3 45.6
+// and 35.6, bfloat16 2048 x 768 x 1024 29.6 and 19.4; long sums of few tiles stay split, by themselves:
+// bfloat16 16384 x 128 x 256 20 and 126, 4096 x 256 x 512 17.3 and 21.3.
+struct PairPlan {
+    bool pair;
+    Plan x, w;                    // of each by itself
+    ProductGrid gx, gw;
+    size_t dpre, by_x, by_w;      // bytes of the operands laid out anew
+};
+static PairPlan pair_of(const ProductArgs &x, const ProductArgs &w) {
+    PairPlan p = {};
+    p.x = plan_of(x);
+    p.w = plan_of(w);
+    const Shape &sh = (x.dtype == 1 ? bf16_dma : f32_dma)[0];
+    if (!p.x.dma || !p.w.dma || p.x.g.bm != sh.size || p.w.g.bm != sh.size || p.x.pack_a != p.w.pack_a) return p;
+    const int64_t e = elem(x), ks = 128 / e;
+    p.gx = cut(x, sh, 1);
+    p.gw = cut(w, sh, 1);
+    if ((int64_t)p.gx.full + p.gw.full > kPairTiles) return p;
+    // a CU's share of both and a part of the longer tile for the uneven end, or the longer tile alone;
+    // against both in turn and what lies between two launches (3 us)
+    const float sx = (x.K + ks - 1) / ks, sw = (w.K + ks - 1) / ks, longer = sx > sw ? sx : sw;
+    const float each = (p.gx.full * sx + p.gw.full * sw) / 256 + 0.25f * longer;
+    const float both = (each * sh.step > longer * sh.alone ? each * sh.step : longer * sh.alone) + sh.fixed;
+    p.pair = both < cost_of(x, sh, p.x.g) + cost_of(w, sh, p.w.g) + 3.f;
+    if (p.x.pack_a) p.dpre = packed_bytes(lines_of(x, false), e);
+    if (p.x.pack_b) p.by_x = packed_bytes(lines_of(x, true), e);
+    if (p.w.pack_b) p.by_w = packed_bytes(lines_of(w, true), e);
+    return p;
+}
+
+size_t product_grads_workspace_bytes(const ProductArgs &x, const ProductArgs &w) {
+    const size_t a = product_workspace_bytes(x), b = product_workspace_bytes(w);
+    const PairPlan p = pair_of(x, w);
+    const size_t both = p.pair ? p.dpre + p.by_x + p.by_w : 0;
+    return both > a && both > b ? both : a > b ? a : b;
+}
+
+hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
+    auto at16 = [](bool packed, const void *q) { return packed || ((uintptr_t)q & 15u) == 0; };
+    const PairPlan p = pair_of(x, w);
+    if (!x.y || !w.y || !p.pair || !at16(p.x.pack_a, x.a.p) || !at16(p.x.pack_b, x.b.p) || !at16(p.w.pack_b, w.b.p)) {
+        const hipError_t r = x.y ? launch_product(x, s) : hipSuccess;
+        return r == hipSuccess && w.y ? launch_product(w, s) : r;
+    }
+    ProductArgs ax = x, aw = w;
+    const int64_t e = elem(x);
+    const Lines ld = lines_of(w, false), lx = lines_of(x, true), lw = lines_of(w, true);    // of dpre, the weight and x
+    aw.a.size = ld.length;
+    ax.b.size = lx.length;
+    aw.b.size = lw.length;
+    Packing job[3];
+    int n = 0;
+    char *to = reinterpret_cast<char *>(x.part);
+    auto add = [&](const Lines &o, Operand *op) {
+        job[n++] = {op->p, o.ld, o.count, o.length, to};
+        op->p = to;
+        op->ld = op->size = packed_ld(o, e);
+        to += packed_bytes(o, e);
+    };
+    if (p.x.pack_a) {
+        add(ld, &aw.a);
+        ax.a.p = aw.a.p;
+        ax.a.ld = aw.a.ld;
+    }
+    if (p.x.pack_b) add(lx, &ax.b);
+    if (p.w.pack_b) add(lw, &aw.b);
+    if (n) {
+        const hipError_t r = pack_launch(job, n, e, s);
+        if (r != hipSuccess) return r;
+    }
+    // one line of k has no stride of its own; lines past K lie past it
+    if (ld.count == 1 && aw.a.ld < aw.a.size) aw.a.ld = aw.a.size;
+    if (lx.count == 1 && ax.b.ld < ax.b.size) ax.b.ld = ax.b.size;
+    if (lw.count == 1 && aw.b.ld < aw.b.size) aw.b.ld = aw.b.size;
+    const bool x_first = x.K >= w.K;                            // the longer tiles first
+    return x.dtype == 1 ? launch_pair_bf16(ax, p.gx, aw, p.gw, x_first, s) : launch_pair_f32(ax, p.gx, aw, p.gw, x_first, s);
 }
 
 }  // namespace ssd

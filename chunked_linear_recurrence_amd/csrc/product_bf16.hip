@@ -9,4 +9,9 @@ hipError_t launch_tiles_bf16(const ProductArgs &a, const ProductGrid &g, hipStre
     return launch_tiles_of<bf16, 64, 64, 2, 2, true>(a, g, s);
 }
 
+hipError_t launch_pair_bf16(const ProductArgs &x, const ProductGrid &gx, const ProductArgs &w, const ProductGrid &gw,
+                          bool x_first, hipStream_t s) {
+    return launch_pair_of<bf16>(x, gx, w, gw, x_first, s);
+}
+
 }  // namespace ssd

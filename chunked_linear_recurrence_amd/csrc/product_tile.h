@@ -159,9 +159,8 @@ __device__ __forceinline__ int xcd_order(int i, int n) {
     return x * per + min(x, more) + i / 8;
 }
 
-__device__ __forceinline__ Work work_of(const ProductGrid &g, int64_t steps) {
+__device__ __forceinline__ Work work_of(const ProductGrid &g, int id, int64_t steps) {
     Work w;
-    int id = blockIdx.x;
     if (id < g.full) {
         id = xcd_order(id, g.full);
         w.first = 0;
@@ -180,20 +179,20 @@ __device__ __forceinline__ Work work_of(const ProductGrid &g, int64_t steps) {
     return w;
 }
 
+// The work of workgroup `block` of a product's grid, in LDS of the kernel's.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductArgs p, Epilogue ep, ProductGrid grid) {
+__device__ __forceinline__ void product_tile(const ProductArgs &p, const Epilogue &ep, const ProductGrid &grid, int block,
+                                             unsigned char *A0, unsigned char *B0, unsigned char *A1, unsigned char *B1,
+                                             unsigned char *unread) {
     typedef typename C::T T;
     typedef typename Frag<T>::type F;
     typedef typename C::LA LA;
     typedef typename C::LB LB;
     constexpr int E = (int)sizeof(T), V = 16 / E;
-    __shared__ __align__(16) unsigned char A0[LA::BYTES], B0[LB::BYTES], A1[LA::BYTES], B1[LB::BYTES];
-    __shared__ __align__(16) unsigned char unread[C::TOUCH ? C::NW * 256 : 16];      // what touched lines leave
-
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
     const int64_t all = (p.K + C::KS - 1) / C::KS;
-    const Work work = work_of(grid, all);
+    const Work work = work_of(grid, block, all);
     const int64_t m0 = (int64_t)work.m * C::BM, n0 = (int64_t)work.n * C::BCOLS;
     const int steps = work.steps;
     const int64_t k_first = work.first * C::KS;
@@ -503,6 +502,24 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductAr
 }
 
 template <class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES) void product_kernel(ProductArgs p, Epilogue ep, ProductGrid grid) {
+    __shared__ __align__(16) unsigned char A0[C::LA::BYTES], B0[C::LB::BYTES], A1[C::LA::BYTES], B1[C::LB::BYTES];
+    __shared__ __align__(16) unsigned char unread[C::TOUCH ? C::NW * 256 : 16];      // what touched lines leave
+    product_tile<C>(p, ep, grid, blockIdx.x, A0, B0, A1, B1, unread);
+}
+
+// Two products whose tiles lie in LDS alike: the first's workgroups, then the second's.
+template <class C, class D>
+__global__ __launch_bounds__(C::THREADS, C::WAVES) void product_pair_kernel(ProductArgs p, Epilogue pe, ProductGrid pg,
+                                                                           ProductArgs q, Epilogue qe, ProductGrid qg) {
+    static_assert(C::LA::BYTES == D::LA::BYTES && C::LB::BYTES == D::LB::BYTES && C::THREADS == D::THREADS && !C::TOUCH &&
+                  !D::TOUCH, "tiles alike");
+    __shared__ __align__(16) unsigned char A0[C::LA::BYTES], B0[C::LB::BYTES], A1[C::LA::BYTES], B1[C::LB::BYTES];
+    if ((int)blockIdx.x < pg.full) product_tile<C>(p, pe, pg, blockIdx.x, A0, B0, A1, B1, nullptr);
+    else product_tile<D>(q, qe, qg, blockIdx.x - pg.full, A0, B0, A1, B1, nullptr);
+}
+
+template <class C>
 hipError_t launch_tiles(const ProductArgs &a, const ProductGrid &g, hipStream_t s) {
     product_kernel<C><<<(uint32_t)(g.full + g.rest * g.splits), C::THREADS, 0, s>>>(a, epilogue_of(a), g);
     return hipGetLastError();
@@ -516,6 +533,18 @@ hipError_t launch_tiles_of(const ProductArgs &a, const ProductGrid &g, hipStream
     if (a.kind == kLinear) return launch_tiles<ProductCfg<T, BM, BN, WM, WN, false, false, DMA, kLinear>>(a, g, s);
     if (a.a_rows) return launch_tiles<ProductCfg<T, BM, BN, WM, WN, true, true, DMA, kPlain>>(a, g, s);
     return launch_tiles<ProductCfg<T, BM, BN, WM, WN, false, true, DMA, kPlain>>(a, g, s);
+}
+
+// The launch of both gradients' products, by x and by a weight, in tiles of 64; whole tiles only.
+template <typename T>
+hipError_t launch_pair_of(const ProductArgs &x, const ProductGrid &gx, const ProductArgs &w, const ProductGrid &gw,
+                          bool x_first, hipStream_t s) {
+    typedef ProductCfg<T, 64, 64, 2, 2, false, true, true, kPlain> X;
+    typedef ProductCfg<T, 64, 64, 2, 2, true, true, true, kPlain> W;
+    const uint32_t n = (uint32_t)(gx.full + gw.full);
+    if (x_first) product_pair_kernel<X, W><<<n, X::THREADS, 0, s>>>(x, epilogue_of(x), gx, w, epilogue_of(w), gw);
+    else product_pair_kernel<W, X><<<n, X::THREADS, 0, s>>>(w, epilogue_of(w), gw, x, epilogue_of(x), gx);
+    return hipGetLastError();
 }
 
 }  // namespace ssd

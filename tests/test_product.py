@@ -197,3 +197,20 @@ def test_calls_repeat_bit_for_bit():
         for _ in range(3):
             c = ssd.linear_fwd(x, w, b, r), *ssd.linear_bwd(dy, x, w, b)
             assert all(torch.equal(p, q) for p, q in zip(a, c))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(256, 256, 256), (640, 333, 517), (1024, 520, 264), (77, 1000, 1040), (900, 70, 1999)], ids=str)
+def test_both_gradients_are_those_of_each_alone(shape, dtype):
+    """Whether one launch takes both products or one each; with dy and x off 16 bytes too."""
+    m, k, n = shape
+    x, w, b, _, dy = make(m, k, n, dtype, 6)
+    X, W, B, G = dev(x, w, b, dy)
+    off = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+    for xs, gs in ((X, G), (off(X), G), (X, off(G))):
+        both = ssd.linear_bwd(gs, xs, W, B)
+        x_alone = ssd.linear_bwd(gs, xs, W, B, need=(True, False, False)).dx
+        w_alone = ssd.linear_bwd(gs, xs, W, B, need=(False, True, False)).dweight
+        y = ssd.linear_fwd(xs, W, B)
+        R.check_linear(dtype, (y, None) + both, x, w, b, None, None, dy)
+        R.check_linear(dtype, (y, None, x_alone, w_alone, both.dbias), x, w, b, None, None, dy)
