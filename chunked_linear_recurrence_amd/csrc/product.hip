@@ -125,22 +125,26 @@ struct Plan {
     bool dma, pack_a, pack_b;
     ProductGrid g;
     size_t part, total;           // the partial results' place in the workspace (packed operands first), its bytes
+    float cost;
 };
+static float packing_cost(size_t bytes) { return bytes ? 6.f + bytes * 6e-7f : 0.f; }
 static size_t part_bytes(const ProductGrid &g) { return (size_t)part_floats(g) * 4; }
 
 static Plan plan_of(const ProductArgs &a) {
     const int64_t e = elem(a);
     const Lines la = lines_of(a, false), lb = lines_of(a, true);
-    Plan p = {true, !direct(la, e), !direct(lb, e), {}, 0, 0};
-    float fast, any;
-    p.g = grid_of(a, true, &fast);
+    Plan p = {true, !direct(la, e), !direct(lb, e), {}, 0, 0, 0.f};
+    float any;
+    p.g = grid_of(a, true, &p.cost);
     if (p.pack_a || p.pack_b) {
         const ProductGrid g = grid_of(a, false, &any);
         const size_t bytes = (p.pack_a ? packed_bytes(la, e) : 0) + (p.pack_b ? packed_bytes(lb, e) : 0);
         const bool can = (!p.pack_a || can_pack(la, e)) && (!p.pack_b || can_pack(lb, e));
-        if (can && fast + 6.f + bytes * 6e-7f < any) {
+        if (can && p.cost + packing_cost(bytes) < any) {
             p.part = bytes;
+            p.cost += packing_cost(bytes);
         } else {
+            p.cost = any;
             p.dma = p.pack_a = p.pack_b = false;
             p.g = g;
         }
@@ -288,7 +292,7 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     auto at16 = [](const void *q) { return ((uintptr_t)q & 15u) == 0; };
     if (p.dma && ((!p.pack_a && !at16(a.a.p)) || (!p.pack_b && !at16(a.b.p)))) {
         float cost;
-        p = {false, false, false, grid_of(a, false, &cost), 0, 0};
+        p = {false, false, false, grid_of(a, false, &cost), 0, 0, cost};
     }
     char *ws = reinterpret_cast<char *>(a.part);
     hipError_t r = pack(p, la, lb, &a, ws, s);
@@ -303,24 +307,28 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     return a.dtype == 1 ? join<bf16>(a, p.g, s) : join<float>(a, p.g, s);
 }
 
-// A gradient's two products in one launch, where tiles of 64 are the cheapest for each and their work
-// together loads the CUs more evenly than in turn: dpre, x and the weight laid out anew once, tiles
+// A gradient's two products in one launch, where tiles of 64 suit each and their work together loads the CUs more evenly than in turn: dpre, x and the weight laid out anew once, tiles
 // whole.  Both gradients, us in turn and together: float32 1999 x 777 x 1025 98 and 80, 1024^3 45.6
-// and 35.6, bfloat16 2048 x 768 x 1024 29.6 and 19.4; long sums of few tiles stay split, by themselves:
+// and 35.6, bfloat16 2048 x 768 x 1024 29.6 and 19.4, 3000 x 300 x 2000 54 and 33; long sums of few tiles stay split, by themselves:
 // bfloat16 16384 x 128 x 256 20 and 126, 4096 x 256 x 512 17.3 and 21.3.
 struct PairPlan {
-    bool pair;
-    Plan x, w;                    // of each by itself
+    bool pair, pack_d, pack_x, pack_w;       // dpre, x and the weight are laid out anew
     ProductGrid gx, gw;
-    size_t dpre, by_x, by_w;      // bytes of the operands laid out anew
+    size_t bytes;
 };
 static PairPlan pair_of(const ProductArgs &x, const ProductArgs &w) {
     PairPlan p = {};
-    p.x = plan_of(x);
-    p.w = plan_of(w);
     const Shape &sh = (x.dtype == 1 ? bf16_dma : f32_dma)[0];
-    if (!p.x.dma || !p.w.dma || p.x.g.bm != sh.size || p.w.g.bm != sh.size || p.x.pack_a != p.w.pack_a) return p;
     const int64_t e = elem(x), ks = 128 / e;
+    const Plan by_x = plan_of(x), by_w = plan_of(w);
+    if ((by_x.dma && by_x.g.bm != sh.size) || (by_w.dma && by_w.g.bm != sh.size)) return p;
+    const Lines dx = lines_of(x, false), dw = lines_of(w, false), lw = lines_of(x, true), lx = lines_of(w, true);
+    p.pack_d = !direct(dx, e) || !direct(dw, e);
+    p.pack_w = !direct(lw, e);
+    p.pack_x = !direct(lx, e);
+    if ((p.pack_d && !(can_pack(dx, e) && can_pack(dw, e))) || (p.pack_w && !can_pack(lw, e)) || (p.pack_x && !can_pack(lx, e)))
+        return p;
+    p.bytes = (p.pack_d ? packed_bytes(dw, e) : 0) + (p.pack_w ? packed_bytes(lw, e) : 0) + (p.pack_x ? packed_bytes(lx, e) : 0);
     p.gx = cut(x, sh, 1);
     p.gw = cut(w, sh, 1);
     if ((int64_t)p.gx.full + p.gw.full > kPairTiles) return p;
@@ -329,33 +337,30 @@ static PairPlan pair_of(const ProductArgs &x, const ProductArgs &w) {
     const float sx = (x.K + ks - 1) / ks, sw = (w.K + ks - 1) / ks, longer = sx > sw ? sx : sw;
     const float each = (p.gx.full * sx + p.gw.full * sw) / 256 + 0.25f * longer;
     const float both = (each * sh.step > longer * sh.alone ? each * sh.step : longer * sh.alone) + sh.fixed;
-    p.pair = both < cost_of(x, sh, p.x.g) + cost_of(w, sh, p.w.g) + 3.f;
-    if (p.x.pack_a) p.dpre = packed_bytes(lines_of(x, false), e);
-    if (p.x.pack_b) p.by_x = packed_bytes(lines_of(x, true), e);
-    if (p.w.pack_b) p.by_w = packed_bytes(lines_of(w, true), e);
+    p.pair = both + packing_cost(p.bytes) < by_x.cost + by_w.cost + 3.f;
     return p;
 }
 
 size_t product_grads_workspace_bytes(const ProductArgs &x, const ProductArgs &w) {
     const size_t a = product_workspace_bytes(x), b = product_workspace_bytes(w);
     const PairPlan p = pair_of(x, w);
-    const size_t both = p.pair ? p.dpre + p.by_x + p.by_w : 0;
+    const size_t both = p.pair ? p.bytes : 0;
     return both > a && both > b ? both : a > b ? a : b;
 }
 
 hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
     auto at16 = [](bool packed, const void *q) { return packed || ((uintptr_t)q & 15u) == 0; };
     const PairPlan p = pair_of(x, w);
-    if (!x.y || !w.y || !p.pair || !at16(p.x.pack_a, x.a.p) || !at16(p.x.pack_b, x.b.p) || !at16(p.w.pack_b, w.b.p)) {
+    if (!x.y || !w.y || !p.pair || !at16(p.pack_d, x.a.p) || !at16(p.pack_w, x.b.p) || !at16(p.pack_x, w.b.p)) {
         const hipError_t r = x.y ? launch_product(x, s) : hipSuccess;
         return r == hipSuccess && w.y ? launch_product(w, s) : r;
     }
     ProductArgs ax = x, aw = w;
     const int64_t e = elem(x);
-    const Lines ld = lines_of(w, false), lx = lines_of(x, true), lw = lines_of(w, true);    // of dpre, the weight and x
+    const Lines ld = lines_of(w, false), lw = lines_of(x, true), lx = lines_of(w, true);
     aw.a.size = ld.length;
-    ax.b.size = lx.length;
-    aw.b.size = lw.length;
+    ax.b.size = lw.length;
+    aw.b.size = lx.length;
     Packing job[3];
     int n = 0;
     char *to = reinterpret_cast<char *>(x.part);
@@ -365,21 +370,21 @@ hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipS
         op->ld = op->size = packed_ld(o, e);
         to += packed_bytes(o, e);
     };
-    if (p.x.pack_a) {
+    if (p.pack_d) {
         add(ld, &aw.a);
         ax.a.p = aw.a.p;
         ax.a.ld = aw.a.ld;
     }
-    if (p.x.pack_b) add(lx, &ax.b);
-    if (p.w.pack_b) add(lw, &aw.b);
+    if (p.pack_w) add(lw, &ax.b);
+    if (p.pack_x) add(lx, &aw.b);
     if (n) {
         const hipError_t r = pack_launch(job, n, e, s);
         if (r != hipSuccess) return r;
     }
     // one line of k has no stride of its own; lines past K lie past it
     if (ld.count == 1 && aw.a.ld < aw.a.size) aw.a.ld = aw.a.size;
-    if (lx.count == 1 && ax.b.ld < ax.b.size) ax.b.ld = ax.b.size;
-    if (lw.count == 1 && aw.b.ld < aw.b.size) aw.b.ld = aw.b.size;
+    if (lw.count == 1 && ax.b.ld < ax.b.size) ax.b.ld = ax.b.size;
+    if (lx.count == 1 && aw.b.ld < aw.b.size) aw.b.ld = aw.b.size;
     const bool x_first = x.K >= w.K;                            // the longer tiles first
     return x.dtype == 1 ? launch_pair_bf16(ax, p.gx, aw, p.gw, x_first, s) : launch_pair_f32(ax, p.gx, aw, p.gw, x_first, s);
 }

@@ -949,7 +949,8 @@ def linear_bwd(dy, x, weight, bias=None, pre=None, *, act=None, need=(True, True
     """Gradients of linear_fwd (ssd_linear_bwd) from dy [M, N], with the pre of a
     linear_fwd(keep=True) on the same arguments where there is an activation.  need: which of
     dx, dweight and dbias are wanted (the others are None, as dbias is where the forward had
-    no bias).  The residual's gradient is dy itself."""
+    no bias); sums may be cut differently for one of dx and dweight than for both, in their last
+    bits.  The residual's gradient is dy itself."""
     return _product_bwd("ssd_linear_bwd", False, dy, x, weight, bias, pre, act, need, workspace, stream)
 
 
