@@ -153,7 +153,7 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
 // Up to 32 rows; up to 48 of a weight of many rows, which workgroups take 32 at a time; up to 64 of a
 // small weight: beyond, tiles share x's reads, which here every workgroup makes for itself.  In
 // bfloat16, here and in tiles: 32 rows of 4096 x 4096 12.8 us and 13.8, 64 rows 21.7 and 13.9; 48
-// rows of 2048 x (2 x 5632) 16.2 and 19.6, 64 rows 19.6 and 19.9; 64 rows of 1536 x 768 8.9 and 11.3.
+// rows of 2048 x (2 x 5632) 15.5 and 19.6, 64 rows 19.6 and 19.9; 64 rows of 1536 x 768 8.9 and 11.3.
 bool product_few_rows(const ProductArgs &a) {
     if (a.a_rows || a.b_rows) return false;
     return a.M <= SSD_PRODUCT_FEW_ROWS || (a.M <= 48 && a.N > 4096) ||
@@ -161,14 +161,15 @@ bool product_few_rows(const ProductArgs &a) {
 }
 
 // 16 rows of the weight a workgroup and up to 16 waves for them while that leaves CUs idle, else 32
-// rows and 4 waves, which halves the reads of x: 32 rows of 2048 x (2 x 5632) 16.8 us with 16 and
-// 13.5 with 32, one row 10.6 and 10.4.
+// rows, which halves the reads of x, and 4 waves, 8 for 33 to 48 rows: 32 rows of 2048 x (2 x 5632)
+// 16.8 us with 16 and 13.5 with 32, one row 10.6 and 10.4, 48 rows 21.1 with 16, 16.2 with 32 and 4
+// waves, 15.5 with 8.
 template <typename T, ProductKind KIND, int MT>
 static hipError_t rows_launch(const ProductArgs &a, hipStream_t s) {
     const Epilogue ep = epilogue_of(a);
-    constexpr int WAVES = MT == 1 ? 16 : MT == 2 ? 8 : 4;
+    constexpr int WAVES = MT == 1 ? 16 : MT == 2 ? 8 : 4, WIDE = MT == 3 ? 8 : 4;
     if (a.N <= 4096) product_rows_kernel<T, KIND, MT, 1, WAVES><<<(uint32_t)((a.N + 15) / 16), 64 * WAVES, 0, s>>>(a, ep);
-    else product_rows_kernel<T, KIND, MT, 2, 4><<<(uint32_t)((a.N + 31) / 32), 256, 0, s>>>(a, ep);
+    else product_rows_kernel<T, KIND, MT, 2, WIDE><<<(uint32_t)((a.N + 31) / 32), 64 * WIDE, 0, s>>>(a, ep);
     return hipGetLastError();
 }
 
