@@ -100,12 +100,14 @@ static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
         // workgroup, as many as it holds, or half of that
         const ProductGrid whole = cut(a, shapes[i], 1);
         const int rest = (whole.full + whole.rest) % 256;
-        int64_t most = steps / kSplitSteps < kMostSplits ? steps / kSplitSteps : kMostSplits;
+        const int64_t by_steps = steps / kSplitSteps, most = by_steps < 1 ? 1 : by_steps < kMostSplits ? by_steps : kMostSplits;
         const int64_t one = rest ? 256 / rest : 1, all = rest ? shapes[i].slots() / rest : 1;
+        int64_t tried = 0;
         for (int64_t want : {(int64_t)1, one, (all + 1) / 2, all}) {
             const int64_t splits = want < most ? want : most;
-            if (splits < 1) continue;
-            const ProductGrid g = cut(a, shapes[i], splits);
+            if (splits == tried) continue;
+            tried = splits;
+            const ProductGrid g = splits == 1 ? whole : cut(a, shapes[i], splits);
             const float t = cost_of(a, shapes[i], g);
             if (t < least) {
                 least = t;
@@ -168,14 +170,13 @@ bool product_fits(const ProductArgs &a) {
 
 // Tensors may start off 16 bytes, which their sizes do not tell: the product then runs from any
 // address.
-size_t product_workspace_bytes(const ProductArgs &a) {
-    if (product_few_rows(a)) return 0;
-    const Plan p = plan_of(a);
+static size_t bytes_of(const ProductArgs &a, const Plan &p) {
     if (!p.dma) return p.total;
     float cost;
     const size_t any = part_bytes(grid_of(a, false, &cost));
     return p.total > any ? p.total : any;
 }
+size_t product_workspace_bytes(const ProductArgs &a) { return product_few_rows(a) ? 0 : bytes_of(a, plan_of(a)); }
 
 // Lines of `length` values at ld to lines of whole pieces, the rest of the last piece zeros: up to
 // three operands (blockIdx.y) in one launch, a wave for each line, four pieces of a lane on their way.
@@ -316,11 +317,10 @@ struct PairPlan {
     ProductGrid gx, gw;
     size_t bytes;
 };
-static PairPlan pair_of(const ProductArgs &x, const ProductArgs &w) {
+static PairPlan pair_of(const ProductArgs &x, const ProductArgs &w, const Plan &by_x, const Plan &by_w) {
     PairPlan p = {};
     const Shape &sh = (x.dtype == 1 ? bf16_dma : f32_dma)[0];
     const int64_t e = elem(x), ks = 128 / e;
-    const Plan by_x = plan_of(x), by_w = plan_of(w);
     if ((by_x.dma && by_x.g.bm != sh.size) || (by_w.dma && by_w.g.bm != sh.size)) return p;
     const Lines dx = lines_of(x, false), dw = lines_of(w, false), lw = lines_of(x, true), lx = lines_of(w, true);
     p.pack_d = !direct(dx, e) || !direct(dw, e);
@@ -342,16 +342,17 @@ static PairPlan pair_of(const ProductArgs &x, const ProductArgs &w) {
 }
 
 size_t product_grads_workspace_bytes(const ProductArgs &x, const ProductArgs &w) {
-    const size_t a = product_workspace_bytes(x), b = product_workspace_bytes(w);
-    const PairPlan p = pair_of(x, w);
+    const Plan by_x = plan_of(x), by_w = plan_of(w);
+    const size_t a = bytes_of(x, by_x), b = bytes_of(w, by_w);
+    const PairPlan p = pair_of(x, w, by_x, by_w);
     const size_t both = p.pair ? p.bytes : 0;
     return both > a && both > b ? both : a > b ? a : b;
 }
 
 hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
     auto at16 = [](bool packed, const void *q) { return packed || ((uintptr_t)q & 15u) == 0; };
-    const PairPlan p = pair_of(x, w);
-    if (!x.y || !w.y || !p.pair || !at16(p.pack_d, x.a.p) || !at16(p.pack_w, x.b.p) || !at16(p.pack_x, w.b.p)) {
+    const PairPlan p = x.y && w.y ? pair_of(x, w, plan_of(x), plan_of(w)) : PairPlan{};
+    if (!p.pair || !at16(p.pack_d, x.a.p) || !at16(p.pack_w, x.b.p) || !at16(p.pack_x, w.b.p)) {
         const hipError_t r = x.y ? launch_product(x, s) : hipSuccess;
         return r == hipSuccess && w.y ? launch_product(w, s) : r;
     }
