@@ -45,8 +45,8 @@ struct Shape {
 // For operands copied to LDS directly and for those from any address
 constexpr Shape bf16_dma[] = {{64, 4, 0.30f, 0.22f, 3.f}, {128, 2, 0.58f, 0.60f, 4.f}, {256, 1, 1.7f, 1.7f, 6.f}};
 constexpr Shape bf16_any[] = {{64, 4, 0.30f, 0.32f, 3.f}, {128, 2, 0.9f, 0.9f, 4.f}};
-constexpr Shape f32_dma[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 4.f}};
-constexpr Shape f32_any[] = {{64, 4, 0.7f, 0.8f, 3.f}, {128, 2, 2.5f, 2.4f, 4.f}};
+constexpr Shape f32_dma[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 14.f}};
+constexpr Shape f32_any[] = {{64, 4, 0.7f, 0.8f, 3.f}, {128, 2, 2.5f, 2.4f, 14.f}};
 constexpr int kPairTiles = 1 << 20;                     // of two products in one launch, well within a grid's range
 
 // A split's partial results (64 KB of a tile of 128, written and read again) have to be fewer than what
@@ -88,7 +88,8 @@ static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g
 // The cheapest way to cut a product, by its sizes and type alone.  Small tiles give every CU work,
 // large ones read less from LDS and the caches for each product: us in tiles of 64, 128 and 256,
 // bfloat16, 512 x 2048 x 2048 13.5, 23.3, 32.9; 2048 x 2048 x 4096 55.9, 40.0, 49.3; 4096^3 189, 134,
-// 109; float32 512 x 1024 x 1024 16.8, 29.2 (whole tiles of 64: 21.6).
+// 109; float32 512 x 1024 x 1024 16.8, 29.2 (whole tiles of 64: 21.6), 8192 x 64 x 2048 36, 67, 8192 x
+// 256 x 4096 144, 175 (a tile of 128 alone stores for 14 us).
 static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
     const Shape *shapes = a.dtype == 1 ? (dma ? bf16_dma : bf16_any) : dma ? f32_dma : f32_any;
     const int n = a.dtype == 1 && dma ? 3 : 2;
