@@ -6,7 +6,11 @@
 //     plain    c = A B^T
 //
 // Every sum over k is held in float32 in the matrix units' accumulators; results are rounded
-// once, when they are stored.
+// once, when they are stored.  pre, which a backward takes, is rounded to the activations' type as
+// they are, and so is the gradient by it before its two products: in bfloat16 three roundings lie
+// between the inputs and a gradient, 0.0030 of relative error in the 2-norm for the gradients of
+// 8192 x 2048 x (2 x 5632) where the last one alone leaves 0.0017.  pre in float32 would leave 0.0024
+// and take 74 us (7%) more there; the matrix units take no float32 gradient at that rate.
 #pragma once
 
 #include "ssd_block.h"
