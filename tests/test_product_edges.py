@@ -1,5 +1,9 @@
 """The products where they are cut, joined and laid out in each of their ways: the same bits at every
-call."""
+call, and what is not finite.
+
+A row of x (or of dy) is a row of the result, so nothing of one row may reach another: not by the
+rows that a tile repeats past the last one, nor by the values beside a row's last ones, nor by
+zeros past K.  Results of clean rows have to be the same bits with and without it."""
 import pytest
 import torch
 
@@ -8,6 +12,7 @@ from chunked_linear_recurrence_amd import ssd
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 DTYPES = [torch.float32, torch.bfloat16]
+INF, NAN = float("inf"), float("nan")
 
 # rows, inner, outer, and what the forward's workspace shows of its path: more than nothing where K is
 # split, both operands where they are laid out anew, less than that where they pass through registers
@@ -53,3 +58,76 @@ def test_gated_calls_repeat_bit_for_bit(path, dtype):
         got = (h, pre) + ssd.gated_bwd(dh, x, w, b, pre)
         first = first or got
         assert all(torch.equal(p, q) for p, q in zip(first, got))
+
+
+def bad_rows(t):
+    """The same with infinities of both signs in a row and a NaN at the end of the last one; the others."""
+    m, k = t.shape
+    t = t.clone()
+    t[m // 2, 3], t[m // 2, k - 1], t[m - 1, k - 1] = INF, -INF, NAN
+    rows = torch.ones(m, dtype=torch.bool, device=DEV)
+    rows[[m // 2, m - 1]] = False
+    return t, rows
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("path", PATHS)
+def test_a_row_stays_in_its_row_forward(path, dtype):
+    m, k, n, kind = PATHS[path]
+    x, w, b, r, _ = make(m, k, n, dtype, 1)
+    check_path(m, k, n, dtype, kind, False)
+    x2, rows = bad_rows(x)
+    for act in (None, "silu"):
+        clean, got = (ssd.linear_fwd(v, w, b, r, act=act) for v in (x, x2))
+        assert torch.equal(got[rows], clean[rows])
+        assert got[m - 1].isnan().all()
+    f = n // 2
+    check_path(m, k, f, dtype, None, True)
+    clean, got = (ssd.gated_fwd(v, w[:2 * f], b[:2 * f]) for v in (x, x2))
+    assert torch.equal(got[rows], clean[rows])
+    assert got[m - 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("path", PATHS)
+def test_a_row_stays_in_its_row_by_x(path, act, dtype):
+    """dx: a row of dy is a row of dx; the sums run over the outer dimension."""
+    m, n, k, _ = PATHS[path]                           # the path's K is what dx sums over
+    x, w, b, _, dy = make(m, k, n, dtype, 2)
+    _, pre = ssd.linear_fwd(x, w, b, act=act, keep=True)
+    dy2, rows = bad_rows(dy)
+    for need in ((True, False, False), (True, True, True)):
+        clean, got = (ssd.linear_bwd(v, x, w, b, pre, act=act, need=need).dx for v in (dy, dy2))
+        assert torch.equal(got[rows], clean[rows])
+        assert got[m - 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("path", PATHS)
+def test_a_column_stays_in_its_column_by_the_weight(path, act, dtype):
+    """dweight sums over the rows: a column of dy is a row of it, a column of x a column."""
+    n, m, k, _ = PATHS[path]                           # the path's K is the rows here
+    x, w, b, _, dy = make(m, k, n, dtype, 3)
+    _, pre = ssd.linear_fwd(x, w, b, act=act, keep=True)
+    dyt, rows = bad_rows(dy.t().contiguous())
+    xt, cols = bad_rows(x.t().contiguous())
+    dy2, x2 = dyt.t().contiguous(), xt.t().contiguous()
+    for need in ((False, True, False), (True, True, True)):
+        clean = ssd.linear_bwd(dy, x, w, b, pre, act=act, need=need).dweight
+        got = ssd.linear_bwd(dy2, x, w, b, pre, act=act, need=need).dweight
+        assert torch.equal(got[rows], clean[rows]) and got[n - 1].isnan().all()
+        got = ssd.linear_bwd(dy, x2, w, b, pre, act=act, need=need).dweight
+        assert torch.equal(got[:, cols], clean[:, cols]) and got[:, k - 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_gated_row_stays_in_its_row_backward(dtype):
+    for m, k, f in ((130, 200, 264), (150, 131, 35), (1500, 1001, 602)):
+        x, w, b, _, _ = make(m, k, 2 * f, dtype, 4)
+        dh = make(m, 1, f, dtype, 5)[4]
+        _, pre = ssd.gated_fwd(x, w, b, keep=True)
+        dh2, rows = bad_rows(dh)
+        clean, got = (ssd.gated_bwd(v, x, w, b, pre).dx for v in (dh, dh2))
+        assert torch.equal(got[rows], clean[rows]) and got[m - 1].isnan().all()
