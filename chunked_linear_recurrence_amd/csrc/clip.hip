@@ -8,9 +8,10 @@
 // workgroup takes one chunk of one tensor.  Squares are summed in float64, in which no float32
 // value's square overflows or vanishes; every workgroup of the second pass adds the chunks'
 // sums in the same order, so it needs no third launch and results do not change from call to
-// call.  A norm that is not finite changes no element.  Bound by memory: the second pass takes the
-// chunks from the last to the first, which the last-level cache still holds: 322 MB of bfloat16 and
-// float32 in 160 us (6.0 TB/s; in the norm's order 171), 78 of them for the norm.
+// call.  A norm that is not finite as it is returned, in float32, changes no element.  Bound by
+// memory: the second pass takes the chunks from the last to the first, which the last-level cache
+// still holds: 322 MB of bfloat16 and float32 in 160 us (6.0 TB/s; in the norm's order 171), 78 of
+// them for the norm.
 #include "clip.h"
 
 #include <type_traits>
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipBatch b, i
     const ClipChunk c = clip_chunk(b, chunk, gridDim.x - 1 - blockIdx.x);
     const void *src = b.in[c.tensor];
     void *dst = b.out[c.tensor];
-    const bool clips = total > max_norm && total <= 1.7976931348623157e308;
+    const bool clips = total > max_norm && (float)total <= 3.40282347e38f;
     if (!clips && src == dst) return;
     const float factor = clips ? (float)(max_norm / total) : 1.f;
     if (b.wide(c.tensor))

@@ -1140,7 +1140,7 @@ def grad_norm(tensors, *, workspace=None, stream=None):
 
 def clip_grads(tensors, max_norm, *, out=None, workspace=None, stream=None):
     """Scales the tensors by min(1, max_norm / norm), norm as grad_norm's (ssd_clip), in place or
-    into `out` (tensors of the same shapes and dtypes).  A norm that is not finite leaves the
-    values as they are.  Returns the norm (of the values before), a float32 scalar on their
-    device; nothing waits for it."""
+    into `out` (tensors of the same shapes and dtypes).  A norm that is not finite as it is
+    returned leaves the values as they are.  Returns the norm (of the values before), a float32
+    scalar on their device; nothing waits for it."""
     return _clip(tensors, max_norm, out, True, workspace, stream)

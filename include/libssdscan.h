@@ -481,11 +481,11 @@ ssd_status_t ssd_residual_norm_bwd(const ssd_residual_norm_dims_t *dims, const v
 
 /* norm = sqrt of the sum of the squares of every element of `count` tensors (host arrays of
  * device pointers, element counts >= 0 and ssd_dtype_t), in float64 until it is stored, and
- * out[i] = in[i] min(1, max_norm / norm).  Where norm is not finite, and where it does not exceed
- * max_norm, values are left as they are.  in[i] and out[i] are the same pointer (clipped in
- * place) or do not overlap; out may be NULL (the norm alone; max_norm is then not looked at).
- * norm [1] float32 on the device.  max_norm >= 0, infinity included.  The host arrays are read
- * before the call returns. */
+ * out[i] = in[i] min(1, max_norm / norm).  Where norm is not finite as it is stored (beyond float32
+ * it is infinite there), and where it does not exceed max_norm, values are left as they are.
+ * in[i] and out[i] are the same pointer (clipped in place) or do not overlap; out may be NULL (the
+ * norm alone; max_norm is then not looked at).  norm [1] float32 on the device.  max_norm >= 0,
+ * infinity included.  The host arrays are read before the call returns. */
 size_t ssd_clip_workspace_bytes(int32_t count, const int64_t *sizes);
 ssd_status_t ssd_clip(int32_t count, const void *const *in, void *const *out, const int64_t *sizes,
                       const int32_t *dtypes, double max_norm, float *norm, void *workspace, size_t workspace_bytes,
