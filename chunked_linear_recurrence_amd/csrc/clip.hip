@@ -82,16 +82,28 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(ClipBatch b, in
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-template <typename T>
-__device__ __forceinline__ void scaled(const T *src, T *dst, int64_t n, float factor) {
+// F: the factor's type.  A factor below float32's normal numbers has too few bits there, and its
+// products with large elements are ordinary numbers: float64 takes it.
+template <typename T, typename F>
+__device__ __forceinline__ void scaled(const T *src, T *dst, int64_t n, F factor) {
     each(src, n, aligned_from(src, dst, n), [&](const T *q, auto width) {
         constexpr int V = decltype(width)::value;
         float v[V];
         unpack<T, V>(load_pack<T, V>(q), v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= factor;
+        for (int i = 0; i < V; ++i) v[i] = (float)(v[i] * factor);
         store_f32<T, V>(dst + (q - src), v);
     });
+}
+
+template <typename F>
+__device__ __forceinline__ void scaled(const ClipBatch &b, const ClipChunk &c, F factor) {
+    const void *src = b.in[c.tensor];
+    void *dst = b.out[c.tensor];
+    if (b.wide(c.tensor))
+        scaled(reinterpret_cast<const float *>(src) + c.first, reinterpret_cast<float *>(dst) + c.first, c.count, factor);
+    else
+        scaled(reinterpret_cast<const bf16 *>(src) + c.first, reinterpret_cast<bf16 *>(dst) + c.first, c.count, factor);
 }
 
 __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipBatch b, int64_t chunk, const double *part, int parts,
@@ -103,15 +115,11 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipBatch b, i
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
     if (!scale) return;
     const ClipChunk c = clip_chunk(b, chunk, gridDim.x - 1 - blockIdx.x);
-    const void *src = b.in[c.tensor];
-    void *dst = b.out[c.tensor];
     const bool clips = total > max_norm && (float)total <= 3.40282347e38f;
-    if (!clips && src == dst) return;
-    const float factor = clips ? (float)(max_norm / total) : 1.f;
-    if (b.wide(c.tensor))
-        scaled(reinterpret_cast<const float *>(src) + c.first, reinterpret_cast<float *>(dst) + c.first, c.count, factor);
-    else
-        scaled(reinterpret_cast<const bf16 *>(src) + c.first, reinterpret_cast<bf16 *>(dst) + c.first, c.count, factor);
+    if (!clips && b.in[c.tensor] == b.out[c.tensor]) return;
+    const double factor = clips ? max_norm / total : 1.;
+    if (factor < 0x1p-126) scaled(b, c, factor);
+    else scaled(b, c, (float)factor);
 }
 
 // Elements of a chunk: about 2048 chunks in all, 4096 elements at least.
