@@ -26,6 +26,10 @@ constexpr int kRnFwdBlocks = 1024, kRnBwdBlocks = 512;   // workgroups at most
 template <int WPR> constexpr int rn_threads() { return WPR == 8 ? 512 : 256; }
 // Whether registers hold the next row beside the backward's current one
 template <typename T, int V, int K> constexpr bool rn_ahead() { return K * V * (int)sizeof(T) / 4 <= 8; }
+// Whether the backward's parameters are set to 1 where another thread counts, or its sums over a row leave
+// those values out: 8 waves of bfloat16 have no registers left (4000 x 7001 290 us, 224 with the sums; 1
+// wave, 20000 x 777, 77 and 82, 4 waves, 8000 x 3001, 155 and 165; float32 by 8, 3000 x 8001, 401 and 443)
+template <typename T, int WPR> constexpr bool rn_own() { return sizeof(T) == 4 || WPR < 8; }
 template <int WPR> constexpr int rn_rows() { return WPR == 1 ? 4 : 1; }       // rows a workgroup holds at a time
 
 // Where a thread's k-th access of V values to a row of D begins.  ANY: rows may start anywhere and end
@@ -94,14 +98,51 @@ __device__ __forceinline__ const T *row_at(const void *p, int64_t row, int64_t s
     return p ? reinterpret_cast<const T *>(p) + row * stride : nullptr;
 }
 
-template <int V, int K, int WPR, bool ANY>
+// A parameter's values, 1 where it is not given.  WHOLE: in whole accesses also off 16 bytes.
+template <int V, int K, int WPR, bool ANY, bool WHOLE>
 __device__ __forceinline__ void load_params(const float *p, int D, int tid, float (&v)[K][V]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const Place<V, WPR, ANY> at(k, tid, D);
+        if constexpr (ANY && WHOLE) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] = p && at.on ? p[at.c + i] : 1.f;
+            for (int i = 0; i < V; ++i) v[k][i] = 1.f;
+            if (p && at.on) __builtin_memcpy(v[k], p + at.c, sizeof(v[k]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = p && at.on ? p[at.c + i] : 1.f;
+        }
     }
+}
+// Of what was loaded, another thread's values to 1: 0 x 1 in the row's sums, not 0 x infinity.  By
+// selects in the forward (4000 x 7001 62 us, 69 in a branch), in a branch that only a row's last
+// thread takes in the backward (20000 x 777 77 us, 87 by selects).
+template <int V, int K, int WPR, bool ANY, bool BRANCH>
+__device__ __forceinline__ void own_params(int D, int tid, float (&v)[K][V]) {
+    if constexpr (ANY) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Place<V, WPR, ANY> at(k, tid, D);
+            if (BRANCH && at.over <= 0) continue;
+            if (BRANCH) asm volatile("");
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = i < at.over ? 1.f : v[k][i];
+        }
+    }
+}
+
+// dot and the products x y of an access, but the first `over`
+template <int V, bool SOME>
+__device__ __forceinline__ float add_own(int over, const float (&x)[V], const float (&y)[V], float dot) {
+    if (!SOME || over == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot = fmaf(x[i], y[i], dot);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i >= over) dot = fmaf(x[i], y[i], dot);
+    }
+    return dot;
 }
 
 template <typename T, int V, int K, int WPR, bool ANY>
@@ -111,9 +152,12 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
     const int tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
     const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? threadIdx.x / 64 : 0), by = (int64_t)gridDim.x * R;
     float post[K][V], scale[K][V], pre[K][V];
-    load_params<V, K, WPR, ANY>(a.post, a.D, tid, post);
-    load_params<V, K, WPR, ANY>(a.scale, a.D, tid, scale);
-    load_params<V, K, WPR, ANY>(a.pre, a.D, tid, pre);
+    load_params<V, K, WPR, ANY, true>(a.post, a.D, tid, post);
+    load_params<V, K, WPR, ANY, true>(a.scale, a.D, tid, scale);
+    load_params<V, K, WPR, ANY, true>(a.pre, a.D, tid, pre);
+    own_params<V, K, WPR, ANY, false>(a.D, tid, post);
+    own_params<V, K, WPR, ANY, false>(a.D, tid, scale);
+    own_params<V, K, WPR, ANY, false>(a.D, tid, pre);
     RowRegs<T, V, K, WPR, ANY> bn = {}, zn = {}, rn = {};
     auto fetch = [&](int64_t row) {
         bn.load(row_at<T>(a.branch, row, a.branch_stride), a.D, tid);
@@ -230,12 +274,13 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
     __shared__ float red[16];
     __shared__ float cols[WPR == 1 ? 3 * 64 * V * K : 1];
     constexpr int R = rn_rows<WPR>();
+    constexpr bool OWN = rn_own<T, WPR>();
     const int wave = threadIdx.x / 64, tid = WPR == 1 ? threadIdx.x % 64 : threadIdx.x;
     const int64_t first = (int64_t)blockIdx.x * R + (WPR == 1 ? wave : 0), by = (int64_t)gridDim.x * R;
     float post[K][V], scale[K][V], pre[K][V], sums[3][K][V];
-    load_params<V, K, WPR, ANY>(a.post, a.D, tid, post);
-    load_params<V, K, WPR, ANY>(a.scale, a.D, tid, scale);
-    load_params<V, K, WPR, ANY>(a.pre, a.D, tid, pre);
+    load_params<V, K, WPR, ANY, OWN>(a.post, a.D, tid, post);
+    load_params<V, K, WPR, ANY, OWN>(a.scale, a.D, tid, scale);
+    load_params<V, K, WPR, ANY, OWN>(a.pre, a.D, tid, pre);
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
@@ -254,6 +299,11 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
         rs_n = a.stats[a.rows + row];
     };
     if (first < a.rows) fetch(first);
+    if constexpr (OWN) {
+        own_params<V, K, WPR, ANY, true>(a.D, tid, post);
+        own_params<V, K, WPR, ANY, true>(a.D, tid, scale);
+        own_params<V, K, WPR, ANY, true>(a.D, tid, pre);
+    }
     for (int64_t row = first; row < a.rows; row += by) {
         RowRegs<T, V, K, WPR, ANY> bq = bn, zq = zn, rq = rn, yq = yn, tq = tn;
         const float rt = rt_n, rs = rs_n;
@@ -279,15 +329,15 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
                 float r[V], dy[V];
                 unpack<T, V>(rq.v[k], r);
                 unpack<T, V>(yq.v[k], dy);
-                const bool on = Place<V, WPR, ANY>(k, tid, a.D).on;
+                const Place<V, WPR, ANY> at(k, tid, a.D);
+                float g[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     s[k][i] = fmaf(that[k][i] * post[k][i], scale[k][i], r[i]) * rs;      // shat
-                    if (on) {
-                        dot = fmaf(dy[i] * pre[k][i], s[k][i], dot);
-                        sums[0][k][i] = fmaf(dy[i], s[k][i], sums[0][k][i]);
-                    }
+                    g[i] = dy[i] * pre[k][i];
+                    if (at.on) sums[0][k][i] = fmaf(dy[i], s[k][i], sums[0][k][i]);
                 }
+                if (at.on) dot = add_own<V, ANY && !OWN>(at.over, g, s[k], dot);
             }
         }
         if (a.dy) {
@@ -312,8 +362,8 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
                     d[k][i] *= scale[k][i];                    // dp
                     sums[2][k][i] = fmaf(d[k][i], that[k][i], sums[2][k][i]);
                     d[k][i] *= post[k][i];
-                    dot = fmaf(d[k][i], that[k][i], dot);
                 }
+                dot = add_own<V, ANY && !OWN>(at.over, d[k], that[k], dot);
             }
         }
         if (a.post) {

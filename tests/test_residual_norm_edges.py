@@ -1,0 +1,57 @@
+"""The norms around a residual at infinite parameters."""
+import pytest
+import torch
+
+from chunked_linear_recurrence_amd import ssd
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DTYPES = [torch.float32, torch.bfloat16]
+INF = float("inf")
+# a whole number of 16 bytes, rows that end inside an access, and rows that registers do not hold
+CHANNELS = [1024, 1025, 1029, 333, 8201]
+
+
+def shared(d, dtype):
+    """The last channel that a row's last access shares with the one before it, if any are."""
+    v = 16 // torch.empty((), dtype=dtype).element_size()
+    return d - 1 - d % v
+
+
+def rand(d, dtype, n, rows=5):
+    gen = torch.Generator().manual_seed(d)
+    return [(torch.randn(rows, d, generator=gen).to(dtype)).to(DEV) for _ in range(n)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", CHANNELS)
+@pytest.mark.parametrize("which", ["post", "scale"])
+def test_an_infinite_parameter_stays_in_its_channel(which, d, dtype):
+    """The sum of squares of the total is infinite and not NaN: the normed row is 0 but for the
+    infinite channel itself."""
+    branch, residual = rand(d, dtype, 2)
+    at = shared(d, dtype)
+    par = torch.ones(d, device=DEV)
+    par[at] = INF
+    post, scale = (par, None) if which == "post" else (None, par)
+    y, total = ssd.residual_norm_fwd(branch, residual, None, post, scale, torch.ones(d, device=DEV))
+    others = [c for c in range(d) if c != at]
+    assert total[:, at].isinf().all() and total[:, others].isfinite().all()
+    assert (y[:, others] == 0).all() and y[:, at].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", CHANNELS)
+def test_an_infinite_weight_in_the_gradient(d, dtype):
+    """Without the second norm: h = dtotal post is infinite in one channel, so is the mean of h that,
+    and so every gradient of the row: infinite by the formula, NaN in the channel alone
+    (infinity - infinity) or infinite there too."""
+    branch, dtotal = rand(d, dtype, 2)
+    at = shared(d, dtype)
+    post = torch.ones(d, device=DEV)
+    post[at] = INF
+    _, _, stats = ssd.residual_norm_fwd(branch, None, None, post, want_stats=True)
+    g = ssd.residual_norm_bwd(None, dtotal, branch, None, None, post, None, None, stats)
+    others = [c for c in range(d) if c != at]
+    assert g.dbranch[:, others].isinf().all()
+    assert g.dpost_weight[others].isfinite().all()
