@@ -93,6 +93,8 @@ struct RowRegs {
     }
 };
 
+__device__ __forceinline__ float gate_f32(float z) { return silu_limit(z, sigmoid_f32(z)); }
+
 template <typename T>
 __device__ __forceinline__ const T *row_at(const void *p, int64_t row, int64_t stride) {
     return p ? reinterpret_cast<const T *>(p) + row * stride : nullptr;
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_fwd_kernel(Re
                 float g[V];
                 unpack<T, V>(z.v[k], g);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[k][i] *= silu_f32(g[i]);
+                for (int i = 0; i < V; ++i) v[k][i] *= gate_f32(g[i]);
             }
             if (Place<V, WPR, ANY>(k, tid, a.D).on)
 #pragma unroll
@@ -230,7 +232,7 @@ struct WideRow {
     __device__ __forceinline__ WideRow(const ResidualNormArgs &args, int64_t row)
         : b(row_at<T>(args.branch, row, args.branch_stride)), z(row_at<T>(args.gate, row, args.gate_stride)),
           r(row_at<T>(args.residual, row, args.residual_stride)), a(args) {}
-    __device__ __forceinline__ float t(int c) const { return z ? to_f32(b[c]) * silu_f32(to_f32(z[c])) : to_f32(b[c]); }
+    __device__ __forceinline__ float t(int c) const { return z ? to_f32(b[c]) * gate_f32(to_f32(z[c])) : to_f32(b[c]); }
     __device__ __forceinline__ float p(float t, float rt, int c) const { return a.post ? t * rt * a.post[c] : t; }
     __device__ __forceinline__ float s(float p, int c) const {
         return fmaf(p, a.scale ? a.scale[c] : 1.f, r ? to_f32(r[c]) : 0.f);
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
                 float z[V];
                 unpack<T, V>(zq.v[k], z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) that[k][i] *= silu_f32(z[i]);
+                for (int i = 0; i < V; ++i) that[k][i] *= gate_f32(z[i]);
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) that[k][i] *= rt;
@@ -384,8 +386,8 @@ __global__ __launch_bounds__(rn_threads<WPR>()) void residual_norm_bwd_kernel(Re
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float sg = sigmoid_f32(z[i]);
-                    dz[i] = d[k][i] * b[i] * sg * fmaf(z[i], 1.f - sg, 1.f);
-                    d[k][i] *= z[i] * sg;
+                    dz[i] = d[k][i] * b[i] * sg * dsilu_limit(z[i], sg);
+                    d[k][i] *= silu_limit(z[i], sg);
                 }
                 store_at<T, V, WPR, ANY>(a.dgate, row, a.D, at, dz);
             }
@@ -476,8 +478,8 @@ __global__ __launch_bounds__(1024) void residual_norm_bwd_wide_kernel(ResidualNo
         if (a.post) d = rt * (d * a.post[c] - that * mean_t);
         if (a.gate) {
             const float z = to_f32(w.z[c]), sg = sigmoid_f32(z);
-            reinterpret_cast<T *>(a.dgate)[row * a.D + c] = from_f32<T>(d * to_f32(w.b[c]) * sg * fmaf(z, 1.f - sg, 1.f));
-            d *= z * sg;
+            reinterpret_cast<T *>(a.dgate)[row * a.D + c] = from_f32<T>(d * to_f32(w.b[c]) * sg * dsilu_limit(z, sg));
+            d *= silu_limit(z, sg);
         }
         reinterpret_cast<T *>(a.dbranch)[row * a.D + c] = from_f32<T>(d);
     }

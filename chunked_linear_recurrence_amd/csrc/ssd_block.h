@@ -133,6 +133,7 @@ hipError_t launch_sel_step(const SelStepArgs &a, hipStream_t s);
 // ---------------------------------------------------------------------------------
 constexpr float kLog2eF = 1.44269504088896340736f;
 constexpr float kLn2F = 0.69314718055994530942f;
+constexpr float kMostF = 3.40282347e38f;     // the largest finite float32
 
 // V consecutive elements as one access (V * sizeof(T) bytes, naturally aligned).
 template <typename T, int V>
@@ -179,6 +180,14 @@ __device__ __forceinline__ float silu_f32(float v) { return v * sigmoid_f32(v); 
 __device__ __forceinline__ float dsilu_f32(float v) {
     const float s = sigmoid_f32(v);
     return s * fmaf(v, 1.f - s, 1.f);
+}
+
+// With s = sigmoid_f32(v), the same two with their limits at the infinities, where 0 and infinity meet
+// in the products above: v s, and the factor 1 + v (1 - s) of the derivative beside s.  Bit for bit as
+// above elsewhere.
+__device__ __forceinline__ float silu_limit(float v, float s) { return __builtin_amdgcn_fmed3f(v, -kMostF, __builtin_inff()) * s; }
+__device__ __forceinline__ float dsilu_limit(float v, float s) {
+    return fmaf(__builtin_amdgcn_fmed3f(v, -kMostF, kMostF), 1.f - s, 1.f);
 }
 
 // log(1 + e^v) and, in *sig, its derivative.  With w = fl(1 + e^v) the logarithm of w misses

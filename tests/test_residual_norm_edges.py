@@ -1,4 +1,4 @@
-"""The norms around a residual at infinite parameters."""
+"""The norms around a residual at infinite parameters and gates."""
 import pytest
 import torch
 
@@ -55,3 +55,29 @@ def test_an_infinite_weight_in_the_gradient(d, dtype):
     others = [c for c in range(d) if c != at]
     assert g.dbranch[:, others].isinf().all()
     assert g.dpost_weight[others].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", CHANNELS + [3])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_an_infinite_gate_in_the_gradient(sign, d, dtype):
+    """silu is v at +infinity with a derivative of 1, and 0 at -infinity with a derivative of 0:
+    dgate = dtotal scale branch, or 0."""
+    branch, residual, gate, dtotal = rand(d, dtype, 4)
+    branch = branch.abs() + 1
+    dtotal = dtotal.abs() + 1
+    at = shared(d, dtype) if d > 8 else 1
+    gate[:, at] = sign * INF
+    scale = torch.full((d,), 0.5, device=DEV)
+    others = [c for c in range(d) if c != at]
+    _, total, stats = ssd.residual_norm_fwd(branch, residual, gate, None, scale, want_stats=True)
+    g = ssd.residual_norm_bwd(None, dtotal, branch, residual, gate, None, scale, None, stats)
+    assert total[:, others].isfinite().all() and g.dbranch[:, others].isfinite().all()
+    if sign > 0:
+        assert (total[:, at] == INF).all() and (g.dbranch[:, at] == INF).all()
+        want = (dtotal[:, at].float() * 0.5 * branch[:, at].float()).to(dtype)
+    else:
+        assert torch.equal(total[:, at], residual[:, at]) and (g.dbranch[:, at] == 0).all()
+        want = torch.zeros_like(g.dgate[:, at])
+        assert g.dscale[at] == 0
+    assert torch.equal(g.dgate[:, at], want) and g.dgate[:, others].isfinite().all()
