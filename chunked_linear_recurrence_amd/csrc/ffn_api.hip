@@ -266,7 +266,7 @@ struct NormLayout {
 NormLayout norm_layout(const ssd_residual_norm_dims_t &d) {
     NormLayout lo;
     lo.mean = align_up((size_t)ssd::residual_norm_bwd_blocks(d.rows) * 3 * (size_t)d.channels * 4);
-    lo.total = lo.mean + align_up(ssd::residual_norm_mean_rows(d.rows, d.channels) * 4);
+    lo.total = lo.mean + align_up(ssd::residual_norm_mean_rows(d.rows, d.channels, d.dtype) * 4);
     return lo;
 }
 

@@ -25,7 +25,7 @@ struct ResidualNormArgs {
 
 bool residual_norm_fits(const ResidualNormArgs &a);
 int64_t residual_norm_bwd_blocks(int64_t rows);
-size_t residual_norm_mean_rows(int64_t rows, int64_t D);
+size_t residual_norm_mean_rows(int64_t rows, int64_t D, int dtype);
 hipError_t launch_residual_norm_fwd(const ResidualNormArgs &a, hipStream_t s);
 hipError_t launch_residual_norm_bwd(const ResidualNormArgs &a, hipStream_t s);
 

@@ -1,4 +1,4 @@
-"""The norms around a residual at infinite parameters and gates."""
+"""The norms around a residual at infinite parameters and gates, and at many narrow rows."""
 import pytest
 import torch
 
@@ -8,6 +8,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 DTYPES = [torch.float32, torch.bfloat16]
 INF = float("inf")
+EPS = 1e-5
 # a whole number of 16 bytes, rows that end inside an access, and rows that registers do not hold
 CHANNELS = [1024, 1025, 1029, 333, 8201]
 
@@ -81,3 +82,40 @@ def test_an_infinite_gate_in_the_gradient(sign, d, dtype):
         want = torch.zeros_like(g.dgate[:, at])
         assert g.dscale[at] == 0
     assert torch.equal(g.dgate[:, at], want) and g.dgate[:, others].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.float32, 4), (torch.float32, 7), (torch.float32, 3), (torch.bfloat16, 3),
+                                     (torch.bfloat16, 8)], ids=str)
+def test_many_narrow_rows(dtype, d):
+    """More rows than a launch has workgroups of 1024 threads.  Float32 sums of a row have at most 7
+    terms: 4e-5 of the largest value as for other rows, and half a step of what is stored; a column's sum
+    is rows / 512 terms in turn, then 512: that many times 2^-24 of the terms' sizes, and 4e-5 of
+    them for the terms themselves."""
+    rows = 4_200_001
+    gen = torch.Generator(device=DEV).manual_seed(d)
+    act = lambda: torch.randn(rows, d, generator=gen, device=DEV).to(dtype)
+    par = lambda: 1 + 0.3 * torch.randn(d, generator=gen, device=DEV)
+    branch, residual, dy, dtotal, post, scale, pre = act(), act(), act(), act(), par(), par(), par()
+    branch.add_(torch.where(branch < 0, -1., 1.).to(dtype))       # no row of a norm near 0, whose inverse is large
+    residual.mul_(0.25)
+    y, total, stats = ssd.residual_norm_fwd(branch, residual, None, post, scale, pre, EPS, want_stats=True)
+    g = ssd.residual_norm_bwd(dy, dtotal, branch, residual, None, post, scale, pre, stats)
+    torch.cuda.synchronize()
+    B, R, P, S, Q = (t.double().requires_grad_(True) for t in (branch, residual, post, scale, pre))
+    rms = lambda v: v / torch.sqrt((v * v).mean(1, keepdim=True) + EPS)
+    tr = R + rms(B) * P * S
+    yr = rms(tr) * Q
+    grads = torch.autograd.grad((yr, tr), (B, R, P, S, Q), (dy.double(), dtotal.double()))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    with torch.no_grad():
+        inv = 1 / torch.sqrt((tr * tr).mean(1, keepdim=True) + EPS)
+        ds = dtotal.double().abs() + 2 * inv * (dy.double() * Q).abs()
+        dt = 2 * ds * (S * P).abs() / torch.sqrt((B * B).mean(1, keepdim=True) + EPS)
+        near = lambda got, ref, size: ((got.double() - ref).abs() <= 4e-5 * size + half * ref.abs()).all()
+        assert near(total, tr, tr.abs().max()) and near(y, yr, yr.abs().max())
+        assert near(g.dresidual, grads[1], ds.max(1, keepdim=True).values) and near(g.dbranch, grads[0], dt.max(1, keepdim=True).values)
+        count = 2.0 ** -24 * (rows / 512 + 512) + 4e-5
+        that = rms(B)
+        for got, ref, terms in ((g.dpost_weight, grads[2], ds * (S * that).abs()), (g.dscale, grads[3], ds * (that * P).abs()),
+                                (g.dpre_weight, grads[4], (dy.double() * rms(tr)).abs())):
+            assert ((got.double() - ref).abs() <= count * terms.sum(0)).all()
