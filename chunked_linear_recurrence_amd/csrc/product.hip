@@ -17,7 +17,8 @@ static Lines lines_of(const ProductArgs &a, bool of_b) {
     const int64_t ks = 128 / elem(a), rows = !of_b ? a.M : a.kind == kGated ? 2 * a.N : a.N;
     const bool contiguous = of_b ? a.b_rows : a.a_rows;
     const int64_t ld = of_b ? a.b.ld : a.a.ld;
-    if (contiguous) return {a.K, rows, ld, ks, true};
+    // one line of k has no stride of its own; lines past K, at which a tile's offsets point, lie past it
+    if (contiguous) return {a.K, rows, a.K == 1 && ld < rows ? rows : ld, ks, true};
     return {rows, a.K, ld, of_b && a.kind == kGated ? a.N + 256 : 256, false};
 }
 
@@ -290,6 +291,8 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     const Lines la = lines_of(a, false), lb = lines_of(a, true);
     a.a.size = la.length;
     a.b.size = lb.length;
+    a.a.ld = la.ld;
+    a.b.ld = lb.ld;
     Plan p = plan_of(a);
     auto at16 = [](const void *q) { return ((uintptr_t)q & 15u) == 0; };
     if (p.dma && ((!p.pack_a && !at16(a.a.p)) || (!p.pack_b && !at16(a.b.p)))) {
@@ -300,9 +303,6 @@ hipError_t launch_product(const ProductArgs &a0, hipStream_t s) {
     hipError_t r = pack(p, la, lb, &a, ws, s);
     if (r != hipSuccess) return r;
     a.part = reinterpret_cast<float *>(ws + p.part);
-    // one line of k has no stride of its own; lines past K lie past it
-    if (la.rows && la.count == 1 && a.a.ld < a.a.size) a.a.ld = a.a.size;
-    if (lb.rows && lb.count == 1 && a.b.ld < a.b.size) a.b.ld = a.b.size;
     if (a.dtype == 1) r = p.dma ? launch_tiles_bf16(a, p.g, s) : launch_tiles_bf16_any(a, p.g, s);
     else r = p.dma ? launch_tiles_f32(a, p.g, s) : launch_tiles_f32_any(a, p.g, s);
     if (r != hipSuccess || p.g.rest == 0) return r;
@@ -363,6 +363,9 @@ hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipS
     aw.a.size = ld.length;
     ax.b.size = lw.length;
     aw.b.size = lx.length;
+    aw.a.ld = ld.ld;
+    ax.b.ld = lw.ld;
+    aw.b.ld = lx.ld;
     Packing job[3];
     int n = 0;
     char *to = reinterpret_cast<char *>(x.part);
@@ -383,10 +386,6 @@ hipError_t launch_product_grads(const ProductArgs &x, const ProductArgs &w, hipS
         const hipError_t r = pack_launch(job, n, e, s);
         if (r != hipSuccess) return r;
     }
-    // one line of k has no stride of its own; lines past K lie past it
-    if (ld.count == 1 && aw.a.ld < aw.a.size) aw.a.ld = aw.a.size;
-    if (lw.count == 1 && ax.b.ld < ax.b.size) ax.b.ld = ax.b.size;
-    if (lx.count == 1 && aw.b.ld < aw.b.size) aw.b.ld = aw.b.size;
     const bool x_first = x.K >= w.K;                            // the longer tiles first
     return x.dtype == 1 ? launch_pair_bf16(ax, p.gx, aw, p.gw, x_first, s) : launch_pair_f32(ax, p.gx, aw, p.gw, x_first, s);
 }

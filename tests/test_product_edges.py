@@ -131,3 +131,25 @@ def test_a_gated_row_stays_in_its_row_backward(dtype):
         dh2, rows = bad_rows(dh)
         clean, got = (ssd.gated_bwd(v, x, w, b, pre).dx for v in (dh, dh2))
         assert torch.equal(got[rows], clean[rows]) and got[m - 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("wide", ["outer", "inner"])
+def test_one_row_by_many_columns(wide, dtype):
+    """The weight's gradient of a single row, whose sums have one term: a line of k so long that a
+    tile's offsets over further lines, which there are none of, pass 32 bits.  Zeros stand for them,
+    whatever the row holds there."""
+    n = 40_000_000
+    # the value that line 54 (bfloat16) or 27 of a tile's first column wraps to
+    at = 54 * n - 2 ** 31 if dtype == torch.bfloat16 else 27 * n - 2 ** 30
+    assert 0 < at < n
+    inner, outer = (8, n) if wide == "outer" else (n, 8)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(1, inner, generator=gen, device=DEV).to(dtype)
+    dy = torch.randn(1, outer, generator=gen, device=DEV).to(dtype)
+    (dy if wide == "outer" else x)[0, at] = INF
+    w = torch.zeros(outer, inner, dtype=dtype, device=DEV)
+    got = ssd.linear_bwd(dy, x, w, need=(False, True, False)).dweight
+    del w
+    want = (dy.float().t() * x.float()).to(dtype)
+    assert torch.equal(got, want)
