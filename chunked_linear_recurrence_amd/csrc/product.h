@@ -137,8 +137,7 @@ __device__ __forceinline__ float normal_cdf(float v) {
     return v != v ? v : (v < 0.f ? c : 1.f - c);
 }
 
-__device__ __forceinline__ float act_f32(float v, int act) {
-    if (act == kActNone) return v;
+__device__ __forceinline__ float act_f32(float v, int act) {     // kActSilu or kActGelu
     const float c = act == kActSilu ? sigmoid_f32(v) : normal_cdf(v);
     return c == 0.f ? 0.f : v * c;                              // 0 at -infinity too
 }
@@ -154,12 +153,8 @@ __device__ __forceinline__ void act_all(float (&v)[V], int act) {
         for (int i = 0; i < V; ++i) v[i] = act_f32(v[i], kActGelu);
     }
 }
-// act(v) and, in *d, its derivative
+// act(v) and, in *d, its derivative; kActSilu or kActGelu
 __device__ __forceinline__ float act_d_f32(float v, int act, float *d) {
-    if (act == kActNone) {
-        *d = 1.f;
-        return v;
-    }
     const bool silu = act == kActSilu;
     const float c = silu ? sigmoid_f32(v) : normal_cdf(v);
     // c'(v): s (1 - s) or the normal density
