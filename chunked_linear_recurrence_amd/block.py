@@ -138,6 +138,11 @@ class _ResidualNorm(torch.autograd.Function):
         return g.dbranch, g.dresidual, g.dgate, g.dpost_weight, g.dscale, g.dpre_weight, None
 
 
+def _differentiated(*tensors):
+    """Whether a backward can follow a call on these tensors (None: not given)."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 def norm(x, weight=None, bias=None, eps=1e-5):
     """ssd.norm_fwd with gradients: x [rows, channels]."""
     return _Norm.apply(x, weight, bias, eps)
@@ -156,18 +161,25 @@ def selective(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state=Non
 
 
 def linear(x, weight, bias=None, residual=None, act=None):
-    """ssd.linear_fwd with gradients: x [rows, inner], weight [outer, inner]."""
+    """ssd.linear_fwd with gradients: x [rows, inner], weight [outer, inner].  What a backward needs is
+    kept where one can follow: gradients are enabled and an input requires them."""
+    if not _differentiated(x, weight, bias, residual):
+        return ssd.linear_fwd(x, weight, bias, residual, act=act)
     return _Linear.apply(x, weight, bias, residual, act)
 
 
 def gated(x, weight, bias=None, act="silu"):
-    """ssd.gated_fwd with gradients: x [rows, inner], weight [2 hidden, inner].  What the backward
-    needs (2 hidden values a row) is kept by every call; ssd.gated_fwd by itself keeps nothing."""
+    """ssd.gated_fwd with gradients: x [rows, inner], weight [2 hidden, inner].  What a backward needs
+    (2 hidden values a row) is kept as by linear."""
+    if not _differentiated(x, weight, bias):
+        return ssd.gated_fwd(x, weight, bias, act=act)
     return _Gated.apply(x, weight, bias, act)
 
 
 def residual_norm(branch, residual=None, gate=None, post_weight=None, scale=None, pre_weight=None, eps=1e-5):
     """ssd.residual_norm_fwd with gradients; (y, total), y None without pre_weight."""
+    if not _differentiated(branch, residual, gate, post_weight, scale, pre_weight):
+        return ssd.residual_norm_fwd(branch, residual, gate, post_weight, scale, pre_weight, eps)
     return _ResidualNorm.apply(branch, residual, gate, post_weight, scale, pre_weight, eps)
 
 
