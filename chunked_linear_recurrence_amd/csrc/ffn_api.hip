@@ -44,12 +44,16 @@ ssd_status_t check_product(const ssd_product_dims_t *d, bool gated) {
 }
 
 ssd_status_t act_of(uint32_t flags, bool gated, int *act) {
-    if (flags & ~(SSD_FLAG_SILU | SSD_FLAG_GELU)) return fail(SSD_ERR_BAD_SHAPE, "unknown flags 0x%x", flags);
-    if (flags == (SSD_FLAG_SILU | SSD_FLAG_GELU)) return fail(SSD_ERR_BAD_SHAPE, "two activations (flags 0x%x)", flags);
-    if (gated && !flags) return fail(SSD_ERR_BAD_SHAPE, "a gated product has an activation (flags 0)");
+    if (flags & ~(SSD_FLAG_SILU | SSD_FLAG_GELU | SSD_FLAG_PRE_F32)) return fail(SSD_ERR_BAD_SHAPE, "unknown flags 0x%x", flags);
+    const uint32_t which = flags & (SSD_FLAG_SILU | SSD_FLAG_GELU);
+    if (which == (SSD_FLAG_SILU | SSD_FLAG_GELU)) return fail(SSD_ERR_BAD_SHAPE, "two activations (flags 0x%x)", flags);
+    if (gated && !which) return fail(SSD_ERR_BAD_SHAPE, "a gated product has an activation (flags 0x%x)", flags);
     *act = flags & SSD_FLAG_SILU ? ssd::kActSilu : flags & SSD_FLAG_GELU ? ssd::kActGelu : ssd::kActNone;
     return SSD_OK;
 }
+
+// Bytes of an element of pre
+size_t pre_bytes(int32_t dtype, uint32_t flags) { return flags & SSD_FLAG_PRE_F32 ? 4 : (size_t)act_bytes(dtype); }
 
 ssd::ProductArgs product_args(const ssd_product_dims_t &d, bool gated) {
     ssd::ProductArgs a;
@@ -139,14 +143,14 @@ ssd_status_t product_fwd(const char *what, bool gated, const ssd_product_dims_t 
     if (!ssd::product_fits(a)) return beyond(what);
     const size_t need = align_up(ssd::product_workspace_bytes(a));
     TRY(check_workspace(workspace, workspace_bytes, need));
-    const size_t e = (size_t)act_bytes(d.dtype), n = (size_t)d.outer * (gated ? 2 : 1), m = (size_t)d.rows;
+    const size_t e = (size_t)act_bytes(d.dtype), ep = pre_bytes(d.dtype, flags), n = (size_t)d.outer * (gated ? 2 : 1), m = (size_t)d.rows;
     size_t nx, nr = 0;
     if (!span(d.rows, d.x_row_stride, 1, 0, d.inner, (int64_t)e, &nx) ||
         (residual && !span(d.rows, d.residual_row_stride, 1, 0, d.outer, (int64_t)e, &nr)))
         return fail(SSD_ERR_BAD_SHAPE, "strides must be >= 0 and spans below 2^58 elements");
     const Tensor in[] = {{"x", x, nx, e}, {"weight", weight, n * (size_t)d.inner * e, e}, {"bias", bias, n * e, e},
                          {"residual", residual, nr, e}};
-    const Tensor out[] = {{gated ? "h" : "y", y, m * (size_t)d.outer * e, e}, {"pre", pre, m * n * e, e},
+    const Tensor out[] = {{gated ? "h" : "y", y, m * (size_t)d.outer * e, e}, {"pre", pre, m * n * ep, ep},
                           {"workspace", need ? workspace : nullptr, need, 16}};
     TRY(check_tensors(in, 4, out, 3));
     a.a.p = x;
@@ -157,6 +161,7 @@ ssd_status_t product_fwd(const char *what, bool gated, const ssd_product_dims_t 
     a.act = act;
     a.y = y;
     a.pre = pre;
+    a.pre_f32 = ep == 4;
     a.part = static_cast<float *>(workspace);
     return launched(what, ssd::launch_product(a, static_cast<hipStream_t>(stream)));
 }
@@ -175,7 +180,7 @@ ssd_status_t product_bwd(const char *what, bool gated, const ssd_product_dims_t 
     if (!dx && !dweight && !dbias) return fail(SSD_ERR_NULL_ARG, "dx, dweight and dbias are all NULL");
     const GradLayout lo = grad_layout(d, gated, forms);
     TRY(check_workspace(workspace, workspace_bytes, lo.total));
-    const size_t e = (size_t)act_bytes(d.dtype), m = (size_t)d.rows;
+    const size_t e = (size_t)act_bytes(d.dtype), ep = pre_bytes(d.dtype, flags), m = (size_t)d.rows;
     const int64_t cols = gated ? 2 * d.outer : d.outer;
     const size_t n = (size_t)cols, k = (size_t)d.inner;
     size_t nx, ng;
@@ -183,7 +188,7 @@ ssd_status_t product_bwd(const char *what, bool gated, const ssd_product_dims_t 
         !span(d.rows, d.dy_row_stride, 1, 0, d.outer, (int64_t)e, &ng))
         return fail(SSD_ERR_BAD_SHAPE, "strides must be >= 0 and spans below 2^58 elements");
     const Tensor in[] = {{gated ? "dh" : "dy", dy, ng, e}, {"x", x, nx, e}, {"weight", weight, n * k * e, e},
-                         {"pre", pre, m * n * e, e}};
+                         {"pre", pre, m * n * ep, ep}};
     const Tensor out[] = {{"dx", dx, m * k * e, e}, {"dweight", dweight, n * k * e, e}, {"dbias", dbias, n * e, e},
                           {"workspace", workspace, lo.total, 16}};
     TRY(check_tensors(in, 4, out, 4));
@@ -198,6 +203,7 @@ ssd_status_t product_bwd(const char *what, bool gated, const ssd_product_dims_t 
     f.dy = dy;
     f.dy_ld = d.dy_row_stride;
     f.pre = pre;
+    f.pre_f32 = ep == 4;
     f.act = act;
     f.dpre = forms ? ws + lo.dpre : nullptr;
     f.part = dbias ? reinterpret_cast<float *>(ws + lo.sums) : nullptr;

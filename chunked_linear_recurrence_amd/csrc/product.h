@@ -6,11 +6,11 @@
 //     plain    c = A B^T
 //
 // Every sum over k is held in float32 in the matrix units' accumulators; results are rounded
-// once, when they are stored.  pre, which a backward takes, is rounded to the activations' type as
-// they are, and so is the gradient by it before its two products: in bfloat16 three roundings lie
-// between the inputs and a gradient, 0.0030 of relative error in the 2-norm for the gradients of
-// 8192 x 2048 x (2 x 5632) where the last one alone leaves 0.0017.  pre in float32 would leave 0.0024
-// and take 74 us (7%) more there; the matrix units take no float32 gradient at that rate.
+// once, when they are stored.  pre, which a backward takes, is float32 or of the activations' type.
+// The gradient by it is rounded to that type before its two products, whose matrix units take no
+// float32 at the rate of bfloat16.  Errors in the 2-norm of the gradients of 8192 x 2048 x (2 x 5632)
+// against 64 bits, in bfloat16: 0.0024 with pre in float32, 0.0030 in bfloat16 and 0.0017 by the
+// last rounding alone; forward and backward 359 + 721 us and 332 + 686.
 #pragma once
 
 #include "ssd_block.h"
@@ -43,6 +43,7 @@ struct ProductArgs {
     int act;
     void *y;                      // [M, N]
     void *pre;                    // linear [M, N], gated [M, 2 F]; or null
+    bool pre_f32;                 // pre is float32, whatever the activations' type
     float *part;                  // workspace of tiles whose K is split: [rest, splits, bm, bn]
 };
 
@@ -98,6 +99,7 @@ struct ProductActArgs {
     const void *dy;               // [M, N] at dy_ld
     int64_t dy_ld;
     const void *pre;              // linear [M, N] (null without an activation), gated [M, 2 N]
+    bool pre_f32;
     int act;
     void *dpre;                   // like pre
     float *part;                  // workspace [product_act_rows, N or 2 N], null without dbias
@@ -205,9 +207,12 @@ struct Epilogue {
     int64_t residual_ld;
     int act;
     void *y, *pre;
+    bool pre_f32;
 };
 
-inline Epilogue epilogue_of(const ProductArgs &a) { return {a.M, a.N, a.bias, a.residual, a.residual_ld, a.act, a.y, a.pre}; }
+inline Epilogue epilogue_of(const ProductArgs &a) {
+    return {a.M, a.N, a.bias, a.residual, a.residual_ld, a.act, a.y, a.pre, a.pre_f32};
+}
 
 // Columns n .. n + V - 1 of the bias, of its half `of_up` in a gated product, and of the residual's row
 // m; zeros where there are none.  A tile reads those of all its rows before it stores any.
@@ -222,6 +227,12 @@ __device__ __forceinline__ typename Pack<T, V>::type load_residual(const Epilogu
     return load_pack<T, V>(reinterpret_cast<const T *>(p.residual) + m * p.residual_ld + n, left);
 }
 
+template <typename T, int V>
+__device__ __forceinline__ void store_pre(const Epilogue &p, int64_t at, int n, const float (&v)[V]) {
+    if (sizeof(T) == 2 && p.pre_f32) store_some<float, V>(reinterpret_cast<float *>(p.pre) + at, n, v);
+    else store_some<T, V>(reinterpret_cast<T *>(p.pre) + at, n, v);
+}
+
 // v: the product's values at row m, columns n .. n + V - 1; b and r: those of the bias and the residual
 template <typename T, int V>
 __device__ __forceinline__ void finish_linear(const Epilogue &p, int64_t m, int64_t n, const float (&b)[V],
@@ -230,7 +241,7 @@ __device__ __forceinline__ void finish_linear(const Epilogue &p, int64_t m, int6
     if (left <= 0) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] += b[i];
-    if (p.pre) store_some<T, V>(reinterpret_cast<T *>(p.pre) + m * p.N + n, left, v);
+    if (p.pre) store_pre<T, V>(p, m * p.N + n, left, v);
     act_all<V>(v, p.act);
     if (p.residual) {
         float f[V];
@@ -259,9 +270,8 @@ __device__ __forceinline__ void finish_gated(const Epilogue &p, int64_t m, int64
         u[i] += bu[i];
     }
     if (p.pre) {
-        T *pre = reinterpret_cast<T *>(p.pre) + 2 * m * p.N + n;
-        store_some<T, V>(pre, left, g);
-        store_some<T, V>(pre + p.N, left, u);
+        store_pre<T, V>(p, 2 * m * p.N + n, left, g);
+        store_pre<T, V>(p, (2 * m + 1) * p.N + n, left, u);
     }
     act_all<V>(g, p.act);
 #pragma unroll

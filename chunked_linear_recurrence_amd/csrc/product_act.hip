@@ -10,12 +10,12 @@
 // elements per result column; a wave takes 64 x 16 bytes of neighbouring columns and every 4th row of its
 // workgroup's share, with one running sum a column, and a second kernel adds the workgroups'
 // rows of sums in order, so results do not depend on scheduling.  Bound by memory: 8192 x (2 x 5632)
-// in bfloat16 92 us, 5.0 TB/s, and 5 for the sums.
+// in bfloat16 with pre in float32 146 us, 4.4 TB/s, and 5 for the sums (pre in bfloat16: 92, 5.0).
 #include "product.h"
 
 namespace ssd {
 
-template <typename T, bool GATED>
+template <typename T, typename P, bool GATED>
 __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int64_t rows_each) {
     constexpr int V = product_vec<T>(), H = GATED ? 2 : 1;
     __shared__ float red[H][V][64];
@@ -28,7 +28,8 @@ __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int6
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[h][i] = 0.f;
-    const T *dy = reinterpret_cast<const T *>(p.dy) + n, *pre = reinterpret_cast<const T *>(p.pre) + n;
+    const T *dy = reinterpret_cast<const T *>(p.dy) + n;
+    const P *pre = reinterpret_cast<const P *>(p.pre) + n;
     T *dpre = reinterpret_cast<T *>(p.dpre) + n;
     if (left > 0)
 #pragma unroll 2
@@ -37,8 +38,8 @@ __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int6
             load_some<T, V>(dy + m * p.dy_ld, left, d);
             if constexpr (GATED) {
                 float g[V], u[V];
-                load_some<T, V>(pre + m * cols, left, g);
-                load_some<T, V>(pre + m * cols + p.N, left, u);
+                load_some<P, V>(pre + m * cols, left, g);
+                load_some<P, V>(pre + m * cols + p.N, left, u);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float s;
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(256) void product_act_kernel(ProductActArgs p, int6
             } else {
                 if (p.act != kActNone) {
                     float v[V];
-                    load_some<T, V>(pre + m * cols, left, v);
+                    load_some<P, V>(pre + m * cols, left, v);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         float s;
@@ -107,17 +108,19 @@ bool product_act_fits(const ProductActArgs &a) {
     return grid_fits(act_across(a), 256) && grid_fits((a.N * (a.gated ? 2 : 1) + 63) / 64, 1024);
 }
 
-template <typename T>
+// P: pre's type
+template <typename T, typename P>
 static void act_launch(const ProductActArgs &a, dim3 grid, int64_t rows_each, hipStream_t s) {
-    if (a.gated) product_act_kernel<T, true><<<grid, 256, 0, s>>>(a, rows_each);
-    else product_act_kernel<T, false><<<grid, 256, 0, s>>>(a, rows_each);
+    if (a.gated) product_act_kernel<T, P, true><<<grid, 256, 0, s>>>(a, rows_each);
+    else product_act_kernel<T, P, false><<<grid, 256, 0, s>>>(a, rows_each);
 }
 
 hipError_t launch_product_act(const ProductActArgs &a, hipStream_t s) {
     const int64_t blocks = product_act_rows(a.M, a.N, a.dtype), each = (a.M + blocks - 1) / blocks;
     const dim3 grid((uint32_t)act_across(a), (uint32_t)((a.M + each - 1) / each));
-    if (a.dtype == 1) act_launch<bf16>(a, grid, each, s);
-    else act_launch<float>(a, grid, each, s);
+    if (a.dtype == 1 && !a.pre_f32) act_launch<bf16, bf16>(a, grid, each, s);
+    else if (a.dtype == 1) act_launch<bf16, float>(a, grid, each, s);
+    else act_launch<float, float>(a, grid, each, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.dbias) return e;
     const int64_t cols = a.gated ? 2 * a.N : a.N;

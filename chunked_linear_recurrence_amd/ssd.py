@@ -21,6 +21,7 @@ SSD_FLAG_SCAN_FORM = 4
 SSD_FLAG_SILU = 8
 SSD_FLAG_SOFTPLUS = 16
 SSD_FLAG_GELU = 32
+SSD_FLAG_PRE_F32 = 128
 
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL_ARG", 2: "SSD_ERR_BAD_SHAPE", 3: "SSD_ERR_BAD_DTYPE",
           4: "SSD_ERR_UNSUPPORTED", 5: "SSD_ERR_MISALIGNED", 6: "SSD_ERR_WORKSPACE",
@@ -885,16 +886,27 @@ def _product_inputs(x, weight, bias, gated):
     return code, m, k, n // 2 if gated else n, xs, (xp, wp, bp)
 
 
+def _keep(keep, dtype):
+    """The dtype that pre is kept in, or None, and the flag that says so."""
+    if not isinstance(keep, torch.dtype):
+        keep = torch.float32 if keep else None
+    elif keep != torch.float32 and keep != dtype:
+        raise ValueError("keep must be True, False, torch.float32 or %s (got %s)" % (dtype, keep))
+    return keep, SSD_FLAG_PRE_F32 if keep is not None and keep != dtype else 0
+
+
 def linear_fwd(x, weight, bias=None, residual=None, *, act=None, y=None, keep=False, workspace=None, stream=None):
     """Matrix product with bias, activation and residual in its epilogue (ssd_linear_fwd):
         pre = x weight^T + bias;  y = act(pre) + residual
     x [M, K], weight [N, K], bias [N], residual [M, N], all of one dtype; act None, "silu" or
-    "gelu".  Returns y [M, N], or with keep=True (y, pre), where pre is what linear_bwd needs
-    (None without an activation)."""
+    "gelu".  Returns y [M, N], or with keep (y, pre), where pre is what linear_bwd needs (None
+    without an activation): float32 with keep=True, or of a dtype given as keep, x's, at the price
+    of a rounding in every gradient."""
     L_ = lib()
     flag = _act_flag(act)
     code, m, k, n, xs, ptrs = _product_inputs(x, weight, bias, False)
     dev, dtype = x.device, x.dtype
+    kept, wide = _keep(keep, dtype)
     rp, rs, _ = _rows("residual", residual, (m, n), dtype, dev) if residual is not None else (None, 0, 0)
     ctx = _elsewhere(x, stream)
     if ctx is not None:
@@ -904,11 +916,11 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=None, y=None, keep=Fa
     ws = _workspace(workspace, L_.ssd_linear_fwd_workspace_bytes(dims) if m > _FEW_ROWS else 0, dev)
     given = y
     y = x.new_empty((m, n)) if y is None else _out("y", y, (m, n), dtype, dev)
-    pre = x.new_empty((m, n)) if keep and flag else None
-    _check(L_.ssd_linear_fwd(dims, *ptrs, rp, y.data_ptr(), _ptr(pre), flag, ws.data_ptr(), ws.numel(), _current(x)))
+    pre = x.new_empty((m, n), dtype=kept) if kept and flag else None
+    _check(L_.ssd_linear_fwd(dims, *ptrs, rp, y.data_ptr(), _ptr(pre), flag | wide, ws.data_ptr(), ws.numel(), _current(x)))
     if given is not None:
         _wrote(given)
-    return (y, pre) if keep else y
+    return (y, pre) if kept else y
 
 
 class ProductGrads(NamedTuple):
@@ -925,7 +937,12 @@ def _product_bwd(entry, gated, dy, x, weight, bias, pre, act, need, workspace, s
     gp, gs, _ = _rows("dh" if gated else "dy", dy, (m, n), dtype, dev)
     if flag and pre is None:
         raise ValueError("pre (from keep=True) is required")
-    pp = _param("pre", pre, (m, cols), dev, dtype) if flag else None
+    pp = None
+    if flag:
+        wide = pre.dtype == torch.float32
+        pp = _param("pre", pre, (m, cols), dev, torch.float32 if wide else dtype)
+        if wide and dtype != torch.float32:
+            flag |= SSD_FLAG_PRE_F32
     want_x, want_w, want_b = need
     want_b = want_b and bias is not None
     if not (want_x or want_w or want_b):
@@ -946,8 +963,8 @@ def _product_bwd(entry, gated, dy, x, weight, bias, pre, act, need, workspace, s
 
 
 def linear_bwd(dy, x, weight, bias=None, pre=None, *, act=None, need=(True, True, True), workspace=None, stream=None):
-    """Gradients of linear_fwd (ssd_linear_bwd) from dy [M, N], with the pre of a
-    linear_fwd(keep=True) on the same arguments where there is an activation.  need: which of
+    """Gradients of linear_fwd (ssd_linear_bwd) from dy [M, N], with the pre of a linear_fwd with
+    keep on the same arguments where there is an activation.  need: which of
     dx, dweight and dbias are wanted (the others are None, as dbias is where the forward had
     no bias); sums may be cut differently for one of dx and dweight than for both, in their last
     bits.  The residual's gradient is dy itself."""
@@ -959,12 +976,13 @@ def gated_fwd(x, weight, bias=None, *, act="silu", h=None, keep=False, workspace
     and their product in one kernel:
         [g | u] = x weight^T + bias;  h = act(g) u
     x [M, K], weight [2 F, K] (the rows of g, then those of u), bias [2 F], all of one dtype;
-    act "silu" or "gelu".  Returns h [M, F], or with keep=True (h, pre), where pre [M, 2 F] is
-    what gated_bwd needs."""
+    act "silu" or "gelu".  Returns h [M, F], or with keep (h, pre), where pre [M, 2 F] is what
+    gated_bwd needs; keep as for linear_fwd."""
     L_ = lib()
     flag = _act_flag(act)
     code, m, k, f, xs, ptrs = _product_inputs(x, weight, bias, True)
     dev, dtype = x.device, x.dtype
+    kept, wide = _keep(keep, dtype)
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
@@ -973,16 +991,16 @@ def gated_fwd(x, weight, bias=None, *, act="silu", h=None, keep=False, workspace
     ws = _workspace(workspace, L_.ssd_gated_fwd_workspace_bytes(dims) if m > _FEW_ROWS else 0, dev)
     given = h
     h = x.new_empty((m, f)) if h is None else _out("h", h, (m, f), dtype, dev)
-    pre = x.new_empty((m, 2 * f)) if keep else None
-    _check(L_.ssd_gated_fwd(dims, *ptrs, h.data_ptr(), _ptr(pre), flag, ws.data_ptr(), ws.numel(), _current(x)))
+    pre = x.new_empty((m, 2 * f), dtype=kept) if kept else None
+    _check(L_.ssd_gated_fwd(dims, *ptrs, h.data_ptr(), _ptr(pre), flag | wide, ws.data_ptr(), ws.numel(), _current(x)))
     if given is not None:
         _wrote(given)
-    return (h, pre) if keep else h
+    return (h, pre) if kept else h
 
 
 def gated_bwd(dh, x, weight, bias, pre, *, act="silu", need=(True, True, True), workspace=None, stream=None):
-    """Gradients of gated_fwd (ssd_gated_bwd) from dh [M, F], with the pre of a
-    gated_fwd(keep=True) on the same arguments; need as for linear_bwd."""
+    """Gradients of gated_fwd (ssd_gated_bwd) from dh [M, F], with the pre of a gated_fwd with keep
+    on the same arguments; need as for linear_bwd."""
     return _product_bwd("ssd_gated_bwd", True, dh, x, weight, bias, pre, act, need, workspace, stream)
 
 

@@ -391,6 +391,9 @@ ssd_status_t ssd_norm_bwd(const ssd_norm_dims_t *dims, const void *dy, const voi
 #define SSD_FLAG_GELU 32u      /* ssd_linear_*, ssd_gated_*: act(v) = v Phi(v), Phi the normal
                                   distribution's function; SSD_FLAG_SILU: v sigmoid(v); neither:
                                   v (linear only); not both                                   */
+#define SSD_FLAG_PRE_F32 128u  /* ssd_linear_*, ssd_gated_*: pre is float32, whatever the activation
+                                  dtype; the same at the forward and its backward.  In bfloat16 this
+                                  takes a rounding out of every gradient                      */
 
 typedef struct ssd_product_dims {
     int64_t rows;      /* M                                                              */
@@ -407,9 +410,9 @@ typedef struct ssd_product_dims {
  *   x         view [rows, inner] (act) at x_row_stride
  *   weight    [outer, inner] (act); bias [outer] (act) or NULL
  *   residual  view [rows, outer] (act) or NULL
- *   y         [rows, outer] (act); pre [rows, outer] (act) or NULL (ssd_linear_bwd needs it
- *             where there is an activation)
- *   flags     0, SSD_FLAG_SILU or SSD_FLAG_GELU
+ *   y         [rows, outer] (act); pre [rows, outer] (act, or float32 by SSD_FLAG_PRE_F32) or
+ *             NULL (ssd_linear_bwd needs it where there is an activation)
+ *   flags     0, SSD_FLAG_SILU or SSD_FLAG_GELU, and SSD_FLAG_PRE_F32
  *   workspace ssd_linear_fwd_workspace_bytes (0 for up to SSD_PRODUCT_FEW_ROWS rows and
  *             wherever none is needed: it may then be NULL) */
 #define SSD_PRODUCT_FEW_ROWS 32
@@ -430,9 +433,9 @@ ssd_status_t ssd_linear_bwd(const ssd_product_dims_t *dims, const void *dy, cons
 /* h = act(g) u,  [g | u] = x weight^T + bias:
  *   x       view [rows, inner] (act) at x_row_stride
  *   weight  [2 outer, inner] (act): the rows of g, then those of u; bias [2 outer] or NULL
- *   h       [rows, outer] (act); pre [rows, 2 outer] (act) or NULL: [g | u], which
- *           ssd_gated_bwd needs
- *   flags   SSD_FLAG_SILU or SSD_FLAG_GELU */
+ *   h       [rows, outer] (act); pre [rows, 2 outer] (act, or float32 by SSD_FLAG_PRE_F32) or
+ *           NULL: [g | u], which ssd_gated_bwd needs
+ *   flags   SSD_FLAG_SILU or SSD_FLAG_GELU, and SSD_FLAG_PRE_F32 */
 size_t ssd_gated_fwd_workspace_bytes(const ssd_product_dims_t *dims);
 ssd_status_t ssd_gated_fwd(const ssd_product_dims_t *dims, const void *x, const void *weight, const void *bias, void *h,
                            void *pre, uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);

@@ -7,6 +7,7 @@ zeros past K.  Results of clean rows have to be the same bits with and without i
 import pytest
 import torch
 
+import ffn_ref as R
 from chunked_linear_recurrence_amd import ssd
 
 pytestmark = pytest.mark.gpu
@@ -153,3 +154,49 @@ def test_one_row_by_many_columns(wide, dtype):
     del w
     want = (dy.float().t() * x.float()).to(dtype)
     assert torch.equal(got, want)
+
+
+def gated_with(m, k, f, dtype, keep, act="silu"):
+    x, w, b, _, _ = make(m, k, 2 * f, dtype, 6)
+    dh = make(m, 1, f, dtype, 7)[4]
+    h, pre = ssd.gated_fwd(x, w, b, act=act, keep=keep)
+    return (x, w, b, dh), (h, pre) + ssd.gated_bwd(dh, x, w, b, pre, act=act)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_have_one_rounding_beside_their_own(act):
+    """bfloat16, in the 2-norm: a gradient's terms are rounded once (the gradient by pre) and so is
+    the result, two independent roundings of the same relative size, so sqrt 2 of what rounding the
+    exact result leaves; with pre rounded too it is sqrt 3 and more.  The bias' gradient sums
+    what is not rounded yet."""
+    m, k, f = 2048, 1024, 1408
+    (x, w, b, dh), got = gated_with(m, k, f, torch.bfloat16, True, act)
+    assert got[1].dtype == torch.float32
+    X, W, B = (t.double().requires_grad_(True) for t in (x, w, b))
+    g, u = (X @ W.t() + B).chunk(2, 1)
+    a = g * torch.sigmoid(g) if act == "silu" else g * torch.special.ndtr(g)
+    ref = torch.autograd.grad(a * u, (X, W, B), dh.double())
+    for name, mine, r, times in zip(("dx", "dweight", "dbias"), got[2:], ref, (1.55, 1.55, 1.05)):
+        alone = (r.bfloat16().double() - r).norm()
+        assert (mine.double() - r).norm() <= times * alone, name
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(3, 200, 72), (130, 200, 264), (150, 131, 35), (700, 1001, 602), (2901, 136, 1424)], ids=str)
+def test_pre_in_either_type(shape, dtype):
+    """float32 by keep=True, or x's own type: what is kept rounded is the same values rounded, and the
+    gradients are off by no more than their roundings (value by value against float64)."""
+    m, k, f = shape
+    runs = [gated_with(m, k, f, dtype, keep) for keep in (True, torch.float32, dtype)]
+    assert [r[1][1].dtype for r in runs] == [torch.float32, torch.float32, dtype]
+    for p, q in zip(runs[0][1], runs[1][1]):
+        assert torch.equal(p, q)
+    assert torch.equal(runs[2][1][0], runs[0][1][0]) and torch.equal(runs[2][1][1], runs[0][1][1].to(dtype))
+    for (x, w, b, dh), got in runs:
+        R.check_gated(dtype, got, x, w, b, "silu", dh)
+    n = 2 * f
+    x, w, b, r, dy = make(m, k, n, dtype, 8)
+    for keep in (True, dtype):
+        y, pre = ssd.linear_fwd(x, w, b, r, act="gelu", keep=keep)
+        assert pre.dtype == (torch.float32 if keep is True else dtype)
+        R.check_linear(dtype, (y, pre) + ssd.linear_bwd(dy, x, w, b, pre, act="gelu"), x, w, b, r, "gelu", dy)
