@@ -50,8 +50,11 @@ constexpr Shape f32_dma[] = {{64, 4, 0.5f, 0.5f, 3.f}, {128, 2, 1.9f, 1.9f, 14.f
 constexpr Shape f32_any[] = {{64, 4, 0.7f, 0.8f, 3.f}, {128, 2, 2.5f, 2.4f, 14.f}};
 constexpr int kPairTiles = 1 << 20;                     // of two products in one launch, well within a grid's range
 
-// A split's partial results (64 KB of a tile of 128, written and read again) have to be fewer than what
-// it reads for them: at least 4 steps of 32 KB.
+// A split's partial results, written and read again, are to be no more than what it reads for them: 128 KB
+// of a tile of 128 and 4 steps of 32 KB (of a tile of 64 a half, of 256 twice of it).  By steps of a
+// split at least, 2, 4 and 8: float32 65 x 1024 x 256 11.8, 10.3 and 11.3 us, 65 x 512 x 128 9.1, 9.1 and
+// 13.4, bfloat16 100 x 4096 x 64 11.5, 11.6 and 10.4.  By splits of a tile, 8, 16 and 32: bfloat16 128 x
+// 16384 x 128 16.9, 15.1 and 18.0, float32 42.1, 27.2 and 24.1; 84 and 309 whole.
 constexpr int kMostSplits = 16, kSplitSteps = 4;        // of a tile; steps of a split at least
 
 // Tiles of a shape for this product; those beyond a whole number for each CU are split.
@@ -82,6 +85,7 @@ static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g
         return t;
     };
     float t = time(g.full, steps);
+    // partial results: a launch, and their stores and the join's reads (12.6 M of them: 12 us in the join)
     if (g.rest) t += time((int64_t)g.rest * g.splits, g.steps) + 4.f + part_floats(g) * 2e-6f;
     return t;
 }
@@ -90,7 +94,8 @@ static float cost_of(const ProductArgs &a, const Shape &sh, const ProductGrid &g
 // large ones read less from LDS and the caches for each product: us in tiles of 64, 128 and 256,
 // bfloat16, 512 x 2048 x 2048 13.5, 23.3, 32.9; 2048 x 2048 x 4096 55.9, 40.0, 49.3; 4096^3 189, 134,
 // 109; float32 512 x 1024 x 1024 16.8, 29.2 (whole tiles of 64: 21.6), 8192 x 64 x 2048 36, 67, 8192 x
-// 256 x 4096 144, 175 (a tile of 128 alone stores for 14 us).
+// 256 x 4096 144, 175 (a tile of 128 alone stores for 14 us, twice its bytes' time: a lane's accesses of 16
+// bytes lie 64 apart from its neighbours').
 static ProductGrid grid_of(const ProductArgs &a, bool dma, float *cost) {
     const Shape *shapes = a.dtype == 1 ? (dma ? bf16_dma : bf16_any) : dma ? f32_dma : f32_any;
     const int n = a.dtype == 1 && dma ? 3 : 2;

@@ -151,19 +151,27 @@ __global__ __launch_bounds__(64 * WAVES) void product_rows_kernel(ProductArgs p,
 }
 
 // Up to 32 rows; up to 48 of a weight of many rows, which workgroups take 32 at a time; up to 64 of a
-// small weight: beyond, tiles share x's reads, which here every workgroup makes for itself.  In
-// bfloat16, here and in tiles: 32 rows of 4096 x 4096 12.8 us and 13.8, 64 rows 21.7 and 13.9; 48
-// rows of 2048 x (2 x 5632) 15.5 and 19.6, 64 rows 19.6 and 19.9; 64 rows of 1536 x 768 8.9 and 11.3.
+// small weight: beyond, tiles share x's reads, which here every workgroup makes for itself.  Kernels
+// among others, weights from memory, us here and in tiles, bfloat16: 2048 x 4096 32 rows 9.1 and 13.8, 33
+// 10.4 and 13.7; 4096 x 4096 32 rows 14.6 and 19.4, 33 16.9 and 19.3, 49 22.4 and 19.6; 2048 x (2 x 5632)
+// 48 rows 16.8 and 25.4, 49 20.6 and 25.3; 4096 x 4160 48 rows 22.5 and 23.4, 64 25.8 and 23.4; 1536 x 768
+// 64 rows 10.2 and 10.0, 1024 x 1024 7.9 and 11.5.  Float32: 2048 x 4096 32 rows 15.3 and 21.5, 1024 x
+// 1024 64 rows 12.5 and 11.4.  The edges are those of bfloat16 and do not look at k: to either side of
+// them the other way is quicker at 33 to 48 rows of up to 4096 (2048 x (2 x 4096) 12.1 and 25.7), at 49
+// to 64 of a short k, and in tiles at 4096 x (2 x 4160) from 32 rows on (25.9 and 23.9) and for
+// 33 rows of a small float32 weight (2048 x (2 x 1024) 28.4 and 18.2).
 bool product_few_rows(const ProductArgs &a) {
     if (a.a_rows || a.b_rows) return false;
     return a.M <= SSD_PRODUCT_FEW_ROWS || (a.M <= 48 && a.N > 4096) ||
            (a.M <= 64 && a.N * a.K <= (INT64_C(1) << 22));
 }
 
-// 16 rows of the weight a workgroup and up to 16 waves for them while that leaves CUs idle, else 32
-// rows, which halves the reads of x, and 4 waves, 8 for 33 to 48 rows: 32 rows of 2048 x (2 x 5632)
-// 16.8 us with 16 and 13.5 with 32, one row 10.6 and 10.4, 48 rows 21.1 with 16, 16.2 with 32 and 4
-// waves, 15.5 with 8.
+// 16 rows of the weight a workgroup and up to 16 waves for them up to 4096 rows, a workgroup for each
+// CU, else 32 rows, which halves the reads of x, and 4 waves, 8 for 33 to 48 rows.  16 and 32 rows a
+// workgroup, bfloat16: 32 rows of 2048 x 4096 9.1 us and 11.1, of 2048 x 4160 14.1 and 11.0, of 2048 x (2 x
+// 4096) 11.8 and 15.1, of 2048 x (2 x 4160) 18.9 and 15.5; one row of 2048 x 4096 6.0 and 8.4, of 4160
+// 8.7 and 8.4; float32, one row of 2048 x 4096 8.8 and 14.3, of 5632 13.4 and 14.2.  4 and 8 waves by 32:
+// 48 rows of 2048 x (2 x 5632) 17.6 and 16.8 (float32 31.9 and 36.0), 32 rows 15.2 and 15.7.
 template <typename T, ProductKind KIND, int MT>
 static hipError_t rows_launch(const ProductArgs &a, hipStream_t s) {
     const Epilogue ep = epilogue_of(a);

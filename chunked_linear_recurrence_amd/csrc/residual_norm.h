@@ -1,4 +1,4 @@
-// Arguments and launch functions of the norms around a residual, and of clipping.
+// Arguments and launch functions of the norms around a residual.
 #pragma once
 
 #include "ssd_rows.h"
