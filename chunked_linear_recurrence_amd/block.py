@@ -20,6 +20,7 @@ import math
 
 import torch
 import torch.nn.functional as F
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import ssd
@@ -139,8 +140,11 @@ class _ResidualNorm(torch.autograd.Function):
 
 
 def _differentiated(*tensors):
-    """Whether a backward can follow a call on these tensors (None: not given)."""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """Whether a backward can follow a call on these tensors (None: not given), or a tangent comes
+    with one, which the functions with gradients refuse."""
+    given = [t for t in tensors if t is not None]
+    return (torch.is_grad_enabled() and any(t.requires_grad for t in given)) or any(
+        forward_ad.unpack_dual(t).tangent is not None for t in given)
 
 
 def norm(x, weight=None, bias=None, eps=1e-5):

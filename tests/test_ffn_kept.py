@@ -54,3 +54,14 @@ def test_nothing_kept_without_gradients(calls):
         assert kept(calls) == [False] * 3 and not any(v.requires_grad for v in out)
     run(z(5, 8), z(6, 8), z(8))
     assert kept(calls) == [False] * 3
+
+
+def test_tangents_are_refused(calls):
+    """Forward mode has no formula here: a call that dropped the tangent would answer with none."""
+    one, w = z(8), z(6, 8)
+    with torch.autograd.forward_ad.dual_level():
+        x = torch.autograd.forward_ad.make_dual(z(5, 8), torch.ones(5, 8))
+        for grad in (True, False):
+            for f in (lambda: block.linear(x, w), lambda: block.gated(x, w), lambda: block.residual_norm(x, pre_weight=one)):
+                with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="jvp"):
+                    f()
