@@ -458,6 +458,7 @@ typedef struct ssd_residual_norm_dims {
 /* The norms after and before a block, rms(v) = v / sqrt(mean(v^2) + eps) over a row:
  *     t = branch gate sigmoid(gate);  p = rms(t) post_weight;  total = residual + scale p;
  *     y = rms(total) pre_weight                     (of total before it is rounded)
+ * (gate sigmoid(gate) and its derivative at infinities are their limits.)
  * branch, residual and gate are views [rows, channels] (act); residual, gate, post_weight,
  * scale and pre_weight (the last three [channels] float32) may be NULL: what they bring drops
  * out (no post_weight: p = t; no pre_weight: y must be NULL).  total and y [rows, channels]
