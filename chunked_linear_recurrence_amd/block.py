@@ -140,9 +140,9 @@ class _ResidualNorm(torch.autograd.Function):
 
 
 def _differentiated(*tensors):
-    """Whether a backward can follow a call on these tensors (None: not given), or a tangent comes
-    with one, which the functions with gradients refuse."""
-    given = [t for t in tensors if t is not None]
+    """Whether a backward can follow a call on these tensors (others are left to the call's own
+    checks), or a tangent comes with one, which the functions with gradients refuse."""
+    given = [t for t in tensors if isinstance(t, torch.Tensor)]
     return (torch.is_grad_enabled() and any(t.requires_grad for t in given)) or any(
         forward_ad.unpack_dual(t).tangent is not None for t in given)
 

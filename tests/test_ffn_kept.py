@@ -65,3 +65,14 @@ def test_tangents_are_refused(calls):
             for f in (lambda: block.linear(x, w), lambda: block.gated(x, w), lambda: block.residual_norm(x, pre_weight=one)):
                 with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="jvp"):
                     f()
+
+
+def test_what_is_no_tensor_is_named(calls):
+    for grad in (True, False):
+        with torch.set_grad_enabled(grad):
+            for f, msg in ((lambda: block.linear([1.0], z(6, 8)), "x must be a torch.Tensor"),
+                           (lambda: block.linear(z(5, 8), [1.0]), "weight must be a torch.Tensor"),
+                           (lambda: block.gated(None, z(6, 8)), "x must be a torch.Tensor"),
+                           (lambda: block.residual_norm(None, pre_weight=z(8)), "branch must be a torch.Tensor")):
+                with pytest.raises(ValueError, match=msg):
+                    f()
